@@ -1,0 +1,647 @@
+// Dense attention in fp32 on the CUDA cores: forward, gradients, and the tree form
+// over a cache.
+//
+// One block holds a tile of 64 query rows and walks the 64-key tiles those rows can
+// see, with the running maximum and sum of the softmax (one pass over the keys):
+//   S = Q K^T, m' = max(m, max S), P = 2^(S - m'), l = l 2^(m - m') + sum P,
+//   O = O 2^(m - m') + P V
+// in base 2 with the scale folded into the exponent.  256 threads form a 16 x 16
+// grid; a thread owns 4 rows x 4 keys of S (rows and keys 16 apart) and the same
+// rows of D/16 columns of O.  The products are register-tiled from shared memory:
+// 64 FMAs per 8 16-byte loads for S.  Bound by the FMA pipe and those loads.
+#include "dense_common.cuh"
+
+namespace msa {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kTile = 64;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct Smem {
+  static constexpr int kPitch = D + 4;  // rows 4 banks apart: 16-byte loads of 8 rows do not collide
+  static constexpr int kTileFloats = kTile * kPitch;
+  static constexpr int kPPitch = kTile + 4;
+  static constexpr int kPFloats = kTile * kPPitch;
+};
+
+// Rows 0..63 of `src` (row r at src + r * stride elements) into an fp32 tile; rows
+// from `valid` on are zero.
+template <typename T, int D>
+__device__ __forceinline__ void load_tile(float* dst, const T* src, long long stride, int valid) {
+  constexpr int vec = 16 / int(sizeof(T)), lanes = D / vec;
+  for (int i = threadIdx.x; i < kTile * lanes; i += kThreads) {
+    const int r = i / lanes, c = (i % lanes) * vec;
+    float x[vec];
+    if (r < valid) {
+      load_vec<T, vec>(src + r * stride + c, x);
+    } else {
+#pragma unroll
+      for (int e = 0; e < vec; ++e) x[e] = 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < vec; e += 4)
+      *reinterpret_cast<float4*>(dst + r * Smem<D>::kPitch + c + e) =
+          make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+  }
+}
+
+// acc[i][j] += A[row ty + 16 i] . B[row tx + 16 j] over D columns.
+template <int D>
+__device__ __forceinline__ void product_nt(const float* A, const float* B, int ty, int tx,
+                                           float (&acc)[4][4]) {
+  constexpr int P = Smem<D>::kPitch;
+#pragma unroll 4
+  for (int d = 0; d < D; d += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * P + d);
+      b[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * P + d);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+      }
+  }
+}
+
+// acc[i][c] += sum_k W[row ty + 16 i][k] * B[k][col], W [64][kPPitch], columns
+// tx * 4 + 64 * (c / 4) + c % 4 (D = 64: 4 columns, 128: 8).
+template <int D>
+__device__ __forceinline__ void product_nn(const float* W, const float* B, int ty, int tx,
+                                           float (&acc)[4][D / 16]) {
+  constexpr int P = Smem<D>::kPitch, PP = Smem<D>::kPPitch;
+#pragma unroll 2
+  for (int k = 0; k < kTile; k += 4) {
+    float4 w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty + 16 * i) * PP + k);
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+#pragma unroll
+      for (int c = 0; c < D / 16; c += 4) {
+        const float4 b = *reinterpret_cast<const float4*>(B + (k + kk) * P + tx * 4 + c * 16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float x = reinterpret_cast<const float*>(&w[i])[kk];
+          acc[i][c] = fmaf(x, b.x, acc[i][c]);
+          acc[i][c + 1] = fmaf(x, b.y, acc[i][c + 1]);
+          acc[i][c + 2] = fmaf(x, b.z, acc[i][c + 2]);
+          acc[i][c + 3] = fmaf(x, b.w, acc[i][c + 3]);
+        }
+      }
+    }
+  }
+}
+
+// acc[i][c] += sum_r W[r][row ty + 16 i] * B[r][col]: product_nn with W transposed.
+template <int D>
+__device__ __forceinline__ void product_tn(const float* W, const float* B, int ty, int tx,
+                                           float (&acc)[4][D / 16]) {
+  constexpr int P = Smem<D>::kPitch, PP = Smem<D>::kPPitch;
+#pragma unroll 4
+  for (int r = 0; r < kTile; ++r) {
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = W[r * PP + ty + 16 * i];
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 4) {
+      const float4 b = *reinterpret_cast<const float4*>(B + r * P + tx * 4 + c * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        acc[i][c] = fmaf(w[i], b.x, acc[i][c]);
+        acc[i][c + 1] = fmaf(w[i], b.y, acc[i][c + 1]);
+        acc[i][c + 2] = fmaf(w[i], b.z, acc[i][c + 2]);
+        acc[i][c + 3] = fmaf(w[i], b.w, acc[i][c + 3]);
+      }
+    }
+  }
+}
+
+__device__ __forceinline__ float max16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(MSA_FULL_MASK, v, o));
+  return v;
+}
+__device__ __forceinline__ float sum16(float v) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) v += __shfl_xor_sync(MSA_FULL_MASK, v, o);
+  return v;
+}
+
+// Running softmax of a thread's 4 rows (each shared by the 16 threads of a row).
+template <int D>
+struct Running {
+  float m[4], l[4], o[4][D / 16];
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+    }
+  }
+  // Scores (already scaled to base 2, -inf where hidden) of one key tile: P into Ps.
+  __device__ __forceinline__ void step(float (&s)[4][4], float* Ps, int ty, int tx) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+      mx = fmaxf(m[i], max16(mx));
+      const float base = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing yet
+      const float keep = exp2f(m[i] - base);
+      m[i] = mx;
+      float sum = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float p = exp2f(s[i][j] - base);
+        sum += p;
+        Ps[(ty + 16 * i) * Smem<D>::kPPitch + tx + 16 * j] = p;
+      }
+      l[i] = l[i] * keep + sum16(sum);
+#pragma unroll
+      for (int c = 0; c < D / 16; ++c) o[i][c] *= keep;
+    }
+  }
+};
+
+template <typename T>
+__device__ __forceinline__ void store4(T* dst, const float* x, float scale) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) dst[e] = from_f32<T>(x[e] * scale);
+}
+
+template <int D>
+constexpr size_t fwd_smem() {
+  return sizeof(float) * (3 * Smem<D>::kTileFloats + Smem<D>::kPFloats);
+}
+
+// ---------------------------------------------------------------------------
+// Forward over whole prompts: block = (query tile half, head)
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
+                      const T* __restrict__ v, T* __restrict__ out, float* __restrict__ lse) {
+  extern __shared__ float sm[];
+  float* Qs = sm;
+  float* Ks = Qs + Smem<D>::kTileFloats;
+  float* Vs = Ks + Smem<D>::kTileFloats;
+  float* Ps = Vs + Smem<D>::kTileFloats;
+  const int h = blockIdx.x % P.Hq, t2 = blockIdx.x / P.Hq;
+  int qt;
+  const SeqRec s = query_tile(P, t2 >> 1, &qt);
+  const int i0 = qt * kDenseTile + (1 - (t2 & 1)) * kTile;  // first row of the tile
+  if (i0 >= s.nq) return;
+  const int rows = min(kTile, s.nq - i0), g = h / P.G;
+  const int b = P.seqs ? 0 : s.q0 / P.Sq;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  load_tile<T, D>(Qs, q + ((long long)(s.q0 + i0) * P.Hq + h) * D, (long long)P.Hq * D, rows);
+  Running<D> R;
+  R.clear();
+  const float sl2 = P.scale * kLog2e;
+  const int seen = min(s.nk, s.pos0 + i0 + rows);  // keys that the tile's last row sees
+  for (int j0 = 0; j0 < seen; j0 += kTile) {
+    const long long row = tile_row(P, b, s.k0, j0 / kDenseTile) + (j0 % kDenseTile);
+    const int valid = min(kTile, s.nk - j0);
+    __syncthreads();  // the previous tile's P and V are read
+    load_tile<T, D>(Ks, k + (row * P.Hkv + g) * D, (long long)P.Hkv * D, valid);
+    load_tile<T, D>(Vs, v + (row * P.Hkv + g) * D, (long long)P.Hkv * D, valid);
+    __syncthreads();
+    float sc[4][4] = {};
+    product_nt<D>(Qs, Ks, ty, tx, sc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bool sees = j0 + tx + 16 * j <= s.pos0 + i0 + ty + 16 * i;
+        sc[i][j] = sees ? sc[i][j] * sl2 : -INFINITY;
+      }
+    R.step(sc, Ps, ty, tx);
+    __syncthreads();
+    product_nn<D>(Ps, Vs, ty, tx, R.o);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= rows) continue;
+    const long long at = (long long)(s.q0 + i0 + r) * P.Hq + h;
+    const float inv = 1.f / R.l[i];
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 4) store4(out + at * D + tx * 4 + c * 16, &R.o[i][c], inv);
+    if (lse && tx == 0) lse[at] = (R.m[i] + log2f(R.l[i])) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Gradients
+// ---------------------------------------------------------------------------
+// delta[row, head] = sum_d dout out, one warp per (row, head).
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+dense_delta_kernel(const T* __restrict__ dout, const T* __restrict__ out, float* __restrict__ delta,
+                   long long n) {
+  const long long r = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  if (r >= n) return;
+  constexpr int N = D / 32;
+  float a[N], b[N], s = 0.f;
+  load_vec<T, N>(dout + r * D + lane * N, a);
+  load_vec<T, N>(out + r * D + lane * N, b);
+#pragma unroll
+  for (int i = 0; i < N; ++i) s += a[i] * b[i];
+  s = warp_sum_f32(s);
+  if (lane == 0) delta[r] = s;
+}
+
+// P and dS of one 64 x 64 tile into shared memory (rows = queries).
+template <int D>
+__device__ __forceinline__ void tile_grads(const float* Qs, const float* Ks, const float* Vs,
+                                           const float* Gs, float* Ps, float* Ss,
+                                           const float* lse_s, const float* delta_s, float scale,
+                                           int pos, int rows, int j0, int ty, int tx) {
+  float s[4][4] = {}, dp[4][4] = {};
+  product_nt<D>(Qs, Ks, ty, tx, s);
+  product_nt<D>(Gs, Vs, ty, tx, dp);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int c = tx + 16 * j;
+      const bool sees = r < rows && j0 + c <= pos + r;
+      const float p = sees ? exp2f(s[i][j] * (scale * kLog2e) - lse_s[r] * kLog2e) : 0.f;
+      if (Ps) Ps[r * Smem<D>::kPPitch + c] = p;
+      Ss[r * Smem<D>::kPPitch + c] = sees ? p * (dp[i][j] - delta_s[r]) : 0.f;
+    }
+  }
+}
+
+template <int D>
+constexpr size_t bwd_smem() {
+  return sizeof(float) * (4 * Smem<D>::kTileFloats + 2 * Smem<D>::kPFloats + 2 * kTile);
+}
+
+// dk and dv: block = (key tile half, key head); walks the group's heads and the query
+// tiles that see it.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+dense_dkv_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ q,
+                      const T* __restrict__ k, const T* __restrict__ v,
+                      const float* __restrict__ lse, const float* __restrict__ delta,
+                      T* __restrict__ dk, T* __restrict__ dv) {
+  extern __shared__ float sm[];
+  float* Ks = sm;
+  float* Vs = Ks + Smem<D>::kTileFloats;
+  float* Qs = Vs + Smem<D>::kTileFloats;
+  float* Gs = Qs + Smem<D>::kTileFloats;
+  float* Ps = Gs + Smem<D>::kTileFloats;
+  float* Ss = Ps + Smem<D>::kPFloats;
+  float* lse_s = Ss + Smem<D>::kPFloats;
+  float* delta_s = lse_s + kTile;
+  const int g = blockIdx.x % P.Hkv, t2 = blockIdx.x / P.Hkv;
+  int kt;
+  const SeqRec s = key_tile(P, t2 >> 1, &kt);
+  const int j0 = kt * kDenseTile + (t2 & 1) * kTile;
+  if (j0 >= s.nk) return;
+  const int keys = min(kTile, s.nk - j0);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const long long kst = (long long)P.Hkv * D, qst = (long long)P.Hq * D;
+  const long long kat = ((long long)(s.k0 + j0) * P.Hkv + g) * D;
+  load_tile<T, D>(Ks, k + kat, kst, keys);
+  load_tile<T, D>(Vs, v + kat, kst, keys);
+  float ak[4][D / 16] = {}, av[4][D / 16] = {};
+  // the first query row that sees key j0 sits at position j0
+  const int i_first = max(0, j0 - s.pos0) / kTile * kTile;
+  for (int h = g * P.G; h < (g + 1) * P.G; ++h) {
+    for (int i0 = i_first; i0 < s.nq; i0 += kTile) {
+      const int rows = min(kTile, s.nq - i0);
+      const long long at = (long long)(s.q0 + i0) * P.Hq + h;
+      __syncthreads();
+      load_tile<T, D>(Qs, q + at * D, qst, rows);
+      load_tile<T, D>(Gs, dout + at * D, qst, rows);
+      if (threadIdx.x < kTile) {
+        const bool ok = int(threadIdx.x) < rows;
+        lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] : 0.f;
+        delta_s[threadIdx.x] = ok ? delta[at + (long long)threadIdx.x * P.Hq] : 0.f;
+      }
+      __syncthreads();
+      tile_grads<D>(Qs, Ks, Vs, Gs, Ps, Ss, lse_s, delta_s, P.scale, s.pos0 + i0, rows, j0, ty, tx);
+      __syncthreads();
+      product_tn<D>(Ps, Gs, ty, tx, av);
+      product_tn<D>(Ss, Qs, ty, tx, ak);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= keys) continue;
+    const long long at = kat + r * kst + tx * 4;
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 4) {
+      store4(dk + at + c * 16, &ak[i][c], P.scale);
+      store4(dv + at + c * 16, &av[i][c], 1.f);
+    }
+  }
+}
+
+// dq: block = (query tile half, head); walks the keys that its rows see.
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ q,
+                     const T* __restrict__ k, const T* __restrict__ v,
+                     const float* __restrict__ lse, const float* __restrict__ delta,
+                     T* __restrict__ dq) {
+  extern __shared__ float sm[];
+  float* Ks = sm;
+  float* Vs = Ks + Smem<D>::kTileFloats;
+  float* Qs = Vs + Smem<D>::kTileFloats;
+  float* Gs = Qs + Smem<D>::kTileFloats;
+  float* Ss = Gs + Smem<D>::kTileFloats;
+  float* lse_s = Ss + Smem<D>::kPFloats;
+  float* delta_s = lse_s + kTile;
+  const int h = blockIdx.x % P.Hq, t2 = blockIdx.x / P.Hq, g = h / P.G;
+  int qt;
+  const SeqRec s = query_tile(P, t2 >> 1, &qt);
+  const int i0 = qt * kDenseTile + (1 - (t2 & 1)) * kTile;
+  if (i0 >= s.nq) return;
+  const int rows = min(kTile, s.nq - i0);
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  const long long kst = (long long)P.Hkv * D, qst = (long long)P.Hq * D;
+  const long long at = (long long)(s.q0 + i0) * P.Hq + h;
+  load_tile<T, D>(Qs, q + at * D, qst, rows);
+  load_tile<T, D>(Gs, dout + at * D, qst, rows);
+  if (threadIdx.x < kTile) {
+    const bool ok = int(threadIdx.x) < rows;
+    lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] : 0.f;
+    delta_s[threadIdx.x] = ok ? delta[at + (long long)threadIdx.x * P.Hq] : 0.f;
+  }
+  float aq[4][D / 16] = {};
+  const int seen = min(s.nk, s.pos0 + i0 + rows);
+  for (int j0 = 0; j0 < seen; j0 += kTile) {
+    const int keys = min(kTile, s.nk - j0);
+    const long long kat = ((long long)(s.k0 + j0) * P.Hkv + g) * D;
+    __syncthreads();
+    load_tile<T, D>(Ks, k + kat, kst, keys);
+    load_tile<T, D>(Vs, v + kat, kst, keys);
+    __syncthreads();
+    tile_grads<D>(Qs, Ks, Vs, Gs, nullptr, Ss, lse_s, delta_s, P.scale, s.pos0 + i0, rows, j0, ty,
+                  tx);
+    __syncthreads();
+    product_nn<D>(Ss, Ks, ty, tx, aq);
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = ty + 16 * i;
+    if (r >= rows) continue;
+#pragma unroll
+    for (int c = 0; c < D / 16; c += 4)
+      store4(dq + (at + (long long)r * P.Hq) * D + tx * 4 + c * 16, &aq[i][c], P.scale);
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Tree attention over a cache
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
+                 const T* __restrict__ v, T* __restrict__ out, float* __restrict__ lse,
+                 int32_t* __restrict__ status) {
+  extern __shared__ float sm[];
+  __shared__ uint8_t seen_s[kTile];  // a draft's row of this key tile is seen by some node
+  const Dense& P = A.d;
+  float* Qs = sm;
+  float* Ks = Qs + Smem<D>::kTileFloats;
+  float* Vs = Ks + Smem<D>::kTileFloats;
+  float* Ps = Vs + Smem<D>::kTileFloats;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, nodes = P.Sq;
+  const float sl2 = P.scale * kLog2e;
+  if (blockIdx.x == 0)
+    for (int b = threadIdx.x; b < P.B; b += kThreads)
+      if (A.kv_lens[b] < 0 || A.kv_lens[b] > P.Skv - nodes) atomicOr(status, kStatusBadLength);
+  const TreeSpan span = tree_span(A, gridDim.x);
+  TreeWalk w;
+  w.begin(A, blockIdx.x, span);
+  TreeWalk::Piece p;
+  while (w.next(A, &p)) {
+    const uint8_t* mask = A.mask + p.b * A.mask_stride;
+    const int row0 = p.group * A.rows, rows = min(A.rows, nodes * P.G - row0);
+    __syncthreads();
+    for (int i = threadIdx.x; i < kTile * (D / 4); i += kThreads) {
+      const int r = i / (D / 4), c = (i % (D / 4)) * 4, node = (row0 + r) / P.G;
+      float x[4] = {};
+      if (r < rows)
+        load_vec<T, 4>(q + (((long long)p.b * nodes + node) * P.Hq + p.g * P.G +
+                            (row0 + r) % P.G) * D + c, x);
+      *reinterpret_cast<float4*>(Qs + r * Smem<D>::kPitch + c) = make_float4(x[0], x[1], x[2], x[3]);
+    }
+    Running<D> R;
+    R.clear();
+    const int total = p.len + nodes;
+    for (int j0 = p.kt0 * kDenseTile; j0 < min(total, p.kt1 * kDenseTile); j0 += kTile) {
+      const long long row = tile_row(P, p.b, P.table ? 0 : p.b * P.Skv, j0 / kDenseTile) + (j0 % kDenseTile);
+      const int valid = min(kTile, total - j0);
+      const bool drafts = j0 + kTile > p.len;  // the tile reaches the drafted tokens
+      __syncthreads();
+      load_tile<T, D>(Ks, k + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
+      load_tile<T, D>(Vs, v + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
+      if (drafts && threadIdx.x < kTile) {
+        const int j = j0 + int(threadIdx.x) - p.len;
+        bool any = j < 0;
+        for (int i = 0; i < nodes && j >= 0 && j < nodes; ++i) any |= mask[i * nodes + j] != 0;
+        seen_s[threadIdx.x] = any;
+      }
+      __syncthreads();
+      if (drafts) {  // a row that no node sees must not reach the products
+        for (int i = threadIdx.x; i < kTile * D; i += kThreads)
+          if (!seen_s[i / D]) Vs[i / D * Smem<D>::kPitch + i % D] = 0.f;
+      }
+      float sc[4][4] = {};
+      product_nt<D>(Qs, Ks, ty, tx, sc);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int node = min((row0 + ty + 16 * i) / P.G, nodes - 1);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int draft = j0 + tx + 16 * j - p.len;
+          const bool sees = draft < 0 || (draft < nodes && mask[node * nodes + draft] != 0);
+          sc[i][j] = sees ? sc[i][j] * sl2 : -INFINITY;
+        }
+      }
+      R.step(sc, Ps, ty, tx);
+      __syncthreads();
+      product_nn<D>(Ps, Vs, ty, tx, R.o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int r = ty + 16 * i;
+      if (r >= rows) continue;
+      if (p.slot >= 0) {
+        const long long at = (long long)(blockIdx.x * 2 + p.slot) * A.rows + r;
+#pragma unroll
+        for (int c = 0; c < D / 16; c += 4)
+          store4(A.part_o + at * D + tx * 4 + c * 16, &R.o[i][c], 1.f);
+        if (tx == 0) A.part_ml[at] = make_float2(R.m[i], R.l[i]);
+        continue;
+      }
+      const long long at = ((long long)p.b * nodes + (row0 + r) / P.G) * P.Hq + p.g * P.G +
+                           (row0 + r) % P.G;
+      const float inv = R.l[i] == 0.f ? 0.f : 1.f / R.l[i];
+#pragma unroll
+      for (int c = 0; c < D / 16; c += 4) store4(out + at * D + tx * 4 + c * 16, &R.o[i][c], inv);
+      if (lse && tx == 0) lse[at] = R.l[i] == 0.f ? -INFINITY : (R.m[i] + log2f(R.l[i])) * kLn2;
+    }
+  }
+}
+
+}  // namespace
+
+// ---------------------------------------------------------------------------
+// Merge of the partial states of units that a share's border cut: a warp per row.
+// ---------------------------------------------------------------------------
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads)
+tree_combine_kernel(Tree A, int ctas, T* __restrict__ out, float* __restrict__ lse) {
+  const Dense& P = A.d;
+  const int nodes = P.Sq, per = P.Hkv * A.groups;
+  const int chunks = (A.rows + 7) / 8;
+  const int chunk = blockIdx.x % chunks, unit = (blockIdx.x / chunks) % per;
+  const int b = blockIdx.x / chunks / per, lane = threadIdx.x & 31;
+  const TreeSpan span = tree_span(A, ctas);
+  long long before = 0;  // key tiles of the sequences before b
+  for (int i = lane; i < b; i += 32) before += tree_seq(A, i).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(MSA_FULL_MASK, before, o);
+  const int n = tree_seq(A, b).tiles;
+  const long long t0 = before * per + (long long)unit * n;
+  const int c0 = int(t0 / span.share), c1 = int((t0 + n - 1) / span.share);
+  if (c0 == c1) return;
+  const int g = unit / A.groups, row0 = (unit % A.groups) * A.rows;
+  const int r = chunk * 8 + (threadIdx.x >> 5);
+  if (r >= min(A.rows, nodes * P.G - row0)) return;
+  // the unit's first piece lies in c0's slot 1, the others in their CTA's slot 0
+  auto at = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * A.rows + r; };
+  float m = -INFINITY;
+  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, A.part_ml[at(c)].x);
+  m = warp_max_f32(m);
+  const float base = m == -INFINITY ? 0.f : m;
+  constexpr int N = D / 32;
+  float o[N] = {}, l = 0.f;
+#pragma unroll 4
+  for (int c = c0; c <= c1; ++c) {
+    const float2 ml = A.part_ml[at(c)];
+    const float w = exp2f(ml.x - base);
+    float x[N];
+    load_vec<float, N>(A.part_o + at(c) * D + lane * N, x);
+    l += w * ml.y;
+#pragma unroll
+    for (int i = 0; i < N; ++i) o[i] += w * x[i];
+  }
+  const long long row = ((long long)b * nodes + (row0 + r) / P.G) * P.Hq + g * P.G + (row0 + r) % P.G;
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+  for (int i = 0; i < N; ++i) out[row * D + lane * N + i] = from_f32<T>(o[i] * inv);
+  if (lse && lane == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+}
+
+namespace {
+
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes) {
+  return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+}
+
+template <typename T, int D>
+cudaError_t fwd(const Dense& P, const void* q, const void* k, const void* v, void* out, float* lse,
+                cudaStream_t s) {
+  cudaError_t e = allow_smem(dense_fwd_simt_kernel<T, D>, fwd_smem<D>());
+  if (e != cudaSuccess) return e;
+  dense_fwd_simt_kernel<T, D><<<unsigned(P.qtiles) * 2 * P.Hq, kThreads, fwd_smem<D>(), s>>>(
+      P, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+      static_cast<T*>(out), lse);
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t bwd(const Dense& P, const void* dout, const void* q, const void* k, const void* v,
+                const void* out, const float* lse, float* delta, void* dq, void* dk, void* dv,
+                cudaStream_t s) {
+  cudaError_t e = allow_smem(dense_dkv_simt_kernel<T, D>, bwd_smem<D>());
+  if (e == cudaSuccess) e = allow_smem(dense_dq_simt_kernel<T, D>, bwd_smem<D>());
+  if (e != cudaSuccess) return e;
+  const long long n = P.rows_q * P.Hq;
+  const T *g_ = static_cast<const T*>(dout), *q_ = static_cast<const T*>(q);
+  const T *k_ = static_cast<const T*>(k), *v_ = static_cast<const T*>(v);
+  if (n > 0)
+    dense_delta_kernel<T, D><<<unsigned((n + 7) / 8), kThreads, 0, s>>>(
+        g_, static_cast<const T*>(out), delta, n);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (P.qtiles > 0)
+    dense_dq_simt_kernel<T, D><<<unsigned(P.qtiles) * 2 * P.Hq, kThreads, bwd_smem<D>(), s>>>(
+        P, g_, q_, k_, v_, lse, delta, static_cast<T*>(dq));
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  dense_dkv_simt_kernel<T, D><<<unsigned(P.ktiles) * 2 * P.Hkv, kThreads, bwd_smem<D>(), s>>>(
+      P, g_, q_, k_, v_, lse, delta, static_cast<T*>(dk), static_cast<T*>(dv));
+  return cudaGetLastError();
+}
+
+template <typename T, int D>
+cudaError_t tree(const Tree& A, const void* q, const void* k, const void* v, void* out, float* lse,
+                 int32_t* status, cudaStream_t s) {
+  cudaError_t e = allow_smem(tree_simt_kernel<T, D>, fwd_smem<D>());
+  if (e != cudaSuccess) return e;
+  tree_simt_kernel<T, D><<<tree_ctas(), kThreads, fwd_smem<D>(), s>>>(
+      A, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
+      static_cast<T*>(out), lse, status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  return launch_tree_combine(A, out, lse, s);
+}
+
+}  // namespace
+
+cudaError_t launch_tree_combine(const Tree& A, void* out, float* lse, cudaStream_t s) {
+  const long long blocks = (long long)A.d.B * A.d.Hkv * A.groups * ((A.rows + 7) / 8);
+  const int ctas = tree_ctas();
+  if (A.d.f32) {
+    auto kern = A.d.D == 128 ? tree_combine_kernel<float, 128> : tree_combine_kernel<float, 64>;
+    kern<<<unsigned(blocks), kThreads, 0, s>>>(A, ctas, static_cast<float*>(out), lse);
+  } else {
+    auto kern = A.d.D == 128 ? tree_combine_kernel<__nv_bfloat16, 128>
+                             : tree_combine_kernel<__nv_bfloat16, 64>;
+    kern<<<unsigned(blocks), kThreads, 0, s>>>(A, ctas, static_cast<__nv_bfloat16*>(out), lse);
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dense_fwd_simt(const Dense& P, const void* q, const void* k, const void* v,
+                                  void* out, float* lse, cudaStream_t s) {
+  auto fn = P.f32 ? (P.D == 128 ? fwd<float, 128> : fwd<float, 64>)
+                  : (P.D == 128 ? fwd<__nv_bfloat16, 128> : fwd<__nv_bfloat16, 64>);
+  return fn(P, q, k, v, out, lse, s);
+}
+
+cudaError_t launch_dense_bwd_simt(const Dense& P, const void* dout, const void* q, const void* k,
+                                  const void* v, const void* out, const float* lse, float* delta,
+                                  void* dq, void* dk, void* dv, cudaStream_t s) {
+  auto fn = P.f32 ? (P.D == 128 ? bwd<float, 128> : bwd<float, 64>)
+                  : (P.D == 128 ? bwd<__nv_bfloat16, 128> : bwd<__nv_bfloat16, 64>);
+  return fn(P, dout, q, k, v, out, lse, delta, dq, dk, dv, s);
+}
+
+cudaError_t launch_tree_simt(const Tree& A, const void* q, const void* k, const void* v, void* out,
+                             float* lse, int32_t* status, cudaStream_t s) {
+  auto fn = A.d.f32 ? (A.d.D == 128 ? tree<float, 128> : tree<float, 64>)
+                    : (A.d.D == 128 ? tree<__nv_bfloat16, 128> : tree<__nv_bfloat16, 64>);
+  return fn(A, q, k, v, out, lse, status, s);
+}
+
+}  // namespace msa

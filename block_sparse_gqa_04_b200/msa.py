@@ -29,7 +29,10 @@ EXPORTED = ("msa_workspace_size", "msa_select", "msa_attend", "msa_forward",
             "msa_device_status", "msa_set_stage_events", "msa_launch_count", "msa_kernel_path",
             "msa_status_string", "msa_select_static", "msa_index_kl",
             "msa_selftest_wait_timeout", "msa_last_cuda_error", "msa_forward_varlen",
-            "msa_varlen_workspace_size", "msa_varlen_launch_count")
+            "msa_varlen_workspace_size", "msa_varlen_launch_count",
+            "msa_dense_attend", "msa_dense_backward", "msa_dense_workspace_size",
+            "msa_tree_attend", "msa_tree_workspace_size", "msa_qk_norm_rope",
+            "msa_qk_norm_rope_backward", "msa_norm_rope_workspace_size")
 STAGES = ("index", "topk", "lists", "attn", "combine")
 
 
@@ -102,6 +105,23 @@ def load() -> ctypes.CDLL:
         lib.msa_varlen_workspace_size.restype = sz
         lib.msa_varlen_launch_count.argtypes = [pp, cu, cu]
         lib.msa_varlen_launch_count.restype = i32
+        lib.msa_dense_attend.argtypes = [pp, cu, cu, vp, vp, vp, vp, vp, vp, sz, vp]
+        lib.msa_dense_attend.restype = i32
+        lib.msa_dense_backward.argtypes = [pp, cu, cu] + [vp] * 10 + [sz, vp]
+        lib.msa_dense_backward.restype = i32
+        lib.msa_dense_workspace_size.argtypes = [pp, cu, cu, i32]
+        lib.msa_dense_workspace_size.restype = sz
+        lib.msa_tree_attend.argtypes = [pp, vp, vp, vp, vp, ctypes.c_int64, vp, vp, vp, vp, sz, vp]
+        lib.msa_tree_attend.restype = i32
+        lib.msa_tree_workspace_size.argtypes = [pp]
+        lib.msa_tree_workspace_size.restype = sz
+        pn = ctypes.POINTER(NormRope)
+        lib.msa_qk_norm_rope.argtypes = [pn] + [vp] * 9
+        lib.msa_qk_norm_rope.restype = i32
+        lib.msa_qk_norm_rope_backward.argtypes = [pn] + [vp] * 13 + [sz, vp]
+        lib.msa_qk_norm_rope_backward.restype = i32
+        lib.msa_norm_rope_workspace_size.argtypes = [pn]
+        lib.msa_norm_rope_workspace_size.restype = sz
         _lib = lib
     return _lib
 
@@ -666,3 +686,360 @@ def forward_varlen(q, k, v, q_idx, k_idx, cu_seqlens_q, cu_seqlens_k, *, block_s
     if return_q2k:
         res += (q2k,)
     return res[0] if len(res) == 1 else res
+
+
+# ---------------------------------------------------------------------------
+# Dense attention, tree attention and the norm and rotation of heads
+# ---------------------------------------------------------------------------
+def _one_device(first, *ts):
+    """All tensors on the first one's CUDA device."""
+    for t in (first,) + ts:
+        if t is not None and not t.is_cuda:
+            raise ValueError("libmsa takes CUDA tensors")
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and on {t.device}")
+
+
+def _want(name, t, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+
+
+def _main_dtype(t):
+    if t.dtype not in (torch.bfloat16, torch.float32):
+        raise ValueError(f"expected bf16 or fp32 tensors, got {t.dtype}")
+
+
+def _new_ws(nbytes, workspace, dev, where):
+    if nbytes == 0:
+        raise MsaError(1, where)
+    if workspace is None:
+        workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be a uint8 tensor on {dev}")
+    return _ws_view(workspace)
+
+
+def _raise_device_status(wp, dev, where):
+    code = ctypes.c_int32(0)
+    _check(load().msa_device_status(ctypes.c_void_p(wp), ctypes.byref(code), _stream(dev)),
+           f"{where} (device status)")
+
+
+def _dense_setup(q, k, v, cu_q, cu_k, q_pos0, softmax_scale, block_table=None, kv_len=None):
+    """(Problem, cu_q, cu_k as ctypes arrays or None) of a dense call, all checked."""
+    _main_dtype(q)
+    packed = cu_q is not None
+    lead = 1 if packed else 2
+    if q.dim() != lead + 2 or k.dim() != (4 if block_table is not None else lead + 2):
+        raise ValueError("dense attention takes q [B, Sq, Hq, D] with k, v [B, Skv, Hkv, D], or "
+                         "packed q [total_q, Hq, D] with k, v [total_k, Hkv, D]")
+    Hq, D = q.shape[-2:]
+    Hkv = k.shape[-2]
+    if packed:
+        kshape = (k.shape[0], Hkv, D)
+    elif block_table is not None:
+        kshape = (k.shape[0], 128, Hkv, D)
+    else:
+        kshape = (q.shape[0], k.shape[1], Hkv, D)
+    _want("q", q, q.shape, q.dtype)
+    _want("k", k, kshape, q.dtype)
+    _want("v", v, kshape, q.dtype)
+    _one_device(q, k, v, block_table)
+    if packed:
+        p, cq, ck = varlen_problem(cu_q, cu_k, Hq, Hkv, D, 32, dtype=q.dtype,
+                                   softmax_scale=softmax_scale)
+        if cq[len(cq) - 1] != q.shape[0] or ck[len(ck) - 1] != k.shape[0]:
+            raise ValueError(f"the prefix sums end at {cq[len(cq) - 1]} / {ck[len(ck) - 1]}, "
+                             f"the tensors hold {q.shape[0]} / {k.shape[0]} rows")
+        return p, cq, ck
+    pg = _paged(block_table, kv_len, q.shape[0], k.shape[0], 128)
+    p = make_problem(q.shape[0], q.shape[1], int(kv_len) if pg else k.shape[1], Hq, Hkv, D, 32,
+                     dtype=q.dtype, q_pos0=q_pos0, softmax_scale=softmax_scale, **pg)
+    return p, None, None
+
+
+def _dense_forward(where, q, k, v, cu_q, cu_k, q_pos0, softmax_scale, return_lse, workspace, out,
+                   check_device_status, block_table=None, kv_len=None):
+    p, cq, ck = _dense_setup(q, k, v, cu_q, cu_k, q_pos0, softmax_scale, block_table, kv_len)
+    dev = q.device
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _want("out", out, q.shape, q.dtype)
+    _one_device(q, out)
+    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if return_lse else None
+    lib = load()
+    wp, wn = _new_ws(lib.msa_dense_workspace_size(ctypes.byref(p), cq, ck, 0), workspace, dev,
+                     where)
+    with torch.cuda.device(dev):
+        _check(lib.msa_dense_attend(ctypes.byref(p), cq, ck, _ptr(q), _ptr(k), _ptr(v), _ptr(out),
+                                    _ptr(lse), ctypes.c_void_p(wp), wn, _stream(dev)), where)
+        if check_device_status:
+            _raise_device_status(wp, dev, where)
+    return (out, lse) if return_lse else out
+
+
+def dense_attend(q, k, v, *, q_pos0: int = 0, softmax_scale: float = 0.0,
+                 return_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                 out: Optional[torch.Tensor] = None, check_device_status: bool = False,
+                 block_table=None, kv_len=None):
+    """Dense causal attention with grouped heads (msa_dense_attend): q [B, Sq, Hq, D],
+    k, v [B, Skv, Hkv, D], bf16 or fp32; query row i sits at position q_pos0 + i and
+    sees keys 0 .. q_pos0 + i.  Returns out like q (and lse [B, Sq, Hq] fp32, which
+    :func:`dense_backward` needs).  With block_table and kv_len, k and v are paged
+    caches [pages, 128, Hkv, D]."""
+    return _dense_forward("msa_dense_attend", q, k, v, None, None, q_pos0, softmax_scale,
+                          return_lse, workspace, out, check_device_status, block_table, kv_len)
+
+
+def dense_attend_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale: float = 0.0,
+                        return_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                        out: Optional[torch.Tensor] = None, check_device_status: bool = False):
+    """:func:`dense_attend` over a packed batch: q [total_q, Hq, D], k, v [total_k, Hkv,
+    D] and host prefix sums as in :func:`forward_varlen` (a sequence's query rows are
+    its last tokens).  Returns out (and lse [total_q, Hq])."""
+    return _dense_forward("msa_dense_attend", q, k, v, cu_seqlens_q, cu_seqlens_k, 0,
+                          softmax_scale, return_lse, workspace, out, check_device_status)
+
+
+def _dense_grads(dout, q, k, v, out, lse, cu_q, cu_k, q_pos0, softmax_scale, workspace,
+                 check_device_status):
+    where = "msa_dense_backward"
+    p, cq, ck = _dense_setup(q, k, v, cu_q, cu_k, q_pos0, softmax_scale)
+    dev = q.device
+    _want("dout", dout, q.shape, q.dtype)
+    _want("out", out, q.shape, q.dtype)
+    _want("lse", lse, q.shape[:-1], torch.float32)
+    _one_device(q, dout, out, lse)
+    dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+    lib = load()
+    wp, wn = _new_ws(lib.msa_dense_workspace_size(ctypes.byref(p), cq, ck, 1), workspace, dev,
+                     where)
+    with torch.cuda.device(dev):
+        _check(lib.msa_dense_backward(ctypes.byref(p), cq, ck, _ptr(dout), _ptr(q), _ptr(k),
+                                      _ptr(v), _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
+                                      ctypes.c_void_p(wp), wn, _stream(dev)), where)
+        if check_device_status:
+            _raise_device_status(wp, dev, where)
+    return dq, dk, dv
+
+
+def dense_backward(dout, q, k, v, out, lse, *, q_pos0: int = 0, softmax_scale: float = 0.0,
+                   workspace: Optional[torch.Tensor] = None, check_device_status: bool = False):
+    """Gradients of :func:`dense_attend` (msa_dense_backward): dout like out, and the
+    forward call's inputs, out and lse.  Returns (dq, dk, dv) in the inputs' dtype."""
+    return _dense_grads(dout, q, k, v, out, lse, None, None, q_pos0, softmax_scale, workspace,
+                        check_device_status)
+
+
+def dense_backward_varlen(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, *,
+                          softmax_scale: float = 0.0, workspace: Optional[torch.Tensor] = None,
+                          check_device_status: bool = False):
+    """Gradients of :func:`dense_attend_varlen`.  Returns (dq, dk, dv)."""
+    return _dense_grads(dout, q, k, v, out, lse, cu_seqlens_q, cu_seqlens_k, 0, softmax_scale,
+                        workspace, check_device_status)
+
+
+def tree_attend(q, k, v, tree_mask, kv_lens, *, softmax_scale: float = 0.0,
+                return_lse: bool = False, workspace: Optional[torch.Tensor] = None,
+                out: Optional[torch.Tensor] = None, check_device_status: bool = False,
+                block_table=None, kv_len=None):
+    """Dense attention of a tree of drafted tokens over a KV cache (msa_tree_attend).
+
+    q [B, n, Hq, D]: n drafted tokens (1..128) of each sequence; k, v: the cache [B,
+    capacity, Hkv, D], or pages [pages, 128, Hkv, D] with block_table [B, ceil(kv_len /
+    128)] and kv_len, the tokens per sequence that it covers.  kv_lens (CUDA int32 [B])
+    counts the cached tokens of each sequence; its drafted tokens' keys and values are
+    the n rows after them.  tree_mask (CUDA bool [n, n] or [B, n, n]): node i sees
+    drafted token j; every node sees the whole cached text.  A row that sees nothing
+    gets zeros and lse -inf.  With n = 1 and a mask of one True this is a decoding step.
+    Returns out like q (and lse [B, n, Hq])."""
+    where = "msa_tree_attend"
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("tree attention takes q [B, n, Hq, D] and a cache [B, capacity, Hkv, D] "
+                         "or [pages, 128, Hkv, D]")
+    _main_dtype(q)
+    B, n, Hq, D = q.shape
+    Hkv = k.shape[2]
+    kshape = (k.shape[0], 128, Hkv, D) if block_table is not None else (B, k.shape[1], Hkv, D)
+    _want("q", q, q.shape, q.dtype)
+    _want("k", k, kshape, q.dtype)
+    _want("v", v, kshape, q.dtype)
+    _want("kv_lens", kv_lens, (B,), torch.int32)
+    _want("tree_mask", tree_mask, (n, n) if tree_mask.dim() == 2 else (B, n, n), torch.bool)
+    _one_device(q, k, v, kv_lens, tree_mask, block_table, out)
+    pg = _paged(block_table, kv_len, B, k.shape[0], 128)
+    p = make_problem(B, n, int(kv_len) if pg else k.shape[1], Hq, Hkv, D, 32, dtype=q.dtype,
+                     softmax_scale=softmax_scale, **pg)
+    dev = q.device
+    if out is None:
+        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    _want("out", out, q.shape, q.dtype)
+    lse = torch.empty((B, n, Hq), dtype=torch.float32, device=dev) if return_lse else None
+    lib = load()
+    wp, wn = _new_ws(lib.msa_tree_workspace_size(ctypes.byref(p)), workspace, dev, where)
+    with torch.cuda.device(dev):
+        _check(lib.msa_tree_attend(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(tree_mask),
+                                   n * n if tree_mask.dim() == 3 else 0, _ptr(kv_lens), _ptr(out),
+                                   _ptr(lse), ctypes.c_void_p(wp), wn, _stream(dev)), where)
+        if check_device_status:
+            _raise_device_status(wp, dev, where)
+    return (out, lse) if return_lse else out
+
+
+class NormRope(ctypes.Structure):
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("rotary_dim", ctypes.c_int32),
+        ("interleaved", ctypes.c_int32), ("dtype", ctypes.c_int32), ("eps", ctypes.c_float),
+        ("reserved", ctypes.c_int32),
+        ("q_stride", ctypes.c_int64), ("k_stride", ctypes.c_int64),
+        ("q_out_stride", ctypes.c_int64), ("k_out_stride", ctypes.c_int64),
+        ("dq_stride", ctypes.c_int64), ("dk_stride", ctypes.c_int64),
+    ]
+
+
+def _row_stride(name, t, lead, dtype):
+    """Elements between the rows of t [*lead, H, D]: heads contiguous, rows evenly
+    spaced on 16-byte boundaries (t may be a slice of a fused projection's output)."""
+    H, D = t.shape[-2:]
+    if tuple(t.shape[:-2]) != tuple(lead) or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(lead) + (H, D)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+    rows = 1
+    for n in lead:
+        rows *= n
+    if rows == 0:
+        return H * D
+    want, stride = None, H * D
+    for n, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+        if n == 1:
+            continue
+        if want is None:
+            stride, want = st, st * n
+        elif st != want:
+            raise ValueError(f"{name}'s rows are not evenly spaced: strides {t.stride()}")
+        else:
+            want = st * n
+    heads_ok = (H == 1 or t.stride(-2) == D) and t.stride(-1) == 1
+    if not heads_ok or stride < H * D or stride * t.element_size() % 16:
+        raise ValueError(f"{name} needs contiguous heads and rows on 16-byte boundaries: "
+                         f"shape {tuple(t.shape)}, strides {t.stride()}")
+    return stride
+
+
+def _span(t, stride):
+    """First and last byte (exclusive) of t's rows, `stride` elements apart."""
+    row = t.shape[-2] * t.shape[-1]
+    rows = t.numel() // row if row else 0
+    n = (rows - 1) * stride + row if rows else 0
+    return t.data_ptr(), t.data_ptr() + n * t.element_size()
+
+
+def _check_overlap(name, dst, stride, *others):
+    """dst may be one of the others (in place) or share no memory with them; rows of
+    one buffer that interleave without touching count as sharing none.  others:
+    (tensor, its row stride)."""
+    a0, a1 = _span(dst, stride)
+    esz = dst.element_size()
+    for o, ostride in others:
+        b0, b1 = _span(o, ostride)
+        if (a0 == b0 and stride == ostride and dst.shape == o.shape) or a1 <= b0 or b1 <= a0:
+            continue
+        row, off = stride * esz, (b0 - a0) % (stride * esz)
+        la, lb = (t.shape[-2] * t.shape[-1] * esz for t in (dst, o))
+        if stride != ostride or la > off or off + lb > row:
+            raise ValueError(f"{name} overlaps another tensor of the call")
+
+
+def _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
+    _main_dtype(q)
+    lead, (Hq, D) = q.shape[:-2], q.shape[-2:]
+    if q.dim() < 3 or (k is not None and (k.dim() != q.dim() or k.shape[-1] != D)):
+        raise ValueError("q and k are [.., heads, D] with the same leading sizes and D")
+    if (k is None) != (k_weight is None):
+        raise ValueError("k and k_weight come together")
+    _one_device(q, k, q_weight, k_weight, inv_freq, positions)
+    _want("q_weight", q_weight, (D,), q.dtype)
+    if k is not None:
+        _want("k_weight", k_weight, (D,), q.dtype)
+    if inv_freq.dim() != 1:
+        raise ValueError("inv_freq must be a vector")
+    _want("inv_freq", inv_freq, inv_freq.shape, torch.float64)
+    _want("positions", positions, lead, torch.int64)
+    rows = positions.numel()
+    return NormRope(rows, Hq, k.shape[-2] if k is not None else 0, D, 2 * inv_freq.numel(),
+                    int(interleaved), MSA_F32 if q.dtype == torch.float32 else MSA_BF16, eps, 0,
+                    _row_stride("q", q, lead, q.dtype),
+                    _row_stride("k", k, lead, q.dtype) if k is not None else 0, 0, 0, 0, 0)
+
+
+def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps: float = 1e-6,
+                 interleaved: bool = False, out=None):
+    """RMS norm of every query and key head and the position rotation, in one pass
+    (msa_qk_norm_rope).  q [.., Hq, D], k [.., Hkv, D] (bf16 or fp32, D 32, 64 or 128;
+    slices of a fused projection's output are taken as they are; k and k_weight may be
+    None), q_weight, k_weight [D] of the same dtype, inv_freq fp64 [rotary_dim / 2] with
+    rotary_dim a multiple of 16 up to D, positions int64 [..].  Pair i of a head is
+    elements (i, i + rotary_dim/2), or (2i, 2i + 1) if interleaved.  Serves the index
+    branch's q_idx and k_idx (as [.., 1, D]) too.  Returns (q_out, k_out), new tensors
+    or out=(q_out, k_out), which may be q and k themselves."""
+    p = _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
+    lead = q.shape[:-2]
+    if out is None:
+        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
+               None if k is None else torch.empty(k.shape, dtype=q.dtype, device=q.device))
+    else:
+        qo, ko = out
+        if qo.shape != q.shape or (ko is None) != (k is None) or (
+                k is not None and ko.shape != k.shape):
+            raise ValueError("out must be (q_out, k_out) shaped like q and k")
+        _one_device(q, qo, ko)
+    qo, ko = out
+    p.q_out_stride = _row_stride("q_out", qo, lead, q.dtype)
+    if k is not None:
+        p.k_out_stride = _row_stride("k_out", ko, lead, q.dtype)
+    ins = [(q, p.q_stride)] + ([(k, p.k_stride)] if k is not None else [])
+    _check_overlap("q_out", qo, p.q_out_stride, *ins)
+    if k is not None:
+        _check_overlap("k_out", ko, p.k_out_stride, (qo, p.q_out_stride), *ins)
+    with torch.cuda.device(q.device):
+        _check(load().msa_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_weight),
+                                       _ptr(k_weight), _ptr(inv_freq), _ptr(positions), _ptr(qo),
+                                       _ptr(ko), _stream(q.device)), "msa_qk_norm_rope")
+    return qo, ko
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, *,
+                          eps: float = 1e-6, interleaved: bool = False,
+                          workspace: Optional[torch.Tensor] = None):
+    """Gradients of :func:`qk_norm_rope` from those of its outputs.  Returns (dq, dk,
+    dq_weight, dk_weight): dq and dk contiguous in the inputs' dtype, the weights'
+    gradients fp32 [D] (dk, dk_weight None without k)."""
+    where = "msa_qk_norm_rope_backward"
+    p = _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
+    lead, dev = q.shape[:-2], q.device
+    if dq_out.shape != q.shape or (dk_out is None) != (k is None) or (
+            k is not None and dk_out.shape != k.shape):
+        raise ValueError("dq_out and dk_out must be shaped like q and k")
+    _one_device(q, dq_out, dk_out)
+    p.q_out_stride = _row_stride("dq_out", dq_out, lead, q.dtype)
+    p.dq_stride = q.shape[-2] * q.shape[-1]
+    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
+    dqw = torch.empty(q.shape[-1], dtype=torch.float32, device=dev)
+    dk = dkw = None
+    if k is not None:
+        p.k_out_stride = _row_stride("dk_out", dk_out, lead, q.dtype)
+        p.dk_stride = k.shape[-2] * k.shape[-1]
+        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
+        dkw = torch.empty(k.shape[-1], dtype=torch.float32, device=dev)
+    lib = load()
+    wp, wn = _new_ws(lib.msa_norm_rope_workspace_size(ctypes.byref(p)), workspace, dev, where)
+    with torch.cuda.device(dev):
+        _check(lib.msa_qk_norm_rope_backward(
+            ctypes.byref(p), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight),
+            _ptr(k_weight), _ptr(inv_freq), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dqw),
+            _ptr(dkw), ctypes.c_void_p(wp), wn, _stream(dev)), where)
+    return dq, dk, dqw, dkw

@@ -41,9 +41,10 @@
  *  - Argument errors are returned synchronously, before any launch, and leave
  *    every output untouched.  A failed launch returns MSA_ERR_CUDA.  Problems
  *    found on the device (a q2k entry outside [-1, floor(t/block_size)] given
- *    to msa_attend: bit 1; a block_table page id outside [0, num_pages): bit 4)
- *    are recorded in the workspace status word, read with msa_device_status();
- *    such entries are skipped, such pages read as page 0.
+ *    to msa_attend: bit 1; a block_table page id outside [0, num_pages): bit 4;
+ *    a cached length of msa_tree_attend outside the cache: bit 8) are recorded
+ *    in the workspace status word, read with msa_device_status(); such entries
+ *    are skipped, such pages read as page 0, such lengths clamped.
  *  - q_len == 0 is a valid empty problem: the call returns MSA_OK without
  *    looking at the pointers or launching anything.
  */
@@ -262,13 +263,130 @@ msa_status_t msa_index_kl(const msa_problem_t* p, const void* q, const void* k,
                           float* loss, float* dq_idx, float* dk_idx, void* ws, size_t ws_bytes,
                           void* stream);
 
+/* Dense causal attention over whole prompts: every query head attends over all
+ * the tokens its row can see, the layers (and the index warm-up) in which the
+ * main branch is not sparse.  Tensors, positions and groups as in msa_attend:
+ * row i of a sequence sits at position t = q_pos0 + i and sees keys 0..t,
+ *   s_j = scale * q . k_j,  out = sum_j softmax(s)_j v_j,  lse = ln sum_j e^s_j
+ * Used fields of p: batch, q_len, kv_len, num_q_heads, num_kv_heads, head_dim (64
+ * or 128), dtype, q_pos0, softmax_scale, num_pages and block_table; the others are
+ * ignored, except that qk_dtype must be 0.  num_q_heads is any multiple of
+ * num_kv_heads.
+ * cu_seqlens_q_opt, cu_seqlens_k_opt: both NULL for the batched layout above; both
+ * given for a packed batch with the layout and rules of msa_forward_varlen (host
+ * arrays, read before the call returns; q_len, kv_len and q_pos0 ignored; num_pages
+ * 0; 0 <= n_q <= n_k per sequence).  No sequence reads another's rows: whatever
+ * they hold, infinities and NaN included, does not reach it.  Inside a sequence
+ * hidden tokens are weighted by zero, so their v must be finite.
+ * lse_opt [batch, q_len, num_q_heads] (packed: [total_q, num_q_heads]) or NULL.
+ * Workspace: msa_dense_workspace_size(.., 0) bytes.  bf16 problems run on the tensor
+ * cores and round the unnormalised probabilities to bf16 for the product with v
+ * (sums in fp32); fp32 problems run in fp32 on the CUDA cores. */
+msa_status_t msa_dense_attend(const msa_problem_t* p, const int32_t* cu_seqlens_q_opt,
+                              const int32_t* cu_seqlens_k_opt, const void* q, const void* k,
+                              const void* v, void* out, float* lse_opt, void* ws,
+                              size_t ws_bytes, void* stream);
+
+/* Gradients of msa_dense_attend: given dout, the gradient of the loss with respect
+ * to out, and the forward call's inputs, out and lse, writes
+ *   delta = sum_d dout_d out_d,  P_j = e^(s_j - lse),  dS_j = P_j (dout . v_j - delta)
+ *   dq = scale sum_j dS_j k_j,  dk_j = scale sum dS_j q,  dv_j = sum P_j dout
+ * (dk and dv summed over the rows that see token j and the heads of its group; zero
+ * for tokens that no row sees).  dq like q, dk and dv like k, all of the problem's
+ * dtype and overwritten; sums in fp32 in a fixed order: the same inputs give the same
+ * bits.  dout, out, dq [.., num_q_heads, head_dim].  num_pages must be 0
+ * (MSA_ERR_UNSUPPORTED).  Workspace: msa_dense_workspace_size(.., 1) bytes. */
+msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlens_q_opt,
+                                const int32_t* cu_seqlens_k_opt, const void* dout, const void* q,
+                                const void* k, const void* v, const void* out, const float* lse,
+                                void* dq, void* dk, void* dv, void* ws, size_t ws_bytes,
+                                void* stream);
+
+/* Workspace bytes of msa_dense_attend (backward 0) or msa_dense_backward (1); 0 if
+ * the problem or the lengths are invalid. */
+size_t msa_dense_workspace_size(const msa_problem_t* p, const int32_t* cu_seqlens_q_opt,
+                                const int32_t* cu_seqlens_k_opt, int32_t backward);
+
+/* Dense attention of a tree of drafted tokens over a KV cache; with q_len 1, the
+ * decoding step of a layer whose attention is dense.  p: batch sequences, q_len
+ * drafted tokens (nodes, 1..128) per sequence, kv_len the rows of k and v per
+ * sequence (the cache's capacity; with pages the tokens that block_table's
+ * ceil(kv_len/128) pages cover); other fields as in msa_dense_attend, q_pos0 ignored.
+ * Sequence b holds kv_lens[b] cached tokens (device int32 [batch], read when the
+ * kernel runs); its drafted tokens' keys and values are the rows kv_lens[b] ..
+ * kv_lens[b] + q_len - 1.  Node i sees every cached token and the drafted tokens j
+ * with tree_mask[b * mask_batch_stride + i * q_len + j] != 0 (device bytes; itself
+ * and its ancestors for a tree; mask_batch_stride 0 shares one mask).  A row that
+ * sees nothing gets zeros and -inf.  Rows of k and v that no node of the sequence
+ * sees are never part of a result, whatever they hold; a drafted token that some
+ * nodes see and others do not must hold finite v.
+ * q, out [batch, q_len, num_q_heads, head_dim]; lse_opt [batch, q_len, num_q_heads].
+ * kv_lens[b] outside [0, kv_len - q_len] is clamped and sets status bit 8.
+ * At most 128 heads per group.  Workspace: msa_tree_workspace_size(p) bytes, the
+ * same for all kv_lens, so a captured call can be replayed with other lengths. */
+msa_status_t msa_tree_attend(const msa_problem_t* p, const void* q, const void* k, const void* v,
+                             const uint8_t* tree_mask, int64_t mask_batch_stride,
+                             const int32_t* kv_lens, void* out, float* lse_opt, void* ws,
+                             size_t ws_bytes, void* stream);
+
+/* Workspace bytes of msa_tree_attend (0 if p is invalid). */
+size_t msa_tree_workspace_size(const msa_problem_t* p);
+
+/* Norm and position rotation of query and key heads (of the main or of the index
+ * branch): every head row x of head_dim elements becomes
+ *   y = w * x / sqrt(mean(x^2) + eps)
+ * and its first rotary_dim elements, as pairs (a, b), turn by the row's angles
+ *   (a cos f - b sin f, b cos f + a sin f),   f = positions[row] * inv_freq[pair],
+ * the angles formed and reduced in fp64, everything else in fp32 and rounded once.
+ * Pair i is (i, i + rotary_dim/2), or (2i, 2i + 1) when interleaved is set. */
+typedef struct {
+  int64_t rows;           /* tokens                                               */
+  int32_t num_q_heads;    /* >= 1                                                 */
+  int32_t num_kv_heads;   /* key heads; 0: queries only (every k pointer ignored)  */
+  int32_t head_dim;       /* 32, 64 or 128                                        */
+  int32_t rotary_dim;     /* a multiple of 16, 0 .. head_dim                      */
+  int32_t interleaved;    /* pairs (2i, 2i + 1) instead of (i, i + rotary_dim/2)  */
+  int32_t dtype;          /* MSA_BF16 or MSA_F32, of every tensor but inv_freq,
+                             positions and the weights' gradients                 */
+  float eps;              /* >= 0                                                 */
+  int32_t reserved;       /* 0                                                    */
+  int64_t q_stride, k_stride;         /* elements from one row of q, k to the next  */
+  int64_t q_out_stride, k_out_stride; /* of q_out, k_out (backward: dq_out, dk_out) */
+  int64_t dq_stride, dk_stride;       /* of dq, dk (backward only)                  */
+} msa_norm_rope_t;
+
+/* q [rows, num_q_heads, head_dim] with q_stride elements from row to row (heads
+ * contiguous), k likewise; rows start on 16-byte boundaries.  q_weight, k_weight
+ * [head_dim]; inv_freq fp64 [rotary_dim/2]; positions int64 [rows], any values.
+ * q_out and k_out may be q and k themselves (same pointer and stride); any other
+ * overlap is not allowed. */
+msa_status_t msa_qk_norm_rope(const msa_norm_rope_t* p, const void* q, const void* k,
+                              const void* q_weight, const void* k_weight, const double* inv_freq,
+                              const int64_t* positions, void* q_out, void* k_out, void* stream);
+
+/* Gradients of msa_qk_norm_rope from those of its outputs: with g the gradient
+ * turned back and r = 1 / sqrt(mean(x^2) + eps),
+ *   dw = sum over rows and heads of g r x,   dx = r (w g - r x mean(w g r x)).
+ * dq, dk like q, k (each may be dq_out, dk_out themselves); dq_weight, dk_weight fp32
+ * [head_dim], summed in a fixed order.  Workspace: msa_norm_rope_workspace_size(p). */
+msa_status_t msa_qk_norm_rope_backward(const msa_norm_rope_t* p, const void* dq_out,
+                                       const void* dk_out, const void* q, const void* k,
+                                       const void* q_weight, const void* k_weight,
+                                       const double* inv_freq, const int64_t* positions, void* dq,
+                                       void* dk, float* dq_weight, float* dk_weight, void* ws,
+                                       size_t ws_bytes, void* stream);
+
+/* Workspace bytes of msa_qk_norm_rope_backward (0 if p is invalid). */
+size_t msa_norm_rope_workspace_size(const msa_norm_rope_t* p);
+
 /* Reads the workspace status word written by the last call that used `ws`:
  * waits for `stream`, stores the device code in *code and returns MSA_OK if it
  * is 0, else MSA_ERR_DEVICE.  The code is a bitmask (an OR of every problem the
  * call's kernels met): 1 = a q2k entry outside the row's visible blocks
  * (skipped), 2 = a bounded wait inside a tensor-core kernel gave up (the
  * kernel's output is incomplete), 4 = a block_table page id outside
- * [0, num_pages) (read as page 0).  This call synchronises. */
+ * [0, num_pages) (read as page 0), 8 = a kv_lens entry outside the cache (clamped).
+ * This call synchronises. */
 msa_status_t msa_device_status(const void* ws, int32_t* code, void* stream);
 
 /* Stage timing (a measurement aid, not part of the method).  When `events` is

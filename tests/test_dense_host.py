@@ -1,0 +1,212 @@
+"""Host-side checks of the dense operators' C ABI: struct layout, workspace sizes and the
+refusals, all decided before any launch (no GPU needed; the pointers are never read)."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+import torch
+
+from block_sparse_gqa_04_b200 import msa
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+FAKE = 1 << 20
+OK, INVALID, UNSUPPORTED, WORKSPACE = 0, 1, 2, 3
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from block_sparse_gqa_04_b200 import build
+    build.build()
+    return msa.load()
+
+
+def _ints(xs):
+    return None if xs is None else (ctypes.c_int32 * len(xs))(*xs)
+
+
+def _problem(**kw):
+    a = dict(batch=2, q_len=64, kv_len=256, Hq=8, Hkv=2, D=128, block=32, q_pos0=100)
+    a.update({k: v for k, v in kw.items() if k in a})
+    p = msa.make_problem(a["batch"], a["q_len"], a["kv_len"], a["Hq"], a["Hkv"], a["D"], a["block"],
+                         q_pos0=a["q_pos0"])
+    for k, v in kw.items():
+        if k not in a:
+            setattr(p, k, v)
+    return p
+
+
+def _attend(lib, p, cq=None, ck=None, ptr=FAKE, lse=FAKE, ws=FAKE, ws_bytes=0):
+    return lib.msa_dense_attend(ctypes.byref(p), _ints(cq), _ints(ck), ptr, FAKE, FAKE, FAKE, lse,
+                                ws, ws_bytes, None)
+
+
+def _backward(lib, p, cq=None, ck=None, ptr=FAKE, ws=FAKE, ws_bytes=0):
+    return lib.msa_dense_backward(ctypes.byref(p), _ints(cq), _ints(ck), *[FAKE] * 7, ptr,
+                                  FAKE, ws, ws_bytes, None)
+
+
+def _tree(lib, p, stride=0, mask=FAKE, lens=FAKE, ws=FAKE, ws_bytes=0):
+    return lib.msa_tree_attend(ctypes.byref(p), FAKE, FAKE, FAKE, mask, stride, lens, FAKE, FAKE,
+                               ws, ws_bytes, None)
+
+
+@pytest.mark.parametrize("field,value,code", [
+    ("batch", 0, INVALID), ("q_len", -1, INVALID), ("kv_len", 0, INVALID),
+    ("num_q_heads", 7, INVALID), ("num_kv_heads", 0, INVALID), ("head_dim", 0, INVALID),
+    ("head_dim", 96, UNSUPPORTED), ("head_dim", 32, UNSUPPORTED), ("dtype", 7, INVALID),
+    ("qk_dtype", 2, UNSUPPORTED), ("softmax_scale", -1.0, INVALID),
+    ("softmax_scale", float("inf"), INVALID), ("softmax_scale", float("nan"), INVALID),
+    ("num_pages", -1, INVALID), ("num_pages", 4, INVALID),  # pages without a table
+])
+def test_problems_that_every_operator_refuses(lib, field, value, code):
+    p = _problem()
+    setattr(p, field, value)
+    assert _attend(lib, p) == code
+    assert _backward(lib, p) == code
+    assert _tree(lib, p) == code
+    for back in (0, 1):
+        assert lib.msa_dense_workspace_size(ctypes.byref(p), None, None, back) == 0
+    assert lib.msa_tree_workspace_size(ctypes.byref(p)) == 0
+
+
+def test_positions_behind_the_keys_are_refused(lib):
+    assert _attend(lib, _problem(q_pos0=0, q_len=256)) == WORKSPACE   # valid, no workspace given
+    p = _problem()
+    p.q_pos0 = 193                                                    # 193 + 64 > 256
+    assert _attend(lib, p) == INVALID
+    p.q_pos0 = -1
+    assert _attend(lib, p) == INVALID
+    assert _tree(lib, p) == WORKSPACE                                 # ignores q_pos0
+
+
+@pytest.mark.parametrize("cq,ck,code", [
+    ([0, 3, 9], None, INVALID), (None, [0, 3, 9], INVALID),
+    ([1, 3, 9], [0, 3, 9], INVALID), ([0, 3, 9], [1, 3, 9], INVALID),
+    ([0, 9, 3], [0, 9, 12], INVALID), ([0, 3, 9], [0, 9, 3], INVALID),
+    ([0, 4, 9], [0, 3, 9], INVALID),                                  # more rows than tokens
+    ([0, 3, 9], [0, 3, 9], WORKSPACE),
+])
+def test_prefix_sums(lib, cq, ck, code):
+    assert _attend(lib, _problem(), cq, ck) == code
+    assert _backward(lib, _problem(), cq, ck) == code
+    size = lib.msa_dense_workspace_size(ctypes.byref(_problem()), _ints(cq), _ints(ck), 1)
+    assert (size > 0) == (code == WORKSPACE)
+
+
+def test_pages(lib):
+    p = _problem(num_pages=9)
+    p.block_table = FAKE
+    assert _attend(lib, p) == WORKSPACE
+    assert _backward(lib, p) == UNSUPPORTED       # no gradients of a cache
+    assert _attend(lib, p, [0, 1, 2], [0, 1, 2]) == UNSUPPORTED
+
+
+def test_workspaces_and_pointers(lib):
+    p = _problem()
+    n = lib.msa_dense_workspace_size(ctypes.byref(p), None, None, 0)
+    nb = lib.msa_dense_workspace_size(ctypes.byref(p), None, None, 1)
+    assert 0 < n < nb and nb >= 2 * 64 * 8 * 4    # one delta per row and head
+    assert _attend(lib, p, ws_bytes=n - 1) == WORKSPACE
+    assert _attend(lib, p, ws=FAKE + 16, ws_bytes=n) == INVALID
+    assert _attend(lib, p, ws=None, ws_bytes=n) == INVALID
+    assert _attend(lib, p, ptr=None, ws_bytes=n) == INVALID
+    assert _attend(lib, p, ptr=FAKE + 8, ws_bytes=n) == INVALID
+    assert _attend(lib, p, lse=FAKE + 4, ws_bytes=n) == INVALID
+    assert _backward(lib, p, ptr=None, ws_bytes=nb) == INVALID
+    assert _backward(lib, p, ws_bytes=nb - 1) == WORKSPACE
+    # nothing to do: no pointer is looked at
+    e = _problem(q_len=0)
+    assert _attend(lib, e, ptr=None, ws=None) == OK
+    assert _tree(lib, e, mask=None, ws=None) == OK
+    assert _backward(lib, _problem(), [0, 0, 0], [0, 0, 0], ptr=None, ws=None) == OK
+
+
+def test_tree_arguments(lib):
+    p = _problem()
+    n = lib.msa_tree_workspace_size(ctypes.byref(p))
+    assert n > 0
+    assert _tree(lib, p, ws_bytes=n - 1) == WORKSPACE
+    assert _tree(lib, p, mask=None, ws_bytes=n) == INVALID
+    assert _tree(lib, p, lens=None, ws_bytes=n) == INVALID
+    assert _tree(lib, p, lens=FAKE + 2, ws_bytes=n) == INVALID
+    assert _tree(lib, p, stride=64 * 64 - 1, ws_bytes=n) == INVALID
+    assert _tree(lib, p, stride=-1, ws_bytes=n) == INVALID
+    assert _tree(lib, _problem(q_len=129)) == UNSUPPORTED
+    assert _tree(lib, _problem(q_len=129, kv_len=128)) == INVALID     # more nodes than cache
+    assert _tree(lib, _problem(Hq=258)) == UNSUPPORTED                # 129 heads per group
+
+
+def test_norm_rope_struct_layout_matches_header(tmp_path):
+    src = tmp_path / "layout.c"
+    names = [n for n, _ in msa.NormRope._fields_]
+    src.write_text('#include <stdio.h>\n#include <stddef.h>\n#include "msa.h"\nint main(void){'
+                   'printf("%zu", sizeof(msa_norm_rope_t));'
+                   + "".join(f'printf(" %zu", offsetof(msa_norm_rope_t, {n}));' for n in names)
+                   + "return 0;}\n")
+    exe = tmp_path / "layout"
+    subprocess.run(["gcc", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)],
+                   check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True, check=True).stdout.split()
+    want = [ctypes.sizeof(msa.NormRope)] + [getattr(msa.NormRope, n).offset for n in names]
+    assert [int(x) for x in got] == want
+
+
+def _norm(**kw):
+    a = dict(rows=10, num_q_heads=8, num_kv_heads=2, head_dim=128, rotary_dim=64, interleaved=0,
+             dtype=msa.MSA_BF16, eps=1e-6, reserved=0, q_stride=1536, k_stride=1536,
+             q_out_stride=1024, k_out_stride=256, dq_stride=1024, dk_stride=256)
+    a.update(kw)
+    return msa.NormRope(**a)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), INVALID), (dict(num_q_heads=0), INVALID), (dict(num_kv_heads=-1), INVALID),
+    (dict(head_dim=96), UNSUPPORTED), (dict(rotary_dim=129), INVALID),
+    (dict(rotary_dim=-16), INVALID), (dict(rotary_dim=24), UNSUPPORTED), (dict(dtype=2), INVALID),
+    (dict(eps=-1.0), INVALID), (dict(eps=float("nan")), INVALID), (dict(reserved=1), INVALID),
+    (dict(rows=1 << 31), UNSUPPORTED), (dict(q_stride=1016), INVALID),
+    (dict(q_stride=1028), INVALID), (dict(k_out_stride=128), INVALID),
+])
+def test_norm_rope_refusals(lib, kw, code):
+    p = _norm(**kw)
+    args = [FAKE] * 8
+    assert lib.msa_qk_norm_rope(ctypes.byref(p), *args, None) == code
+    assert lib.msa_qk_norm_rope_backward(ctypes.byref(p), *[FAKE] * 12, FAKE, 0, None) == code
+    assert lib.msa_qk_norm_rope(ctypes.byref(_norm()), None, *args[1:], None) == INVALID
+    assert lib.msa_qk_norm_rope(ctypes.byref(_norm()), *args[:4], FAKE + 4, *args[5:],
+                                None) == INVALID
+    assert lib.msa_qk_norm_rope_backward(ctypes.byref(_norm()), *[FAKE] * 12, FAKE, 0,
+                                         None) == WORKSPACE
+    assert lib.msa_qk_norm_rope(ctypes.byref(_norm(rows=0)), *[None] * 8, None) == OK
+
+
+def test_python_checks_come_before_the_library():
+    q, k = torch.zeros(1, 4, 8, 64), torch.zeros(1, 4, 2, 64)
+    for bad in (lambda: msa.dense_attend(q, k, k),                        # not on a GPU
+                lambda: msa.dense_attend(q[0], k, k),
+                lambda: msa.dense_attend(q.half(), k.half(), k.half()),
+                lambda: msa.dense_attend(q.transpose(1, 2), k, k),
+                lambda: msa.dense_attend(q, k, k[..., :32]),
+                lambda: msa.dense_attend(q, k.bfloat16(), k),
+                lambda: msa.tree_attend(q, k, k, torch.ones(4, 4, dtype=torch.bool),
+                                        torch.zeros(1, dtype=torch.int64)),
+                lambda: msa.tree_attend(q, k, k, torch.ones(4, 3, dtype=torch.bool),
+                                        torch.zeros(1, dtype=torch.int32))):
+        with pytest.raises(ValueError):
+            bad()
+
+
+def test_overlap_and_stride_checks_of_norm_rope():
+    buf = torch.zeros(6, 1536)
+    q, k = buf[:, :1024].unflatten(1, (8, 128)), buf[:, 1024:1280].unflatten(1, (2, 128))
+    assert msa._row_stride("q", q, (6,), torch.float32) == 1536
+    msa._check_overlap("q_out", q, 1536, (q, 1536), (k, 1536))            # in place; side by side
+    with pytest.raises(ValueError):
+        msa._check_overlap("q_out", q[1:], 1536, (q[:-1], 1536))          # a row later
+    with pytest.raises(ValueError):
+        msa._check_overlap("k_out", buf[:, 1000:1256].unflatten(1, (2, 128)), 1536, (q, 1536))
+    with pytest.raises(ValueError):
+        msa._row_stride("q", q.transpose(1, 2), (6,), torch.float32)
+    with pytest.raises(ValueError):
+        msa._row_stride("q", torch.zeros(4, 6, 8, 128)[:, :3], (4, 3), torch.float32)
