@@ -58,6 +58,10 @@ cudaError_t launch_dense_check_table(const Dense& P, int32_t* status, cudaStream
 
 cudaError_t launch_dense_fwd_simt(const Dense& P, const void* q, const void* k, const void* v,
                                   void* out, float* lse, cudaStream_t s);
+// bf16 on the tensor cores; counter: a zeroed word.
+cudaError_t launch_dense_fwd_tc(const Dense& P, const void* q, const void* k, const void* v,
+                                void* out, float* lse, int32_t* counter, int32_t* status,
+                                cudaStream_t s);
 cudaError_t launch_dense_bwd_simt(const Dense& P, const void* dout, const void* q, const void* k,
                                   const void* v, const void* out, const float* lse, float* delta,
                                   void* dq, void* dk, void* dv, cudaStream_t s);

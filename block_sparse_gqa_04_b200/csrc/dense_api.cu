@@ -17,6 +17,8 @@ using msa::Tree;
 namespace {
 
 constexpr size_t kAlign = 256;
+// Status word, then the work counters of the tensor-core kernels; zeroed by each call.
+constexpr size_t kHeadBytes = 4 * sizeof(int32_t);
 constexpr int kMaxSeqs = 1 << 20;
 constexpr int kMaxNodes = 128;
 
@@ -139,7 +141,7 @@ DenseLayout dense_layout(const Dense& P, bool packed, bool backward) {
   DenseLayout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
-  L.status = take(sizeof(int32_t));
+  L.status = take(kHeadBytes);
   if (packed) L.recs = take(size_t(P.B) * sizeof(SeqRec));
   if (backward) L.delta = take(size_t(P.rows_q) * P.Hq * sizeof(float));
   L.total = off;
@@ -165,9 +167,9 @@ struct Records {
   ~Records() { delete[] r; }
 };
 
-// Clears the status word and puts the records in place.
+// Clears the status word and the counters and puts the records in place.
 msa_status_t begin(Dense* P, const Records& R, const DenseLayout& L, void* ws, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int32_t), s);
+  cudaError_t e = cudaMemsetAsync(ws, 0, kHeadBytes, s);
   if (e == cudaSuccess && R.r) {
     P->seqs = at<SeqRec>(ws, L.recs);
     e = msa::launch_put_records(R.r, at<SeqRec>(ws, L.recs), P->B, s);
@@ -256,7 +258,10 @@ msa_status_t msa_dense_attend(const msa_problem_t* p, const int32_t* cu_seqlens_
   if ((st = check_ws(ws, ws_bytes, L.total)) != MSA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = begin(&P, R, L, ws, s)) != MSA_OK) return st;
-  return msa::status_of(msa::launch_dense_fwd_simt(P, q, k, v, out, lse_opt, s));
+  int32_t* head = at<int32_t>(ws, L.status);
+  return msa::status_of(P.f32
+                            ? msa::launch_dense_fwd_simt(P, q, k, v, out, lse_opt, s)
+                            : msa::launch_dense_fwd_tc(P, q, k, v, out, lse_opt, head + 1, head, s));
 }
 
 msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlens_q_opt,

@@ -1,0 +1,557 @@
+// Dense causal attention on tcgen05 tensor cores (bf16, head_dim 64 or 128).
+//
+// A work item is a pair of 128-row query tiles that share a key head: two heads of
+// the group at the same query tile (their keys are loaded once and both tiles see
+// the same number of them), or, where the group has an odd number of heads, two
+// neighbours in the list of (query tile, head).  Persistent CTAs, one per SM, take
+// items from a counter in the workspace, heaviest first.  Per key tile of 128 keys
+// and per query tile, with the running maximum m and sum l of the softmax held by
+// the thread that owns the row:
+//   S = Q K^T          (both K-major in shared memory, fp32 in TMEM, a row per lane)
+//   P = 2^(c S - c m)  (c = scale log2 e; bf16, written over S in TMEM), l += sum P
+//   O += P V           (P from TMEM, V as an MN-major shared-memory operand)
+// m moves only when a row's maximum has grown by more than 2^kSlack: O, kept in
+// TMEM, is then scaled by the softmax warps; otherwise P just exceeds 1, which fp32
+// sums and a bf16 P carry with the same relative error.
+//
+// Each tile of the pair has its own TMEM columns (S|P 128, O), softmax warpgroup
+// and MMA-issuing thread, so one tile's MMAs run while the other is in its softmax.
+// A fourth warpgroup normalises and stores the finished tiles.  K and V tiles pass
+// through a ring of TMA stages; a stage is free again once both issuers have
+// committed past it.
+//
+// Tokens behind the last key of a sequence (the next sequence's, or an unused part
+// of a page) come in with its last tile.  Their scores are cut by the causal mask;
+// their V rows must not meet a weight of zero as infinities or NaN, so P V runs over
+// whole groups of 16 keys only as far as keys exist, and the rest of the last group
+// is zeroed in shared memory first.
+#include <algorithm>
+
+#include "dense_common.cuh"
+#include "tc_warp.cuh"
+
+namespace msa {
+namespace {
+
+// warp 0 items and TMA, warps 1-2 MMA, warp 3 idle, warps 4-11 softmax, 12-15 epilogue
+constexpr int kThreads = 512;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kItems = 2;     // items in flight
+constexpr float kSlack = 8.f;
+// 96 + 64 + 2 x 176 = 512 = 4 x 128: the registers the CTA is launched with
+constexpr int kRegsCtl = 96, kRegsEpi = 64, kRegsSoftmax = 176;
+constexpr float kLn2 = 0.6931471805599453f;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kHalf = 128 * 64 * 2;            // 64 dims of 128 rows
+  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr uint32_t kIdescS = tc::idesc_bf16_f32(128, 128, 0, 0);
+  static constexpr uint32_t kIdescO = tc::idesc_bf16_f32(128, D, 0, 1);  // V is MN-major
+};
+
+struct Item {
+  int live;               // 0: no more items
+  int n;                  // key tiles to pass through (the larger of nkt)
+  int nkt[2];             // key tiles of each query tile; 0: no such tile
+  int rows[2];            // its rows
+  int pos[2];             // position of its first row
+  int head[2];
+  int row0[2];            // its first row in q
+  int nk;                 // keys of the sequence
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t kv_full[8], kv_empty[8];
+  // per query tile: S computed, P written, each P V done, the tile's last P V done,
+  // O read by the epilogue, sums written, sums read
+  uint64_t s_full[2], p_full[2], o_step[2], o_done[2], o_empty[2], l_full[2], l_empty[2];
+  uint64_t i_full[kItems], i_empty[kItems];
+  uint64_t mma_done;
+  Item item[kItems];
+  float l[2][128];        // sums of the rows, softmax -> epilogue
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+constexpr size_t smem_bytes() {
+  return 1024 + size_t(2 + Cfg<D>::kStages) * Cfg<D>::kTileBytes + sizeof(Bars) + 64;
+}
+static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory of a CTA");
+
+__device__ __forceinline__ int tiles_of(int n) { return (n + kDenseTile - 1) / kDenseTile; }
+
+// Item t of the launch; b and k0 locate its keys (b: batch index for a block table).
+__device__ __forceinline__ void make_item(const Dense& P, int t, Item* it, int* b, int* k0, int* g) {
+  SeqRec s;
+  int p;
+  if (P.seqs) {
+    s = P.seqs[find_seq<&SeqRec::pr0>(P.seqs, P.B, t)];
+    p = (t - s.pr0) / P.Hkv;
+    *g = (t - s.pr0) % P.Hkv;
+    *b = 0;
+  } else {
+    p = t / (P.B * P.Hkv);
+    *b = (t / P.Hkv) % P.B;
+    *g = t % P.Hkv;
+    s = batch_seq(P, *b);
+  }
+  *k0 = s.k0;
+  const int nqt = tiles_of(s.nq);
+  it->live = 1;
+  it->nk = s.nk;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int x = 2 * p + e;
+    const bool there = x < nqt * P.G;
+    const int i0 = (nqt - 1 - (there ? x / P.G : 0)) * kDenseTile;  // last tiles first
+    it->rows[e] = there ? min(kDenseTile, s.nq - i0) : 0;
+    it->pos[e] = s.pos0 + i0;
+    it->head[e] = *g * P.G + (there ? x % P.G : 0);
+    it->row0[e] = s.q0 + i0;
+    it->nkt[e] = there ? tiles_of(min(s.nk, s.pos0 + i0 + it->rows[e])) : 0;
+  }
+  it->n = max(it->nkt[0], it->nkt[1]);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                    const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, Dense P,
+                    __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
+                    int* __restrict__ next_item, int* __restrict__ status) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qbuf = smem;                          // [2]
+  uint8_t* kvbuf = qbuf + 2 * C::kTileBytes;     // [stages], K and V tiles in turn
+  Bars* bars = reinterpret_cast<Bars*>(kvbuf + C::kStages * C::kTileBytes);
+  volatile int* abort = &bars->abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < C::kStages; ++s) {
+      tc::mbar_init(&bars->kv_full[s], 1);
+      tc::mbar_init(&bars->kv_empty[s], 2);  // both MMA issuers
+    }
+    for (int b = 0; b < 2; ++b) {
+      tc::mbar_init(&bars->q_full[b], 1);
+      tc::mbar_init(&bars->q_empty[b], 1);
+      tc::mbar_init(&bars->s_full[b], 1);
+      tc::mbar_init(&bars->p_full[b], 4);    // the tile's softmax warps
+      tc::mbar_init(&bars->o_step[b], 1);
+      tc::mbar_init(&bars->o_done[b], 1);
+      tc::mbar_init(&bars->o_empty[b], 4);   // the epilogue warps
+      tc::mbar_init(&bars->l_full[b], 4);
+      tc::mbar_init(&bars->l_empty[b], 4);
+    }
+    for (int i = 0; i < kItems; ++i) {
+      tc::mbar_init(&bars->i_full[i], 1);
+      tc::mbar_init(&bars->i_empty[i], 14);  // 2 MMA, 8 softmax, 4 epilogue warps
+    }
+    tc::mbar_init(&bars->mma_done, 2);
+    bars->abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::tma_prefetch(&tmap_q);
+    tc::tma_prefetch(&tmap_k);
+    tc::tma_prefetch(&tmap_v);
+  }
+  if (warp == 1) tc::tmem_alloc(&bars->tmem_base, kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  bool failed = false;
+
+  if (warp < 4) {
+    regs_dec<kRegsCtl>();
+    if (warp == 0) {
+      // ---------------- producer: items and TMA ----------------
+      if (lane == 0) {
+        tc::ArmedRing q_armed, kv_armed;
+        int stage = 0, qn[2] = {0, 0};
+        uint32_t phase = 0;
+        int t = atomicAdd(next_item, 1);
+        for (int ii = 0; !failed; ++ii) {
+          const int slot = ii % kItems;
+          if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) {
+            failed = true;
+            break;
+          }
+          Item& it = bars->item[slot];
+          int b = 0, k0 = 0, g = 0;
+          if (t < P.pairs) make_item(P, t, &it, &b, &k0, &g);
+          else it.live = 0;
+          const int live = it.live, n = live ? it.n : 0;
+          int nkt[2], head[2], row0[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            nkt[e] = it.nkt[e];
+            head[e] = it.head[e];
+            row0[e] = it.row0[e];
+          }
+          tc::mbar_arrive(&bars->i_full[slot]);
+          if (!live) break;
+          t = atomicAdd(next_item, 1);  // the next one, on its way during this item's copies
+          auto load = [&](const CUtensorMap* map, int row) -> bool {
+            if (!tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1, abort)) return false;
+            uint64_t* fb = &bars->kv_full[stage];
+            uint8_t* dst = kvbuf + stage * C::kTileBytes;
+            tc::mbar_arrive_expect_tx(fb, C::kTileBytes);
+            kv_armed.note(stage, phase);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_load_3d(dst + h * C::kHalf, map, fb, 64 * h, g, row);
+            if (++stage == C::kStages) { stage = 0; phase ^= 1; }
+            return true;
+          };
+          auto load_q = [&](int e) -> bool {
+            if (nkt[e] == 0) return true;
+            if (!tc::mbar_wait(&bars->q_empty[e], (qn[e] & 1) ^ 1, abort)) return false;
+            tc::mbar_arrive_expect_tx(&bars->q_full[e], C::kTileBytes);
+            q_armed.note(e, qn[e] & 1);
+            ++qn[e];
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_load_3d(qbuf + e * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[e],
+                              64 * h, head[e], row0[e]);
+            return true;
+          };
+          bool good = true;
+          for (int j = 0; j < n && good; ++j) {
+            const int row = int(tile_row(P, b, k0, j));
+            if (j == 0) good = load_q(0);
+            good = good && load(&tmap_k, row);
+            if (j == 0) good = good && load_q(1);
+            good = good && load(&tmap_v, row);
+          }
+          failed = !good;
+        }
+        // every copy issued has landed before the CTA can leave
+        if (!(q_armed.drain(bars->q_full) && kv_armed.drain(bars->kv_full))) failed = true;
+      }
+    } else if (warp < 3) {
+      // ---------------- MMA issuer of query tile e ----------------
+      const int e = warp - 1;
+      const uint32_t st = tmem + e * 256, ot = st + 128;
+      int stage = 0, qn = 0, on = 0;   // ring position; items and key tiles of this tile so far
+      uint32_t phase = 0;
+      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+        const bool ok = lane != 0 || tc::mbar_spin(bar, parity, abort);
+        return __shfl_sync(MSA_FULL_MASK, ok ? 1 : 0, 0) != 0;
+      };
+      for (int ii = 0; !failed; ++ii) {
+        const int slot = ii % kItems;
+        if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+        const Item& it = bars->item[slot];
+        const int live = it.live, n = it.n, nkt = it.nkt[e], nk = it.nk;
+        const int seen = it.pos[e] + it.rows[e];  // keys that the tile's last row sees
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
+        if (!live) break;
+        for (int j = 0; j < n; ++j) {
+          const int ks = stage;
+          const uint32_t kp = phase;
+          if (++stage == C::kStages) { stage = 0; phase ^= 1; }
+          const int vs = stage;
+          const uint32_t vp = phase;
+          if (++stage == C::kStages) { stage = 0; phase ^= 1; }
+          if (!wait(&bars->kv_full[ks], kp)) { failed = true; break; }
+          if (j >= nkt) {  // the other tile's keys: hand the stages back
+            if (!wait(&bars->kv_full[vs], vp)) { failed = true; break; }
+            if (lane == 0) {
+              tc::mbar_arrive(&bars->kv_empty[ks]);
+              tc::mbar_arrive(&bars->kv_empty[vs]);
+            }
+            continue;
+          }
+          if (j == 0 && !wait(&bars->q_full[e], qn & 1)) { failed = true; break; }
+          if (lane == 0) {
+            tc::tc_fence_after();
+            const uint32_t qa = tc::smem_addr(qbuf + e * C::kTileBytes);
+            const uint32_t ka = tc::smem_addr(kvbuf + ks * C::kTileBytes);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
+              tc::mma_ss(st, tc::sdesc_sw128(qa + off, 16, 1024),
+                         tc::sdesc_sw128(ka + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
+            }
+            tc::mma_commit(&bars->s_full[e]);
+            tc::mma_commit(&bars->kv_empty[ks]);
+            if (j == nkt - 1) tc::mma_commit(&bars->q_empty[e]);
+          }
+          // P V over the keys that exist and that some row of the tile sees
+          const int keys = min(128, min(nk, seen) - j * 128);
+          if (!wait(&bars->kv_full[vs], vp)) { failed = true; break; }
+          const uint32_t va = tc::smem_addr(kvbuf + vs * C::kTileBytes);
+          if (keys & 15) {
+            // rows keys .. of the last group of 16: 128 bytes a row and half
+            // whatever the swizzle
+            const int tail = 16 - (keys & 15);
+            for (int i = lane; i < tail * (D / 64) * 8; i += 32) {
+              const int r = keys + i / (8 * (D / 64)), c = i % (8 * (D / 64));
+              *reinterpret_cast<uint4*>(kvbuf + vs * C::kTileBytes + (c >> 3) * C::kHalf +
+                                        r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
+            }
+            tc::fence_async_smem();
+            __syncwarp();
+          }
+          if (!wait(&bars->p_full[e], on & 1) ||
+              (j == 0 && !wait(&bars->o_empty[e], (qn & 1) ^ 1))) {
+            failed = true;
+            break;
+          }
+          if (lane == 0) {
+            tc::tc_fence_after();
+            const int groups = (keys + 15) >> 4;
+            for (int kk = 0; kk < groups; ++kk)
+              tc::mma_ts(ot, st + kk * 8, tc::sdesc_sw128(va + kk * 2048, C::kHalf, 1024),
+                         C::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
+            tc::mma_commit(&bars->kv_empty[vs]);
+            tc::mma_commit(&bars->o_step[e]);
+            if (j == nkt - 1) tc::mma_commit(&bars->o_done[e]);
+          }
+          ++on;
+        }
+        if (nkt > 0) ++qn;
+      }
+      // every MMA issued has completed before TMEM is freed
+      if (lane == 0 && !tc::mma_drain(&bars->mma_done)) failed = true;
+    }
+  } else if (warp < 12) {
+    // ---------------- softmax of query tile e ----------------
+    regs_inc<kRegsSoftmax>();
+    const int e = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t st = tmem + (uint32_t(quarter * 32) << 16) + e * 256, ot = st + 128;
+    const float sl2 = P.scale * 1.4426950408889634f;
+    const uint64_t sl2x2 = f2(sl2, sl2);
+    int qn = 0, on = 0;
+    for (int ii = 0; !failed; ++ii) {
+      const int slot = ii % kItems;
+      if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+      const Item& it = bars->item[slot];
+      const int live = it.live, nkt = it.nkt[e];
+      // last key that the row sees (rows behind the tile's last one: its last)
+      const int last = it.pos[e] + min(row, it.rows[e] - 1);
+      const long long lse_at =
+          lse && row < it.rows[e] ? (long long)(it.row0[e] + row) * P.Hq + it.head[e] : -1;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
+      if (!live) break;
+      if (nkt == 0) continue;
+      float m = -INFINITY, ms = 0.f, l = 0.f;  // running maximum, c m, sum
+      for (int j = 0; j < nkt; ++j, ++on) {
+        if (!warp_wait(&bars->s_full[e], on & 1, abort)) { failed = true; break; }
+        tc::tc_fence_after();
+        uint32_t v[4][32];
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) tc::tmem_ld32(st + q4 * 32, v[q4]);
+        tc::tmem_ld_wait();
+        const int lim = last - j * 128;  // last visible column
+        if (!__all_sync(MSA_FULL_MASK, lim >= 127)) {
+#pragma unroll
+          for (int q4 = 0; q4 < 4; ++q4)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (q4 * 32 + x > lim) v[q4][x] = __float_as_uint(-INFINITY);
+        }
+        float top = max32(v[0], -INFINITY);
+        top = fmaxf(fmaxf(top, max32(v[1], -INFINITY)), fmaxf(max32(v[2], -INFINITY),
+                                                             max32(v[3], -INFINITY)));
+        // the first tile sets the maximum; later ones move it only past the slack
+        const bool grow = j == 0 || (top - m) * sl2 > kSlack;
+        float keep = 1.f;
+        if (grow) {
+          const float nms = top == -INFINITY ? 0.f : top * sl2;
+          keep = m == -INFINITY ? 0.f : ex2_f32(ms - nms);
+          m = top;
+          ms = nms;
+        }
+        const uint64_t nmsx2 = f2(-ms, -ms);
+        uint64_t lsum[2] = {0, 0};
+#pragma unroll
+        for (int q4 = 0; q4 < 4; ++q4) {
+#pragma unroll
+          for (int x8 = 0; x8 < 2; ++x8) {
+            uint32_t pw[8];
+#pragma unroll
+            for (int x = 0; x < 16; x += 2) {
+              const uint32_t* s2 = v[q4] + x8 * 16 + x;
+              const uint64_t z = fma2((uint64_t(s2[1]) << 32) | s2[0], sl2x2, nmsx2);
+              const float pa = ex2_f32(__uint_as_float(uint32_t(z)));
+              const float pb = ex2_f32(__uint_as_float(uint32_t(z >> 32)));
+              lsum[(x >> 1) & 1] = add2(lsum[(x >> 1) & 1], f2(pa, pb));
+              pw[x >> 1] = pack_bf16(pa, pb);
+            }
+            tmem_st8(st + q4 * 16 + x8 * 8, pw);
+          }
+        }
+        if (j > 0 && __any_sync(MSA_FULL_MASK, grow)) {
+          // the tile's previous P V has written O: scale it
+          if (!warp_wait(&bars->o_step[e], (on & 1) ^ 1, abort)) { failed = true; break; }
+          tc::tc_fence_after();
+          const uint64_t k2 = f2(keep, keep);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 32) {
+            uint32_t o[32];
+            tc::tmem_ld32(ot + c, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 32; x += 2) {
+              const uint64_t y = mul2((uint64_t(o[x + 1]) << 32) | o[x], k2);
+              o[x] = uint32_t(y);
+              o[x + 1] = uint32_t(y >> 32);
+            }
+            tc::tmem_st32(ot + c, o);
+          }
+        }
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->p_full[e]);
+        const uint64_t lsx = add2(lsum[0], lsum[1]);
+        l = l * keep + (__uint_as_float(uint32_t(lsx)) + __uint_as_float(uint32_t(lsx >> 32)));
+      }
+      if (failed || !warp_wait(&bars->l_empty[e], (qn & 1) ^ 1, abort)) { failed = true; break; }
+      bars->l[e][row] = l;
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->l_full[e]);
+      if (lse_at >= 0) lse[lse_at] = (ms + log2f(l)) * kLn2;
+      ++qn;
+    }
+  } else {
+    // ---------------- epilogue of both query tiles ----------------
+    regs_dec<kRegsEpi>();
+    const int quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    int qn[2] = {0, 0};
+    for (int ii = 0; !failed; ++ii) {
+      const int slot = ii % kItems;
+      if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+      const Item& it = bars->item[slot];
+      const int live = it.live;
+      int nkt[2], rows[2], head[2], row0[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        nkt[e] = it.nkt[e];
+        rows[e] = it.rows[e];
+        head[e] = it.head[e];
+        row0[e] = it.row0[e];
+      }
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
+      if (!live) break;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        if (nkt[e] == 0 || failed) continue;
+        const uint32_t par = qn[e] & 1;
+        ++qn[e];
+        if (!warp_wait(&bars->l_full[e], par, abort)) { failed = true; continue; }
+        const float inv = 1.f / bars->l[e][row];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->l_empty[e]);
+        if (!warp_wait(&bars->o_done[e], par, abort)) { failed = true; continue; }
+        tc::tc_fence_after();
+        const uint32_t ot = tmem + (uint32_t(quarter * 32) << 16) + e * 256 + 128;
+        const long long at = (long long)(row0[e] + row) * P.Hq + head[e];
+        const bool mine = row < rows[e];
+        const uint64_t inv2 = f2(inv, inv);
+        uint4* dst = reinterpret_cast<uint4*>(out + at * D);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t o[32];
+          tc::tmem_ld32(ot + c * 32, o);
+          tc::tmem_ld_wait();
+          if (c == D / 32 - 1) {
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(&bars->o_empty[e]);
+          }
+          if (mine) {
+#pragma unroll
+            for (int k8 = 0; k8 < 4; ++k8) {
+              const uint32_t* w8 = o + 8 * k8;
+              uint4 u;
+              u.x = to_bf16x2(mul2((uint64_t(w8[1]) << 32) | w8[0], inv2));
+              u.y = to_bf16x2(mul2((uint64_t(w8[3]) << 32) | w8[2], inv2));
+              u.z = to_bf16x2(mul2((uint64_t(w8[5]) << 32) | w8[4], inv2));
+              u.w = to_bf16x2(mul2((uint64_t(w8[7]) << 32) | w8[6], inv2));
+              dst[c * 4 + k8] = u;
+            }
+          }
+        }
+      }
+    }
+  }
+  if (failed) {
+    bars->abort = 1;
+    atomicOr(status, tc::kStatusWaitTimeout);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// Rows of `heads` heads of D: tiles of 128 rows of one head, 64 dims at a time.
+cudaError_t encode_rows(CUtensorMap* map, const void* base, int D, int heads, long long rows) {
+  auto enc = encode_fn();
+  if (!enc) return cudaErrorNotSupported;
+  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(rows)};
+  cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(heads) * D * 2};
+  cuuint32_t box[3] = {64, 1, 128}, estr[3] = {1, 1, 1};
+  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
+             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+// Shared memory of a kernel, and the registers that its setmaxnreg split needs (a
+// build with fewer would leave warpgroups waiting for registers forever).
+template <typename K>
+cudaError_t prepare_kernel(K kern, size_t smem, int split) {
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+  if (e != cudaSuccess) return e;
+  cudaFuncAttributes fa;
+  e = cudaFuncGetAttributes(&fa, kern);
+  if (e != cudaSuccess) return e;
+  return fa.numRegs * (kThreads / 128) < split ? cudaErrorInvalidConfiguration : cudaSuccess;
+}
+
+template <int D>
+cudaError_t fwd_tc(const Dense& P, const void* q, const void* k, const void* v, void* out,
+                   float* lse, int32_t* counter, int32_t* status, cudaStream_t s) {
+  CUtensorMap mq, mk, mv;
+  cudaError_t e = encode_rows(&mq, q, D, P.Hq, P.rows_q);
+  if (e == cudaSuccess) e = encode_rows(&mk, k, D, P.Hkv, P.rows_k);
+  if (e == cudaSuccess) e = encode_rows(&mv, v, D, P.Hkv, P.rows_k);
+  if (e == cudaSuccess)
+    e = prepare_kernel(dense_fwd_tc_kernel<D>, smem_bytes<D>(),
+                       kRegsCtl + kRegsEpi + 2 * kRegsSoftmax);
+  if (e != cudaSuccess) return e;
+  dense_fwd_tc_kernel<D><<<std::min(sm_count(), P.pairs), kThreads, smem_bytes<D>(), s>>>(
+      mq, mk, mv, P, static_cast<__nv_bfloat16*>(out), lse, counter, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_dense_fwd_tc(const Dense& P, const void* q, const void* k, const void* v,
+                                void* out, float* lse, int32_t* counter, int32_t* status,
+                                cudaStream_t s) {
+  return (P.D == 128 ? fwd_tc<128> : fwd_tc<64>)(P, q, k, v, out, lse, counter, status, s);
+}
+
+}  // namespace msa
