@@ -17,9 +17,12 @@ constexpr int kStatusBadLength = 8;  // a kv_lens entry outside the cache
 // first query row; qt0, kt0, pr0: query tiles, key tiles and (tensor-core forward)
 // row-tile pairs x key heads of the sequences before it in this list, which is
 // sorted by length, longest first, so that the heaviest work is dealt out first.
+// qp0: its first row where every sequence's rows are padded to a multiple of 16.
 struct SeqRec {
-  int q0, k0, nq, nk, pos0, qt0, kt0, pr0;
+  int q0, k0, nq, nk, pos0, qt0, kt0, pr0, qp0;
 };
+
+__host__ __device__ inline int pad16(int n) { return (n + 15) & ~15; }
 
 struct Dense {
   int B, Sq, Skv;      // batched layout (seqs == nullptr); B is the number of records otherwise
@@ -28,6 +31,7 @@ struct Dense {
   bool f32;
   int pos0;            // batched layout: position of query row 0
   long long rows_q, rows_k;  // rows of q and of k in memory
+  long long rows_pad;        // rows of q, every sequence's padded to a multiple of 16
   int qtiles, ktiles;  // 128-row query tiles and key tiles of all sequences
   int pairs;           // row-tile pairs x key heads of all sequences
   const SeqRec* seqs;  // device, B records, or nullptr
@@ -62,6 +66,17 @@ cudaError_t launch_dense_fwd_simt(const Dense& P, const void* q, const void* k, 
 cudaError_t launch_dense_fwd_tc(const Dense& P, const void* q, const void* k, const void* v,
                                 void* out, float* lse, int32_t* counter, int32_t* status,
                                 cudaStream_t s);
+// Scratch of the tensor-core gradients: -lse log2 e and delta, [Hq, rows_pad] + 128
+// values each, and with several splits their partial sums, [splits][2][rows_k, Hkv, D].
+struct DenseBwdSpace {
+  float *nl, *dl, *part;
+};
+int dense_bwd_splits(const Dense& P);
+// counters: two zeroed words.
+cudaError_t launch_dense_bwd_tc(const Dense& P, const void* dout, const void* q, const void* k,
+                                const void* v, const void* out, const float* lse,
+                                const DenseBwdSpace& W, void* dq, void* dk, void* dv,
+                                int32_t* counters, int32_t* status, cudaStream_t s);
 cudaError_t launch_dense_bwd_simt(const Dense& P, const void* dout, const void* q, const void* k,
                                   const void* v, const void* out, const float* lse, float* delta,
                                   void* dq, void* dk, void* dv, cudaStream_t s);

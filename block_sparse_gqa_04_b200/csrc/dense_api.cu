@@ -60,8 +60,9 @@ msa_status_t resolve_heads(const msa_problem_t* p, Dense* P) {
 // Rows and work items have to be addressable with 32 bits.
 msa_status_t check_sizes(const Dense& P, long long qtiles, long long ktiles, long long pairs) {
   constexpr long long kMax = 1LL << 31;
-  if (P.rows_q >= kMax || P.rows_k >= kMax || qtiles * 2 * P.Hq >= kMax ||
-      ktiles * 2 * P.Hq >= kMax || pairs >= kMax || P.rows_q * P.Hq >= kMax * 4)
+  if (P.rows_pad >= kMax || P.rows_k >= kMax || qtiles * 2 * P.Hq >= kMax ||
+      ktiles * 2 * P.Hq >= kMax || pairs >= kMax || P.rows_q * P.Hq >= kMax * 4 ||
+      ktiles * P.Hkv * P.G >= kMax)
     return MSA_ERR_UNSUPPORTED;
   return MSA_OK;
 }
@@ -76,6 +77,7 @@ msa_status_t resolve_batched(const msa_problem_t* p, Dense* P) {
   P->pos0 = int(p->q_pos0);
   P->table_w = tiles(p->kv_len);
   P->rows_q = (long long)P->B * P->Sq;
+  P->rows_pad = (long long)P->B * ((P->Sq + 15LL) / 16 * 16);
   P->rows_k = P->table ? (long long)P->pages * msa::kDenseTile : (long long)P->B * P->Skv;
   const long long qt = (long long)P->B * tiles(P->Sq), kt = (long long)P->B * tiles(P->Skv);
   const long long pairs = (long long)P->B * P->Hkv * msa::dense_pairs(tiles(P->Sq), P->G);
@@ -94,16 +96,18 @@ msa_status_t resolve_packed(const msa_problem_t* p, const int32_t* cu_q, const i
   if (p->batch > kMaxSeqs || !cu_q || !cu_k || cu_q[0] != 0 || cu_k[0] != 0)
     return MSA_ERR_INVALID_ARG;
   if (p->num_pages != 0) return MSA_ERR_UNSUPPORTED;
-  long long qt = 0, kt = 0, pairs = 0;
+  long long qt = 0, kt = 0, pairs = 0, pad = 0;
   for (int b = 0; b < p->batch; ++b) {
     const long long nq = (long long)cu_q[b + 1] - cu_q[b], nk = (long long)cu_k[b + 1] - cu_k[b];
     if (nq < 0 || nk < 0 || nq > nk) return MSA_ERR_INVALID_ARG;
+    pad += (nq + 15) / 16 * 16;
     qt += tiles(nq);
     kt += tiles(nk);
     pairs += (long long)P->Hkv * msa::dense_pairs(tiles(nq), P->G);
-    if (recs) recs[b] = SeqRec{cu_q[b], cu_k[b], int(nq), int(nk), int(nk - nq), 0, 0, 0};
+    if (recs) recs[b] = SeqRec{cu_q[b], cu_k[b], int(nq), int(nk), int(nk - nq), 0, 0, 0, 0};
   }
   P->rows_q = cu_q[p->batch];
+  P->rows_pad = pad;
   P->rows_k = cu_k[p->batch];
   if ((st = check_sizes(*P, qt, kt, pairs)) != MSA_OK) return st;
   P->qtiles = int(qt);
@@ -119,6 +123,8 @@ msa_status_t resolve_packed(const msa_problem_t* p, const int32_t* cu_q, const i
       r.qt0 = at.qt0;
       r.kt0 = at.kt0;
       r.pr0 = at.pr0;
+      r.qp0 = at.qp0;
+      at.qp0 += msa::pad16(r.nq);
       at.qt0 += tiles(r.nq);
       at.kt0 += tiles(r.nk);
       at.pr0 += P->Hkv * msa::dense_pairs(tiles(r.nq), P->G);
@@ -134,7 +140,7 @@ msa_status_t resolve_dense(const msa_problem_t* p, const int32_t* cu_q, const in
 }
 
 struct DenseLayout {
-  size_t status, recs, delta, total;
+  size_t status, recs, nl, delta, part, total;
 };
 
 DenseLayout dense_layout(const Dense& P, bool packed, bool backward) {
@@ -143,7 +149,15 @@ DenseLayout dense_layout(const Dense& P, bool packed, bool backward) {
   auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
   L.status = take(kHeadBytes);
   if (packed) L.recs = take(size_t(P.B) * sizeof(SeqRec));
-  if (backward) L.delta = take(size_t(P.rows_q) * P.Hq * sizeof(float));
+  if (backward && P.f32) {
+    L.delta = take(size_t(P.rows_q) * P.Hq * sizeof(float));
+  } else if (backward) {
+    const size_t rows = (size_t(P.rows_pad) * P.Hq + msa::kDenseTile) * sizeof(float);
+    const int splits = msa::dense_bwd_splits(P);
+    L.nl = take(rows);
+    L.delta = take(rows);
+    if (splits > 1) L.part = take(size_t(splits) * 2 * P.rows_k * P.Hkv * P.D * sizeof(float));
+  }
   L.total = off;
   return L;
 }
@@ -282,8 +296,13 @@ msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlen
   if ((st = check_ws(ws, ws_bytes, L.total)) != MSA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = begin(&P, R, L, ws, s)) != MSA_OK) return st;
-  return msa::status_of(msa::launch_dense_bwd_simt(P, dout, q, k, v, out, lse,
-                                                   at<float>(ws, L.delta), dq, dk, dv, s));
+  if (P.f32)
+    return msa::status_of(msa::launch_dense_bwd_simt(P, dout, q, k, v, out, lse,
+                                                     at<float>(ws, L.delta), dq, dk, dv, s));
+  int32_t* head = at<int32_t>(ws, L.status);
+  const msa::DenseBwdSpace W{at<float>(ws, L.nl), at<float>(ws, L.delta), at<float>(ws, L.part)};
+  return msa::status_of(
+      msa::launch_dense_bwd_tc(P, dout, q, k, v, out, lse, W, dq, dk, dv, head + 1, head, s));
 }
 
 size_t msa_tree_workspace_size(const msa_problem_t* p) {
@@ -382,7 +401,7 @@ namespace msa {
 namespace {
 
 // Records per launch: as many as fit the 4 KB of kernel parameters.
-constexpr int kChunkRecs = 120;
+constexpr int kChunkRecs = 112;
 struct Chunk {
   SeqRec r[kChunkRecs];
 };

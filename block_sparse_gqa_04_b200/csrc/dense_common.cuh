@@ -20,7 +20,8 @@ __device__ __forceinline__ int find_seq(const SeqRec* seqs, int n, int x) {
 
 __device__ __forceinline__ SeqRec batch_seq(const Dense& P, int b) {
   // the rows of q, and of an unpaged k, are below 2^31; a paged k has no k0
-  return SeqRec{b * P.Sq, P.table ? 0 : b * P.Skv, P.Sq, P.Skv, P.pos0, 0, 0, 0};
+  return SeqRec{b * P.Sq, P.table ? 0 : b * P.Skv, P.Sq, P.Skv, P.pos0, 0, 0, 0,
+                b * pad16(P.Sq)};
 }
 
 // Query tile `t` of all sequences: its sequence and its tile there, last (heaviest)

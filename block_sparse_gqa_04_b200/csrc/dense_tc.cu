@@ -27,8 +27,7 @@
 // is zeroed in shared memory first.
 #include <algorithm>
 
-#include "dense_common.cuh"
-#include "tc_warp.cuh"
+#include "dense_tc.cuh"
 
 namespace msa {
 namespace {
@@ -40,7 +39,6 @@ constexpr int kItems = 2;     // items in flight
 constexpr float kSlack = 8.f;
 // 96 + 64 + 2 x 176 = 512 = 4 x 128: the registers the CTA is launched with
 constexpr int kRegsCtl = 96, kRegsEpi = 64, kRegsSoftmax = 176;
-constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Cfg {
@@ -81,8 +79,6 @@ constexpr size_t smem_bytes() {
   return 1024 + size_t(2 + Cfg<D>::kStages) * Cfg<D>::kTileBytes + sizeof(Bars) + 64;
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory of a CTA");
-
-__device__ __forceinline__ int tiles_of(int n) { return (n + kDenseTile - 1) / kDenseTile; }
 
 // Item t of the launch; b and k0 locate its keys (b: batch index for a block table).
 __device__ __forceinline__ void make_item(const Dense& P, int t, Item* it, int* b, int* k0, int* g) {
@@ -291,18 +287,8 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const int keys = min(128, min(nk, seen) - j * 128);
           if (!wait(&bars->kv_full[vs], vp)) { failed = true; break; }
           const uint32_t va = tc::smem_addr(kvbuf + vs * C::kTileBytes);
-          if (keys & 15) {
-            // rows keys .. of the last group of 16: 128 bytes a row and half
-            // whatever the swizzle
-            const int tail = 16 - (keys & 15);
-            for (int i = lane; i < tail * (D / 64) * 8; i += 32) {
-              const int r = keys + i / (8 * (D / 64)), c = i % (8 * (D / 64));
-              *reinterpret_cast<uint4*>(kvbuf + vs * C::kTileBytes + (c >> 3) * C::kHalf +
-                                        r * 128 + (c & 7) * 16) = make_uint4(0, 0, 0, 0);
-            }
-            tc::fence_async_smem();
-            __syncwarp();
-          }
+          if (keys & 15)
+            zero_rows<D>(kvbuf + vs * C::kTileBytes, keys, (keys + 15) & ~15);
           if (!wait(&bars->p_full[e], on & 1) ||
               (j == 0 && !wait(&bars->o_empty[e], (qn & 1) ^ 1))) {
             failed = true;
@@ -331,7 +317,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     const int e = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t st = tmem + (uint32_t(quarter * 32) << 16) + e * 256, ot = st + 128;
-    const float sl2 = P.scale * 1.4426950408889634f;
+    const float sl2 = P.scale * kLog2e;
     const uint64_t sl2x2 = f2(sl2, sl2);
     int qn = 0, on = 0;
     for (int ii = 0; !failed; ++ii) {
@@ -503,33 +489,6 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   }
 }
 
-// Rows of `heads` heads of D: tiles of 128 rows of one head, 64 dims at a time.
-cudaError_t encode_rows(CUtensorMap* map, const void* base, int D, int heads, long long rows) {
-  auto enc = encode_fn();
-  if (!enc) return cudaErrorNotSupported;
-  cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(rows)};
-  cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(heads) * D * 2};
-  cuuint32_t box[3] = {64, 1, 128}, estr[3] = {1, 1, 1};
-  return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
-             estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
-             ? cudaSuccess
-             : cudaErrorInvalidValue;
-}
-
-// Shared memory of a kernel, and the registers that its setmaxnreg split needs (a
-// build with fewer would leave warpgroups waiting for registers forever).
-template <typename K>
-cudaError_t prepare_kernel(K kern, size_t smem, int split) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
-  if (e != cudaSuccess) return e;
-  cudaFuncAttributes fa;
-  e = cudaFuncGetAttributes(&fa, kern);
-  if (e != cudaSuccess) return e;
-  return fa.numRegs * (kThreads / 128) < split ? cudaErrorInvalidConfiguration : cudaSuccess;
-}
-
 template <int D>
 cudaError_t fwd_tc(const Dense& P, const void* q, const void* k, const void* v, void* out,
                    float* lse, int32_t* counter, int32_t* status, cudaStream_t s) {
@@ -539,7 +498,7 @@ cudaError_t fwd_tc(const Dense& P, const void* q, const void* k, const void* v, 
   if (e == cudaSuccess) e = encode_rows(&mv, v, D, P.Hkv, P.rows_k);
   if (e == cudaSuccess)
     e = prepare_kernel(dense_fwd_tc_kernel<D>, smem_bytes<D>(),
-                       kRegsCtl + kRegsEpi + 2 * kRegsSoftmax);
+                       kRegsCtl + kRegsEpi + 2 * kRegsSoftmax, kThreads);
   if (e != cudaSuccess) return e;
   dense_fwd_tc_kernel<D><<<std::min(sm_count(), P.pairs), kThreads, smem_bytes<D>(), s>>>(
       mq, mk, mv, P, static_cast<__nv_bfloat16*>(out), lse, counter, status);

@@ -1,0 +1,917 @@
+// Gradients of dense causal attention on tcgen05 tensor cores (bf16, head_dim 64 or
+// 128), in two passes so that every sum has one owner and a fixed order (no atomics):
+//   dk, dv: a CTA owns 128 keys of a key head and walks the group's heads and the query
+//           tiles that see them.  With keys as rows (lanes of TMEM),
+//             S^T = K Q^T,  dP^T = V dO^T,  P^T = 2^(c S^T - c lse),
+//             dS^T = P^T (dP^T - delta),  dV += P^T dO,  dK += dS^T Q:
+//           P^T and dS^T are written to TMEM over S^T and dP^T as bf16 and are A operands
+//           there; Q and dO serve as K-major operands of the first two products and as
+//           MN-major operands of the last two, so nothing is stored twice.
+//   dq:     a CTA owns 128 query rows of a head and walks the keys they see, with the
+//           rows as lanes: S = Q K^T, dP = dO V^T, dS as above, dQ += dS K.
+// The two passes take 4 + 3 products of 128 x 128 x D per pair of tiles where a single
+// pass would take 5; in exchange no gradient leaves the chip before it is finished.
+//
+// One thread issues all MMAs in an order that keeps the pipe fed while the eight
+// elementwise warps (two warpgroups, half of the columns each) work on the other half
+// of a step: dK, dV pass ... dV(i) S(i+1) | dK(i) dP(i+1) | ..., dq pass ... dQ(i)
+// dP(i+1) S(i+2) ...: P(i+1) is computed during the products between the first pair of
+// bars, dS(i+1) during the next.
+//
+// Rows behind the end of a sequence come in with its last tiles.  Query rows there have
+// lse = inf, hence P = 0; the products that sum over rows stop at whole groups of 16,
+// and the rest of the last group is zeroed in shared memory before use.
+#include <algorithm>
+
+#include "dense_tc.cuh"
+
+namespace msa {
+namespace {
+
+// warp 0 items and TMA, warp 1 MMA, warps 2-3 idle, warps 4-11 elementwise
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kItems = 2;
+
+template <int D>
+struct Cfg {
+  static constexpr int kTileBytes = 128 * D * 2;
+  static constexpr int kHalf = 128 * 64 * 2;
+  static constexpr int kStages = 2;                     // dkv: of Q and of dO
+  static constexpr int kRing = D == 128 ? 5 : 8;        // dq: of K and V tiles in turn
+  static constexpr uint32_t kIdescS = tc::idesc_bf16_f32(128, 128, 0, 0);
+  static constexpr uint32_t kIdescG = tc::idesc_bf16_f32(128, D, 0, 1);
+};
+
+__device__ __forceinline__ uint64_t pair_of(const uint32_t* v) {
+  return (uint64_t(v[1]) << 32) | v[0];
+}
+__device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float(uint32_t(x)); }
+__device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float(uint32_t(x >> 32)); }
+
+// S = A B^T over D, both tiles K-major.
+template <int D>
+__device__ __forceinline__ void issue_nt(uint32_t d, uint32_t a, uint32_t b) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    const uint32_t off = (kk >> 2) * Cfg<D>::kHalf + (kk & 3) * 32;
+    tc::mma_ss(d, tc::sdesc_sw128(a + off, 16, 1024), tc::sdesc_sw128(b + off, 16, 1024),
+               Cfg<D>::kIdescS, kk > 0 ? 1u : 0u);
+  }
+}
+
+// G += A B over `groups` groups of 16 rows of B (MN-major tile); A in TMEM as bf16, its
+// first 64 columns of elements at a, the others 64 TMEM columns on.
+template <int D>
+__device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint32_t b, int groups,
+                                         bool fresh) {
+  for (int kk = 0; kk < groups; ++kk)
+    tc::mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8,
+               tc::sdesc_sw128(b + kk * 2048, Cfg<D>::kHalf, 1024), Cfg<D>::kIdescG,
+               (!fresh || kk > 0) ? 1u : 0u);
+}
+
+// ---------------------------------------------------------------------------
+// -c lse and delta = sum_d dout out per (head, row), rows of a sequence padded to
+// groups of 16 (padding: -inf, so that P = 0, and 0): one warp per (16 rows, head).
+// ---------------------------------------------------------------------------
+template <int D>
+__global__ void __launch_bounds__(256)
+dense_prep_kernel(Dense P, const __nv_bfloat16* __restrict__ dout,
+                  const __nv_bfloat16* __restrict__ out, const float* __restrict__ lse,
+                  float* __restrict__ nl, float* __restrict__ dl) {
+  constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
+  const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int lane = threadIdx.x & 31;
+  const int h = int(w % P.Hq);
+  const long long x0 = w / P.Hq * 16;  // padded row
+  if (x0 >= P.rows_pad) return;
+  SeqRec s;
+  if (P.seqs) {
+    s = P.seqs[find_seq<&SeqRec::qp0>(P.seqs, P.B, int(x0))];
+  } else {
+    s = batch_seq(P, int(x0 / pad16(P.Sq)));
+  }
+  const int i0 = int(x0) - s.qp0;
+  float mine = 0.f;
+#pragma unroll
+  for (int r0 = 0; r0 < 16; r0 += kRowsAtOnce) {
+    const int i = i0 + r0 + lane / kLanes;
+    float sum = 0.f;
+    if (i < s.nq) {
+      const long long at = ((long long)(s.q0 + i) * P.Hq + h) * D + (lane % kLanes) * 8;
+      float a[8], b[8];
+      load_vec<__nv_bfloat16, 8>(dout + at, a);
+      load_vec<__nv_bfloat16, 8>(out + at, b);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += a[e] * b[e];
+    }
+#pragma unroll
+    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(MSA_FULL_MASK, sum, o);
+    // lane r of the warp keeps row r
+    const float got = __shfl_sync(MSA_FULL_MASK, sum, (lane % kRowsAtOnce) * kLanes);
+    if (lane / kRowsAtOnce == r0 / kRowsAtOnce) mine = got;
+  }
+  if (lane < 16) {
+    const bool there = i0 + lane < s.nq;
+    const long long at = (long long)h * P.rows_pad + x0 + lane;
+    nl[at] = there ? -kLog2e * lse[(long long)(s.q0 + i0 + lane) * P.Hq + h] : -INFINITY;
+    dl[at] = there ? mine : 0.f;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// dk, dv
+// ---------------------------------------------------------------------------
+struct KeyItem {
+  int live;
+  int nk, j0, k0, g;      // keys of the sequence; first key of the tile; its first row in k
+  int h0, heads;          // heads of this item
+  int qt0, nqt;           // query tiles that see the tile
+  int q0, qp0, nq, pos0;
+  int split;
+};
+
+struct KeyBars {
+  uint64_t kv_full, kv_empty;
+  uint64_t q_full[2], q_empty[2], g_full[2], g_empty[2];  // Q (with lse, delta) and dO stages
+  uint64_t s_full, p_full, dp_full, ds_full, acc_full, acc_empty;
+  uint64_t i_full[kItems], i_empty[kItems];
+  uint64_t mma_done;
+  KeyItem item[kItems];
+  alignas(16) float nl[2][128];
+  alignas(16) float dl[2][128];
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+constexpr size_t key_smem() {
+  return 1024 + size_t(6) * Cfg<D>::kTileBytes + sizeof(KeyBars) + 64;
+}
+static_assert(key_smem<128>() <= 232448, "shared memory of a CTA");
+
+__device__ __forceinline__ void make_key_item(const Dense& P, int t, int splits, KeyItem* it) {
+  const int split = t % splits;
+  t /= splits;
+  const int g = t % P.Hkv;
+  int kt;
+  const SeqRec s = key_tile(P, t / P.Hkv, &kt);
+  const int per = (P.G + splits - 1) / splits;
+  it->live = 1;
+  it->nk = s.nk;
+  it->j0 = kt * kDenseTile;
+  it->k0 = s.k0 + it->j0;
+  it->g = g;
+  it->h0 = g * P.G + split * per;
+  it->heads = max(0, min(per, P.G - split * per));
+  // the first query row that sees key j0 sits at position j0
+  const int nqt = tiles_of(s.nq);
+  it->qt0 = min(max(0, it->j0 - s.pos0) / kDenseTile, nqt);
+  it->nqt = nqt;
+  it->q0 = s.q0;
+  it->qp0 = s.qp0;
+  it->nq = s.nq;
+  it->pos0 = s.pos0;
+  it->split = split;
+}
+
+template <int D, bool PART>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                    const __grid_constant__ CUtensorMap tmap_g,
+                    const __grid_constant__ CUtensorMap tmap_k,
+                    const __grid_constant__ CUtensorMap tmap_v, Dense P, int splits, int items,
+                    const float* __restrict__ nl, const float* __restrict__ dl,
+                    __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
+                    float* __restrict__ part, int* __restrict__ next_item,
+                    int* __restrict__ status) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* kbuf = smem;
+  uint8_t* vbuf = kbuf + C::kTileBytes;
+  uint8_t* qbuf = vbuf + C::kTileBytes;        // [2]
+  uint8_t* gbuf = qbuf + 2 * C::kTileBytes;    // [2]
+  KeyBars* bars = reinterpret_cast<KeyBars*>(gbuf + 2 * C::kTileBytes);
+  volatile int* abort = &bars->abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->kv_full, 1);
+    tc::mbar_init(&bars->kv_empty, 1);
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&bars->q_full[s], 1);
+      tc::mbar_init(&bars->q_empty[s], 1);
+      tc::mbar_init(&bars->g_full[s], 1);
+      tc::mbar_init(&bars->g_empty[s], 1);
+    }
+    tc::mbar_init(&bars->s_full, 1);
+    tc::mbar_init(&bars->p_full, 8);
+    tc::mbar_init(&bars->dp_full, 1);
+    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->acc_full, 1);
+    tc::mbar_init(&bars->acc_empty, 8);
+    for (int i = 0; i < kItems; ++i) {
+      tc::mbar_init(&bars->i_full[i], 1);
+      tc::mbar_init(&bars->i_empty[i], 9);  // the MMA warp and 8 elementwise warps
+    }
+    tc::mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::tma_prefetch(&tmap_q);
+    tc::tma_prefetch(&tmap_g);
+    tc::tma_prefetch(&tmap_k);
+    tc::tma_prefetch(&tmap_v);
+  }
+  if (warp == 1) tc::tmem_alloc(&bars->tmem_base, kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  // S^T | dP^T | dV | dK
+  const uint32_t ts = tmem, tp = tmem + 128, tv = tmem + 256, tk = tmem + 256 + D;
+  bool failed = false;
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    if (lane == 0) {
+      tc::ArmedRing kv_armed, q_armed, g_armed;
+      int n = 0, used = 0;  // steps and items with steps so far
+      int t = atomicAdd(next_item, 1);
+      for (int ii = 0; !failed; ++ii) {
+        const int slot = ii % kItems;
+        if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) {
+          failed = true;
+          break;
+        }
+        if (t < items) make_key_item(P, t, splits, &bars->item[slot]);
+        else bars->item[slot].live = 0;
+        const KeyItem it = bars->item[slot];
+        tc::mbar_arrive(&bars->i_full[slot]);
+        if (!it.live) break;
+        t = atomicAdd(next_item, 1);
+        if (it.heads == 0 || it.qt0 >= it.nqt) continue;
+        if (!tc::mbar_wait(&bars->kv_empty, (used & 1) ^ 1, abort)) { failed = true; break; }
+        tc::mbar_arrive_expect_tx(&bars->kv_full, 2 * C::kTileBytes);
+        kv_armed.note(0, used & 1);
+        ++used;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          tc::tma_load_3d(kbuf + h * C::kHalf, &tmap_k, &bars->kv_full, 64 * h, it.g, it.k0);
+          tc::tma_load_3d(vbuf + h * C::kHalf, &tmap_v, &bars->kv_full, 64 * h, it.g, it.k0);
+        }
+        for (int hh = it.h0; hh < it.h0 + it.heads && !failed; ++hh) {
+          for (int qt = it.qt0; qt < it.nqt; ++qt, ++n) {
+            const int s = n & 1, par = (n >> 1) & 1, row = it.q0 + qt * 128;
+            const long long at = (long long)hh * P.rows_pad + it.qp0 + qt * 128;
+            if (!tc::mbar_wait(&bars->q_empty[s], par ^ 1, abort)) { failed = true; break; }
+            tc::mbar_arrive_expect_tx(&bars->q_full[s], C::kTileBytes + 1024);
+            q_armed.note(s, par);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_load_3d(qbuf + s * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[s],
+                              64 * h, hh, row);
+            tc::bulk_load(bars->nl[s], nl + at, 512, &bars->q_full[s]);
+            tc::bulk_load(bars->dl[s], dl + at, 512, &bars->q_full[s]);
+            if (!tc::mbar_wait(&bars->g_empty[s], par ^ 1, abort)) { failed = true; break; }
+            tc::mbar_arrive_expect_tx(&bars->g_full[s], C::kTileBytes);
+            g_armed.note(s, par);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_load_3d(gbuf + s * C::kTileBytes + h * C::kHalf, &tmap_g, &bars->g_full[s],
+                              64 * h, hh, row);
+          }
+        }
+      }
+      if (!(kv_armed.drain(&bars->kv_full) && q_armed.drain(bars->q_full) &&
+            g_armed.drain(bars->g_full)))
+        failed = true;
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      const bool ok = lane != 0 || tc::mbar_spin(bar, parity, abort);
+      return __shfl_sync(MSA_FULL_MASK, ok ? 1 : 0, 0) != 0;
+    };
+    int n = 0, used = 0;
+    for (int ii = 0; !failed; ++ii) {
+      const int slot = ii % kItems;
+      if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+      const KeyItem it = bars->item[slot];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
+      if (!it.live) break;
+      const int tiles = it.nqt - it.qt0, steps = it.heads * tiles;
+      if (steps <= 0) continue;
+      const uint32_t ka = tc::smem_addr(kbuf), va = tc::smem_addr(vbuf);
+      // S(i) and dP(i): the tile's rows are there, those behind the sequence zero
+      auto first = [&](int i) -> bool {
+        const int s = (n + i) & 1, rows = min(128, it.nq - (it.qt0 + i % tiles) * 128);
+        if (!wait(&bars->q_full[s], ((n + i) >> 1) & 1)) return false;
+        uint8_t* q = qbuf + s * C::kTileBytes;
+        if (rows & 15) zero_rows<D>(q, rows, (rows + 15) & ~15);
+        if (lane == 0) {
+          tc::tc_fence_after();
+          issue_nt<D>(ts, ka, tc::smem_addr(q));
+          tc::mma_commit(&bars->s_full);
+        }
+        return true;
+      };
+      auto second = [&](int i) -> bool {
+        const int s = (n + i) & 1, rows = min(128, it.nq - (it.qt0 + i % tiles) * 128);
+        if (!wait(&bars->g_full[s], ((n + i) >> 1) & 1)) return false;
+        uint8_t* g = gbuf + s * C::kTileBytes;
+        if (rows & 15) zero_rows<D>(g, rows, (rows + 15) & ~15);
+        if (lane == 0) {
+          tc::tc_fence_after();
+          issue_nt<D>(tp, va, tc::smem_addr(g));
+          tc::mma_commit(&bars->dp_full);
+        }
+        return true;
+      };
+      if (!wait(&bars->kv_full, used & 1) || !first(0) || !second(0)) { failed = true; break; }
+      for (int i = 0; i < steps; ++i) {
+        const int s = (n + i) & 1, rows = min(128, it.nq - (it.qt0 + i % tiles) * 128);
+        const int groups = (rows + 15) >> 4;
+        if (!wait(&bars->p_full, (n + i) & 1) ||
+            (i == 0 && !wait(&bars->acc_empty, (used & 1) ^ 1))) {
+          failed = true;
+          break;
+        }
+        if (lane == 0) {
+          tc::tc_fence_after();
+          issue_ts<D>(tv, ts, tc::smem_addr(gbuf + s * C::kTileBytes), groups, i == 0);
+          tc::mma_commit(&bars->g_empty[s]);
+        }
+        if (i + 1 < steps && !first(i + 1)) { failed = true; break; }
+        if (!wait(&bars->ds_full, (n + i) & 1)) { failed = true; break; }
+        if (lane == 0) {
+          tc::tc_fence_after();
+          issue_ts<D>(tk, tp, tc::smem_addr(qbuf + s * C::kTileBytes), groups, i == 0);
+          tc::mma_commit(&bars->q_empty[s]);
+        }
+        if (i + 1 < steps && !second(i + 1)) { failed = true; break; }
+      }
+      if (failed) break;
+      if (lane == 0) {
+        tc::mma_commit(&bars->kv_empty);
+        tc::mma_commit(&bars->acc_full);
+      }
+      n += steps;
+      ++used;
+    }
+    if (lane == 0 && !tc::mma_drain(&bars->mma_done)) failed = true;
+  } else if (warp >= 4) {
+    // ---------------- elementwise: P, dS, then the tile's dV (first warpgroup) or dK ----------------
+    const int half = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = uint32_t(quarter * 32) << 16;
+    const uint32_t sa = ts + lanes + half * 64, pa = tp + lanes + half * 64;
+    const float sl2 = P.scale * kLog2e;
+    const uint64_t sl2x2 = f2(sl2, sl2);
+    int n = 0, used = 0;
+    for (int ii = 0; !failed; ++ii) {
+      const int slot = ii % kItems;
+      if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+      const KeyItem it = bars->item[slot];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
+      if (!it.live) break;
+      const int tiles = it.nqt - it.qt0, steps = it.heads * tiles;
+      for (int i = 0; i < steps; ++i, ++n) {
+        const int s = n & 1;
+        const uint32_t par = n & 1;
+        // first column of this half that sees the thread's key
+        const int from = it.j0 + row - it.pos0 - (it.qt0 + i % tiles) * 128 - half * 64;
+        if (!warp_wait(&bars->q_full[s], (n >> 1) & 1, abort) ||
+            !warp_wait(&bars->s_full, par, abort)) {
+          failed = true;
+          break;
+        }
+        tc::tc_fence_after();
+        uint32_t p[2][32];
+        tc::tmem_ld32(sa, p[0]);
+        tc::tmem_ld32(sa + 32, p[1]);
+        tc::tmem_ld_wait();
+        const float4* nl4 = reinterpret_cast<const float4*>(bars->nl[s] + half * 64);
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            const float4 f = nl4[c * 8 + x / 4];
+            const uint64_t a = fma2(pair_of(&p[c][x]), sl2x2, f2(f.x, f.y));
+            const uint64_t b = fma2(pair_of(&p[c][x + 2]), sl2x2, f2(f.z, f.w));
+            p[c][x] = __float_as_uint(ex2_f32(lo_of(a)));
+            p[c][x + 1] = __float_as_uint(ex2_f32(hi_of(a)));
+            p[c][x + 2] = __float_as_uint(ex2_f32(lo_of(b)));
+            p[c][x + 3] = __float_as_uint(ex2_f32(hi_of(b)));
+          }
+        if (__any_sync(MSA_FULL_MASK, from > 0)) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (c * 32 + x < from) p[c][x] = 0u;
+        }
+        {
+          uint32_t w[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            w[x] = pack_bf16(__uint_as_float(p[x >> 4][(2 * x) & 31]),
+                             __uint_as_float(p[x >> 4][(2 * x + 1) & 31]));
+          tc::tmem_st32(sa, w);
+        }
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->p_full);
+        if (!warp_wait(&bars->dp_full, par, abort)) { failed = true; break; }
+        tc::tc_fence_after();
+        const float4* dl4 = reinterpret_cast<const float4*>(bars->dl[s] + half * 64);
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t d[32];
+          tc::tmem_ld32(pa + c * 32, d);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; x += 4) {
+            const float4 f = dl4[c * 8 + x / 4];
+            const uint64_t a = mul2(pair_of(&p[c][x]), add2(pair_of(&d[x]), f2(-f.x, -f.y)));
+            const uint64_t b = mul2(pair_of(&p[c][x + 2]), add2(pair_of(&d[x + 2]), f2(-f.z, -f.w)));
+            w[c * 16 + x / 2] = to_bf16x2(a);
+            w[c * 16 + x / 2 + 1] = to_bf16x2(b);
+          }
+        }
+        tc::tmem_st32(pa, w);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+      }
+      if (failed) break;
+      const bool any = steps > 0;
+      if (any) {
+        if (!warp_wait(&bars->acc_full, used & 1, abort)) { failed = true; break; }
+        tc::tc_fence_after();
+        ++used;
+      }
+      const float scale = half ? P.scale : 1.f;
+      const bool mine = it.j0 + row < it.nk;
+      const long long at = ((long long)(it.k0 + row) * P.Hkv + it.g) * D;
+      const uint32_t acc = (half ? tk : tv) + lanes;
+      __nv_bfloat16* dst = half ? dk : dv;
+      float* pdst = part + ((long long)(it.split * 2 + half) * P.rows_k * P.Hkv) * D;
+#pragma unroll 1
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t o[32];
+        if (any) {
+          tc::tmem_ld32(acc + c * 32, o);
+          tc::tmem_ld_wait();
+        } else {
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] = 0u;
+        }
+        if (mine && PART) {
+#pragma unroll
+          for (int x = 0; x < 32; x += 4)
+            *reinterpret_cast<uint4*>(pdst + at + c * 32 + x) =
+                make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
+        } else if (mine) {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            w[x] = pack_bf16(__uint_as_float(o[2 * x]) * scale,
+                             __uint_as_float(o[2 * x + 1]) * scale);
+#pragma unroll
+          for (int x = 0; x < 16; x += 4)
+            *reinterpret_cast<uint4*>(dst + at + c * 32 + 2 * x) =
+                make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+        }
+      }
+      if (any) {
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->acc_empty);
+      }
+    }
+  }
+  if (failed) {
+    bars->abort = 1;
+    atomicOr(status, tc::kStatusWaitTimeout);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// dk, dv = the sum of the splits' partial sums, in order.  part [splits][dv, dk][n].
+__global__ void __launch_bounds__(256)
+dense_dkv_sum_kernel(const float* __restrict__ part, int splits, long long n, float scale,
+                     __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const int which = blockIdx.y;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int s = 0; s < splits; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(part + (s * 2 + which) * n + i);
+    sum.x += x.x;
+    sum.y += x.y;
+    sum.z += x.z;
+    sum.w += x.w;
+  }
+  const float f = which ? scale : 1.f;
+  *reinterpret_cast<uint2*>((which ? dk : dv) + i) =
+      make_uint2(pack_bf16(sum.x * f, sum.y * f), pack_bf16(sum.z * f, sum.w * f));
+}
+
+// ---------------------------------------------------------------------------
+// dq
+// ---------------------------------------------------------------------------
+struct RowItem {
+  int live;
+  int n;                  // key tiles
+  int rows, pos, row0, pad0, head, nk;
+};
+
+struct RowBars {
+  uint64_t q_full, q_empty;
+  uint64_t kv_full[8], kv_empty[8];
+  uint64_t s_full[2], dp_full, ds_full, acc_full, acc_empty;
+  uint64_t i_full[kItems], i_empty[kItems];
+  uint64_t mma_done;
+  RowItem item[kItems];
+  uint32_t tmem_base;
+  int abort;
+};
+
+template <int D>
+constexpr size_t row_smem() {
+  return 1024 + size_t(2 + Cfg<D>::kRing) * Cfg<D>::kTileBytes + sizeof(RowBars) + 64;
+}
+static_assert(row_smem<128>() <= 232448 && row_smem<64>() <= 232448, "shared memory of a CTA");
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
+                   const __grid_constant__ CUtensorMap tmap_g,
+                   const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, Dense P, int items,
+                   const float* __restrict__ nl, const float* __restrict__ dl,
+                   __nv_bfloat16* __restrict__ dq, int* __restrict__ next_item,
+                   int* __restrict__ status) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* qbuf = smem;
+  uint8_t* gbuf = qbuf + C::kTileBytes;
+  uint8_t* kvbuf = gbuf + C::kTileBytes;     // [ring], K and V tiles in turn
+  RowBars* bars = reinterpret_cast<RowBars*>(kvbuf + C::kRing * C::kTileBytes);
+  volatile int* abort = &bars->abort;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    tc::mbar_init(&bars->q_full, 1);
+    tc::mbar_init(&bars->q_empty, 1);
+    for (int s = 0; s < C::kRing; ++s) {
+      tc::mbar_init(&bars->kv_full[s], 1);
+      tc::mbar_init(&bars->kv_empty[s], 1);
+    }
+    tc::mbar_init(&bars->s_full[0], 1);
+    tc::mbar_init(&bars->s_full[1], 1);
+    tc::mbar_init(&bars->dp_full, 1);
+    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->acc_full, 1);
+    tc::mbar_init(&bars->acc_empty, 8);
+    for (int i = 0; i < kItems; ++i) {
+      tc::mbar_init(&bars->i_full[i], 1);
+      tc::mbar_init(&bars->i_empty[i], 9);
+    }
+    tc::mbar_init(&bars->mma_done, 1);
+    bars->abort = 0;
+    tc::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tc::tma_prefetch(&tmap_q);
+    tc::tma_prefetch(&tmap_g);
+    tc::tma_prefetch(&tmap_k);
+    tc::tma_prefetch(&tmap_v);
+  }
+  if (warp == 1) tc::tmem_alloc(&bars->tmem_base, kTmemCols);
+  tc::tc_fence_before();
+  __syncthreads();
+  tc::tc_fence_after();
+  const uint32_t tmem = bars->tmem_base;
+  // S of even and of odd key tiles | dP | dQ
+  const uint32_t tp = tmem + 256, tq = tmem + 384;
+  bool failed = false;
+
+  if (warp == 0) {
+    // ---------------- producer ----------------
+    if (lane == 0) {
+      tc::ArmedRing q_armed, kv_armed;
+      int stage = 0;
+      uint32_t phase = 0;
+      int t = atomicAdd(next_item, 1);
+      for (int ii = 0; !failed; ++ii) {
+        const int slot = ii % kItems;
+        if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) {
+          failed = true;
+          break;
+        }
+        RowItem it{};
+        int k0 = 0;
+        if (t < items) {
+          int qt;
+          const SeqRec s = query_tile(P, t / P.Hq, &qt);
+          const int i0 = qt * kDenseTile;
+          it.live = 1;
+          it.rows = min(kDenseTile, s.nq - i0);
+          it.pos = s.pos0 + i0;
+          it.n = tiles_of(min(s.nk, it.pos + it.rows));
+          it.row0 = s.q0 + i0;
+          it.pad0 = s.qp0 + i0;
+          it.head = t % P.Hq;
+          it.nk = s.nk;
+          k0 = s.k0;
+        }
+        bars->item[slot] = it;
+        tc::mbar_arrive(&bars->i_full[slot]);
+        if (!it.live) break;
+        t = atomicAdd(next_item, 1);
+        const int g = it.head / P.G;
+        auto load = [&](const CUtensorMap* map, int row) -> bool {
+          if (!tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1, abort)) return false;
+          uint64_t* fb = &bars->kv_full[stage];
+          tc::mbar_arrive_expect_tx(fb, C::kTileBytes);
+          kv_armed.note(stage, phase);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(kvbuf + stage * C::kTileBytes + h * C::kHalf, map, fb, 64 * h, g, row);
+          if (++stage == C::kRing) { stage = 0; phase ^= 1; }
+          return true;
+        };
+        if (!tc::mbar_wait(&bars->q_empty, (ii & 1) ^ 1, abort)) { failed = true; break; }
+        tc::mbar_arrive_expect_tx(&bars->q_full, 2 * C::kTileBytes);
+        q_armed.note(0, ii & 1);
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+          tc::tma_load_3d(qbuf + h * C::kHalf, &tmap_q, &bars->q_full, 64 * h, it.head, it.row0);
+          tc::tma_load_3d(gbuf + h * C::kHalf, &tmap_g, &bars->q_full, 64 * h, it.head, it.row0);
+        }
+        bool good = true;
+        for (int j = 0; j < it.n && good; ++j)
+          good = load(&tmap_k, k0 + j * 128) && load(&tmap_v, k0 + j * 128);
+        failed = !good;
+      }
+      if (!(q_armed.drain(&bars->q_full) && kv_armed.drain(bars->kv_full))) failed = true;
+    }
+  } else if (warp == 1) {
+    // ---------------- MMA issuer ----------------
+    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
+      const bool ok = lane != 0 || tc::mbar_spin(bar, parity, abort);
+      return __shfl_sync(MSA_FULL_MASK, ok ? 1 : 0, 0) != 0;
+    };
+    long long n = 0;  // key tiles so far; tile x of K is load 2x of the ring, of V 2x + 1
+    for (int ii = 0; !failed; ++ii) {
+      const int slot = ii % kItems;
+      if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+      const RowItem it = bars->item[slot];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
+      if (!it.live) break;
+      const int seen = min(it.nk, it.pos + it.rows);
+      const uint32_t qa = tc::smem_addr(qbuf), ga = tc::smem_addr(gbuf);
+      auto stage_of = [&](long long load) { return int(load % C::kRing); };
+      auto par_of = [&](long long load) { return uint32_t((load / C::kRing) & 1); };
+      auto scores = [&](int j) -> bool {
+        const long long x = 2 * (n + j);
+        const int s = stage_of(x), keys = min(128, seen - j * 128);
+        if (!wait(&bars->kv_full[s], par_of(x))) return false;
+        uint8_t* k = kvbuf + s * C::kTileBytes;
+        if (keys & 15) zero_rows<D>(k, keys, (keys + 15) & ~15);
+        if (lane == 0) {
+          tc::tc_fence_after();
+          issue_nt<D>(tmem + uint32_t(j & 1) * 128, qa, tc::smem_addr(k));
+          tc::mma_commit(&bars->s_full[j & 1]);
+        }
+        return true;
+      };
+      auto products = [&](int j) -> bool {
+        const long long x = 2 * (n + j) + 1;
+        const int s = stage_of(x);
+        if (!wait(&bars->kv_full[s], par_of(x))) return false;
+        if (lane == 0) {
+          tc::tc_fence_after();
+          issue_nt<D>(tp, ga, tc::smem_addr(kvbuf + s * C::kTileBytes));
+          tc::mma_commit(&bars->dp_full);
+          tc::mma_commit(&bars->kv_empty[s]);
+        }
+        return true;
+      };
+      if (!wait(&bars->q_full, ii & 1) || !scores(0) || !products(0) ||
+          (it.n > 1 && !scores(1))) {
+        failed = true;
+        break;
+      }
+      for (int j = 0; j < it.n; ++j) {
+        if (!wait(&bars->ds_full, uint32_t((n + j) & 1)) ||
+            (j == 0 && !wait(&bars->acc_empty, (ii & 1) ^ 1))) {
+          failed = true;
+          break;
+        }
+        const int s = stage_of(2 * (n + j)), keys = min(128, seen - j * 128);
+        if (lane == 0) {
+          tc::tc_fence_after();
+          issue_ts<D>(tq, tp, tc::smem_addr(kvbuf + s * C::kTileBytes), (keys + 15) >> 4, j == 0);
+          tc::mma_commit(&bars->kv_empty[s]);
+        }
+        if ((j + 1 < it.n && !products(j + 1)) || (j + 2 < it.n && !scores(j + 2))) {
+          failed = true;
+          break;
+        }
+      }
+      if (failed) break;
+      if (lane == 0) {
+        tc::mma_commit(&bars->q_empty);
+        tc::mma_commit(&bars->acc_full);
+      }
+      n += it.n;
+    }
+    if (lane == 0 && !tc::mma_drain(&bars->mma_done)) failed = true;
+  } else if (warp >= 4) {
+    // ---------------- elementwise, then half of the tile's dQ columns ----------------
+    const int half = (warp - 4) >> 2, quarter = warp & 3;
+    const int row = quarter * 32 + lane;
+    const uint32_t lanes = uint32_t(quarter * 32) << 16;
+    const uint32_t pa = tp + lanes + half * 64;
+    const float sl2 = P.scale * kLog2e;
+    const uint64_t sl2x2 = f2(sl2, sl2);
+    long long n = 0;
+    int sn[2] = {0, 0};  // score tiles read of each buffer
+    for (int ii = 0; !failed; ++ii) {
+      const int slot = ii % kItems;
+      if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+      const RowItem it = bars->item[slot];
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
+      if (!it.live) break;
+      const bool mine = row < it.rows;
+      const long long at = (long long)it.head * P.rows_pad + it.pad0 + row;
+      const float nlse = mine ? nl[at] : -INFINITY, ndelta = mine ? -dl[at] : 0.f;
+      const uint64_t nl2 = f2(nlse, nlse), nd2 = f2(ndelta, ndelta);
+      for (int j = 0; j < it.n; ++j, ++n) {
+        const int b = j & 1;
+        const uint32_t sa = tmem + b * 128 + lanes + half * 64;
+        if (!warp_wait(&bars->s_full[b], sn[b] & 1, abort)) { failed = true; break; }
+        ++sn[b];
+        tc::tc_fence_after();
+        uint32_t p[2][32];
+        tc::tmem_ld32(sa, p[0]);
+        tc::tmem_ld32(sa + 32, p[1]);
+        tc::tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const uint64_t a = fma2(pair_of(&p[c][x]), sl2x2, nl2);
+            p[c][x] = __float_as_uint(ex2_f32(lo_of(a)));
+            p[c][x + 1] = __float_as_uint(ex2_f32(hi_of(a)));
+          }
+        if (!warp_wait(&bars->dp_full, uint32_t(n & 1), abort)) { failed = true; break; }
+        tc::tc_fence_after();
+        const int lim = it.pos + row - j * 128 - half * 64;  // last visible column of this half
+        const bool cut = __any_sync(MSA_FULL_MASK, lim < 63);
+        uint32_t w[32];
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          uint32_t d[32];
+          tc::tmem_ld32(pa + c * 32, d);
+          tc::tmem_ld_wait();
+#pragma unroll
+          for (int x = 0; x < 32; x += 2) {
+            const uint64_t y = mul2(pair_of(&p[c][x]), add2(pair_of(&d[x]), nd2));
+            d[x] = uint32_t(y);
+            d[x + 1] = uint32_t(y >> 32);
+          }
+          if (cut) {
+#pragma unroll
+            for (int x = 0; x < 32; ++x)
+              if (c * 32 + x > lim) d[x] = 0u;
+          }
+#pragma unroll
+          for (int x = 0; x < 32; x += 2)
+            w[c * 16 + x / 2] = pack_bf16(__uint_as_float(d[x]), __uint_as_float(d[x + 1]));
+        }
+        tc::tmem_st32(pa, w);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+      }
+      if (failed || !warp_wait(&bars->acc_full, ii & 1, abort)) { failed = true; break; }
+      tc::tc_fence_after();
+      __nv_bfloat16* dst = dq + ((long long)(it.row0 + row) * P.Hq + it.head) * D + half * (D / 2);
+#pragma unroll 1
+      for (int c = 0; c < D / 64; ++c) {
+        uint32_t o[32];
+        tc::tmem_ld32(tq + lanes + half * (D / 2) + c * 32, o);
+        tc::tmem_ld_wait();
+        if (mine) {
+          uint32_t w[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x)
+            w[x] = pack_bf16(__uint_as_float(o[2 * x]) * P.scale,
+                             __uint_as_float(o[2 * x + 1]) * P.scale);
+#pragma unroll
+          for (int x = 0; x < 16; x += 4)
+            *reinterpret_cast<uint4*>(dst + c * 32 + 2 * x) =
+                make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+        }
+      }
+      tc::tc_fence_before();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(&bars->acc_empty);
+    }
+  }
+  if (failed) {
+    bars->abort = 1;
+    atomicOr(status, tc::kStatusWaitTimeout);
+  }
+  tc::tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc::tc_fence_after();
+    tc::tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+template <int D>
+cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* k, const void* v,
+                   const void* out, const float* lse, const DenseBwdSpace& W, void* dq, void* dk,
+                   void* dv, int32_t* counters, int32_t* status, cudaStream_t s) {
+  using bf16 = __nv_bfloat16;
+  cudaError_t e = cudaSuccess;
+  const int splits = dense_bwd_splits(P);
+  const long long kelems = P.rows_k * P.Hkv * D;
+  if (P.rows_q == 0) {  // no row sees anything
+    e = cudaMemsetAsync(dk, 0, kelems * 2, s);
+    return e == cudaSuccess ? cudaMemsetAsync(dv, 0, kelems * 2, s) : e;
+  }
+  CUtensorMap mq, mg, mk, mv;
+  e = encode_rows(&mq, q, D, P.Hq, P.rows_q);
+  if (e == cudaSuccess) e = encode_rows(&mg, dout, D, P.Hq, P.rows_q);
+  if (e == cudaSuccess) e = encode_rows(&mk, k, D, P.Hkv, P.rows_k);
+  if (e == cudaSuccess) e = encode_rows(&mv, v, D, P.Hkv, P.rows_k);
+  auto dkv = splits > 1 ? dense_dkv_tc_kernel<D, true> : dense_dkv_tc_kernel<D, false>;
+  if (e == cudaSuccess) e = prepare_kernel(dkv, key_smem<D>(), 0, kThreads);
+  if (e == cudaSuccess) e = prepare_kernel(dense_dq_tc_kernel<D>, row_smem<D>(), 0, kThreads);
+  if (e != cudaSuccess) return e;
+  const long long warps = P.rows_pad / 16 * P.Hq;
+  dense_prep_kernel<D><<<unsigned((warps + 7) / 8), 256, 0, s>>>(
+      P, static_cast<const bf16*>(dout), static_cast<const bf16*>(out), lse, W.nl, W.dl);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int kitems = P.ktiles * P.Hkv * splits;
+  dkv<<<std::min(sm_count(), kitems), kThreads, key_smem<D>(), s>>>(
+      mq, mg, mk, mv, P, splits, kitems, W.nl, W.dl, static_cast<bf16*>(dk),
+      static_cast<bf16*>(dv), W.part, counters, status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (splits > 1) {
+    dense_dkv_sum_kernel<<<dim3(unsigned((kelems / 4 + 255) / 256), 2), 256, 0, s>>>(
+        W.part, splits, kelems, P.scale, static_cast<bf16*>(dk), static_cast<bf16*>(dv));
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  }
+  const int qitems = P.qtiles * P.Hq;
+  dense_dq_tc_kernel<D><<<std::min(sm_count(), qitems), kThreads, row_smem<D>(), s>>>(
+      mq, mg, mk, mv, P, qitems, W.nl, W.dl, static_cast<bf16*>(dq), counters + 1, status);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+// The heads of a group are split over several items where there would otherwise be
+// fewer than three items per SM to balance the load with; each split costs one more
+// write and read of dk and dv in fp32.
+int dense_bwd_splits(const Dense& P) {
+  int n = 1;
+  while (n < P.G && (long long)P.ktiles * P.Hkv * n < 3LL * 148) n *= 2;
+  return std::min(n, P.G);
+}
+
+cudaError_t launch_dense_bwd_tc(const Dense& P, const void* dout, const void* q, const void* k,
+                                const void* v, const void* out, const float* lse,
+                                const DenseBwdSpace& W, void* dq, void* dk, void* dv,
+                                int32_t* counters, int32_t* status, cudaStream_t s) {
+  return (P.D == 128 ? bwd_tc<128> : bwd_tc<64>)(P, dout, q, k, v, out, lse, W, dq, dk, dv,
+                                                 counters, status, s);
+}
+
+}  // namespace msa

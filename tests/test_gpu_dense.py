@@ -167,7 +167,7 @@ def test_same_bits_again_on_other_streams_and_in_used_workspaces():
     want = msa.dense_attend_varlen(q, k, v, cu, cu, return_lse=True)
     want += msa.dense_backward_varlen(dout, q, k, v, *want, cu, cu)
     torch.cuda.synchronize()
-    ws = torch.full((1 << 22,), 0xff, dtype=torch.uint8, device="cuda")
+    ws = torch.full((1 << 25,), 0xff, dtype=torch.uint8, device="cuda")
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
