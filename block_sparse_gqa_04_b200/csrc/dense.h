@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include "../../include/msa.h"
+#include "internal.h"
 
 namespace msa {
 
@@ -50,6 +51,7 @@ struct Tree {
   const int32_t* kv_lens;
   int rows;              // (node, head) rows of one work unit
   int groups;            // units per (sequence, key head)
+  uint4* bits;           // tensor cores: the masks as bits, [masks, nodes + 1]
   float* part_o;         // [2 * CTAs, rows, D] unnormalised partial outputs
   float2* part_ml;       // [2 * CTAs, rows] base-2 running maximum and sum
 };
@@ -82,11 +84,16 @@ cudaError_t launch_dense_bwd_simt(const Dense& P, const void* dout, const void* 
                                   void* dq, void* dk, void* dv, cudaStream_t s);
 
 constexpr int kSimtTreeRows = 64;  // rows of a work unit on the CUDA cores
+constexpr int kTcTreeRows = 128;   // and on the tensor cores
 int tree_ctas();                   // CTAs of a tree launch: one per SM
 // Joins the partial states (second launch of either tree kernel).
 cudaError_t launch_tree_combine(const Tree& T, void* out, float* lse, cudaStream_t s);
 cudaError_t launch_tree_simt(const Tree& T, const void* q, const void* k, const void* v, void* out,
                              float* lse, int32_t* status, cudaStream_t s);
+
+// Clears the status word itself.
+cudaError_t launch_tree_tc(const Tree& T, const void* q, const void* k, const void* v, void* out,
+                           float* lse, int32_t* status, cudaStream_t s);
 
 struct NormRope {
   long long rows;

@@ -200,7 +200,7 @@ msa_status_t resolve_tree(const msa_problem_t* p, Tree* T) {
   msa_status_t st = resolve_batched(&c, &T->d);
   if (st != MSA_OK) return st;
   if (p->q_len > kMaxNodes || T->d.G > 128) return MSA_ERR_UNSUPPORTED;
-  T->rows = msa::kSimtTreeRows;
+  T->rows = T->d.f32 ? msa::kSimtTreeRows : msa::kTcTreeRows;
   T->groups = (T->d.Sq * T->d.G + T->rows - 1) / T->rows;
   if ((long long)T->d.B * T->d.Hkv * T->groups * T->rows / 8 >= (1LL << 31) ||
       (long long)T->d.B * T->d.Hkv * T->groups >= (1LL << 31))
@@ -209,7 +209,7 @@ msa_status_t resolve_tree(const msa_problem_t* p, Tree* T) {
 }
 
 struct TreeLayout {
-  size_t status, part_o, part_ml, total;
+  size_t status, bits, part_o, part_ml, total;
 };
 
 TreeLayout tree_layout(const Tree& T) {
@@ -218,6 +218,7 @@ TreeLayout tree_layout(const Tree& T) {
   auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
   const size_t rows = size_t(msa::tree_ctas()) * 2 * T.rows;
   L.status = take(sizeof(int32_t));
+  if (!T.d.f32) L.bits = take(size_t(T.d.B) * (T.d.Sq + 1) * sizeof(uint4));
   L.part_o = take(rows * T.d.D * sizeof(float));
   L.part_ml = take(rows * sizeof(float2));
   L.total = off;
@@ -329,13 +330,15 @@ msa_status_t msa_tree_attend(const msa_problem_t* p, const void* q, const void* 
   T.mask = tree_mask;
   T.mask_stride = mask_batch_stride;
   T.kv_lens = kv_lens;
+  T.bits = at<uint4>(ws, L.bits);
   T.part_o = at<float>(ws, L.part_o);
   T.part_ml = at<float2>(ws, L.part_ml);
   cudaStream_t s = (cudaStream_t)stream;
-  cudaError_t e = cudaMemsetAsync(ws, 0, sizeof(int32_t), s);
-  if (e == cudaSuccess) e = msa::launch_dense_check_table(T.d, at<int32_t>(ws, L.status), s);
-  if (e == cudaSuccess)
-    e = msa::launch_tree_simt(T, q, k, v, out, lse_opt, at<int32_t>(ws, L.status), s);
+  int32_t* status = at<int32_t>(ws, L.status);
+  if (!T.d.f32)
+    return msa::status_of(msa::launch_tree_tc(T, q, k, v, out, lse_opt, status, s));
+  cudaError_t e = cudaMemsetAsync(status, 0, sizeof(int32_t), s);
+  if (e == cudaSuccess) e = msa::launch_tree_simt(T, q, k, v, out, lse_opt, status, s);
   return msa::status_of(e);
 }
 

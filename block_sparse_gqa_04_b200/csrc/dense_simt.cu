@@ -448,7 +448,12 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
     R.clear();
     const int total = p.len + nodes;
     for (int j0 = p.kt0 * kDenseTile; j0 < min(total, p.kt1 * kDenseTile); j0 += kTile) {
-      const long long row = tile_row(P, p.b, P.table ? 0 : p.b * P.Skv, j0 / kDenseTile) + (j0 % kDenseTile);
+      const long long row =
+          tile_row(P, p.b, P.table ? 0 : p.b * P.Skv, j0 / kDenseTile) + (j0 % kDenseTile);
+      if (P.table && threadIdx.x == 0) {
+        const int pg = P.table[(long long)p.b * P.table_w + j0 / kDenseTile];
+        if (pg < 0 || pg >= P.pages) atomicOr(status, kStatusBadPage);
+      }
       const int valid = min(kTile, total - j0);
       const bool drafts = j0 + kTile > p.len;  // the tile reaches the drafted tokens
       __syncthreads();

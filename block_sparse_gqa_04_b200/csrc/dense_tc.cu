@@ -454,6 +454,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
+          __syncwarp();
           tc::tmem_ld32(ot + c * 32, o);
           tc::tmem_ld_wait();
           if (c == D / 32 - 1) {

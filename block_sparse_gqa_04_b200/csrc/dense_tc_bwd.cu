@@ -469,6 +469,7 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
+        __syncwarp();
         if (any) {
           tc::tmem_ld32(acc + c * 32, o);
           tc::tmem_ld_wait();
@@ -823,6 +824,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll 1
       for (int c = 0; c < D / 64; ++c) {
         uint32_t o[32];
+        __syncwarp();
         tc::tmem_ld32(tq + lanes + half * (D / 2) + c * 32, o);
         tc::tmem_ld_wait();
         if (mine) {

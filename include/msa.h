@@ -321,7 +321,8 @@ size_t msa_dense_workspace_size(const msa_problem_t* p, const int32_t* cu_seqlen
  * sees are never part of a result, whatever they hold; a drafted token that some
  * nodes see and others do not must hold finite v.
  * q, out [batch, q_len, num_q_heads, head_dim]; lse_opt [batch, q_len, num_q_heads].
- * kv_lens[b] outside [0, kv_len - q_len] is clamped and sets status bit 8.
+ * kv_lens[b] outside [0, kv_len - q_len] is clamped and sets status bit 8; entries of
+ * block_table behind a sequence's last token are not looked at.
  * At most 128 heads per group.  Workspace: msa_tree_workspace_size(p) bytes, the
  * same for all kv_lens, so a captured call can be replayed with other lengths. */
 msa_status_t msa_tree_attend(const msa_problem_t* p, const void* q, const void* k, const void* v,

@@ -141,6 +141,34 @@ def test_lengths_outside_the_cache_are_flagged_and_clamped():
     assert torch.equal(got, want)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_pages_that_are_read_are_checked_and_no_others(dtype):
+    q = randn((2, 2, 4, 64), dtype, 1)
+    pk, pv = randn((5, 128, 2, 64), dtype, 2), randn((5, 128, 2, 64), dtype, 3)
+    mask = torch.ones((2, 2), dtype=torch.bool, device="cuda").tril()
+    lens = torch.tensor([100, 300], dtype=torch.int32, device="cuda")
+    table = torch.tensor([[3, 9, -7], [4, 0, 1]], dtype=torch.int32, device="cuda")
+    kw = dict(block_table=table, kv_len=384, return_lse=True)
+    got = msa.tree_attend(q, pk, pv, mask, lens, check_device_status=True, **kw)
+    for i, pages in enumerate(([3], [4, 0, 1])):
+        k, v = (x[pages].flatten(0, 1)[None] for x in (pk, pv))
+        want = msa.tree_attend(q[i:i + 1], k, v, mask, lens[i:i + 1], return_lse=True)
+        r = D.tree_attend(q[i], k[0], v[0], mask.cpu().numpy(), int(lens[i]))
+        f = weight_error(q[i], k[0][:int(lens[i]) + 2])
+        check_forward(got[0][i], got[1][i], r, f, dtype)
+        check_forward(want[0][0], want[1][0], r, f, dtype)
+    for bad in (5, -1):
+        table[1, 2] = bad
+        with pytest.raises(msa.MsaError, match="MSA_ERR_DEVICE"):
+            msa.tree_attend(q, pk, pv, mask, lens, check_device_status=True, **kw)
+        # a page outside the pool reads as page 0
+        table[1, 2] = 0
+        want = msa.tree_attend(q, pk, pv, mask, lens, **kw)
+        table[1, 2] = bad
+        assert all(torch.equal(a, b) for a, b in
+                   zip(want, msa.tree_attend(q, pk, pv, mask, lens, **kw)))
+
+
 def test_captured_and_replayed_with_growing_lengths():
     """One captured call serves every later step: lengths, mask and cache are read when
     it runs.  Two graphs share one workspace."""
