@@ -14,11 +14,10 @@
 // TMEM, is then scaled by the softmax warps; otherwise P just exceeds 1, which fp32
 // sums and a bf16 P carry with the same relative error.
 //
-// Each tile of the pair has its own TMEM columns (S|P 128, O), softmax warpgroup
-// and MMA-issuing thread, so one tile's MMAs run while the other is in its softmax.
-// A fourth warpgroup normalises and stores the finished tiles.  K and V tiles pass
-// through a ring of TMA stages; a stage is free again once both issuers have
-// committed past it.
+// Each tile of the pair has its own TMEM columns (S|P 128, O) and softmax warpgroup;
+// one thread issues the MMAs of both in turn, so one tile's MMAs run while the other is
+// in its softmax.  A fourth warpgroup normalises and stores the finished tiles.  K and V
+// tiles pass through a ring of TMA stages.
 //
 // Tokens behind the last key of a sequence (the next sequence's, or an unused part
 // of a page) come in with its last tile.  Their scores are cut by the causal mask;
@@ -32,10 +31,10 @@
 namespace msa {
 namespace {
 
-// warp 0 items and TMA, warps 1-2 MMA, warp 3 idle, warps 4-11 softmax, 12-15 epilogue
+// warp 0 items and TMA, warp 1 MMA, warp 2 waits for it, warp 3 idle, warps 4-11 softmax, 12-15 epilogue
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kItems = 2;     // items in flight
+constexpr int kItems = 3;     // items in flight
 constexpr float kSlack = 8.f;
 // 96 + 64 + 2 x 176 = 512 = 4 x 128: the registers the CTA is launched with
 constexpr int kRegsCtl = 96, kRegsEpi = 64, kRegsSoftmax = 176;
@@ -44,7 +43,7 @@ template <int D>
 struct Cfg {
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kHalf = 128 * 64 * 2;            // 64 dims of 128 rows
-  static constexpr int kStages = D == 128 ? 5 : 8;
+  static constexpr int kPairs = D == 128 ? 2 : 4;       // stages of a V and a K tile
   static constexpr uint32_t kIdescS = tc::idesc_bf16_f32(128, 128, 0, 0);
   static constexpr uint32_t kIdescO = tc::idesc_bf16_f32(128, D, 0, 1);  // V is MN-major
 };
@@ -62,10 +61,11 @@ struct Item {
 
 struct Bars {
   uint64_t q_full[2], q_empty[2];
-  uint64_t kv_full[8], kv_empty[8];
-  // per query tile: S computed, P written, each P V done, the tile's last P V done,
-  // O read by the epilogue, sums written, sums read
-  uint64_t s_full[2], p_full[2], o_step[2], o_done[2], o_empty[2], l_full[2], l_empty[2];
+  uint64_t k0_full;                     // the CTA's first K tile
+  uint64_t vk_full[4], vk_empty[4];     // a V tile and the K tile after it
+  // per query tile: S computed, P written (and what its products need is there), the
+  // tile's last P V done, O read by the epilogue, sums written, sums read
+  uint64_t s_full[2], p_full[2], o_done[2], o_empty[2], l_full[2], l_empty[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint64_t mma_done;
   Item item[kItems];
@@ -76,7 +76,7 @@ struct Bars {
 
 template <int D>
 constexpr size_t smem_bytes() {
-  return 1024 + size_t(2 + Cfg<D>::kStages) * Cfg<D>::kTileBytes + sizeof(Bars) + 64;
+  return 1024 + size_t(3 + 2 * Cfg<D>::kPairs) * Cfg<D>::kTileBytes + sizeof(Bars) + 64;
 }
 static_assert(smem_bytes<128>() <= 232448 && smem_bytes<64>() <= 232448, "shared memory of a CTA");
 
@@ -125,22 +125,23 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;                          // [2]
-  uint8_t* kvbuf = qbuf + 2 * C::kTileBytes;     // [stages], K and V tiles in turn
-  Bars* bars = reinterpret_cast<Bars*>(kvbuf + C::kStages * C::kTileBytes);
+  uint8_t* k0buf = qbuf + 2 * C::kTileBytes;
+  uint8_t* vkbuf = k0buf + C::kTileBytes;        // [pairs][V, K]
+  Bars* bars = reinterpret_cast<Bars*>(vkbuf + C::kPairs * 2 * C::kTileBytes);
   volatile int* abort = &bars->abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < C::kStages; ++s) {
-      tc::mbar_init(&bars->kv_full[s], 1);
-      tc::mbar_init(&bars->kv_empty[s], 2);  // both MMA issuers
+    tc::mbar_init(&bars->k0_full, 1);
+    for (int s = 0; s < C::kPairs; ++s) {
+      tc::mbar_init(&bars->vk_full[s], 1);
+      tc::mbar_init(&bars->vk_empty[s], 1);
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&bars->q_full[b], 1);
       tc::mbar_init(&bars->q_empty[b], 1);
       tc::mbar_init(&bars->s_full[b], 1);
-      tc::mbar_init(&bars->p_full[b], 4);    // the tile's softmax warps
-      tc::mbar_init(&bars->o_step[b], 1);
+      tc::mbar_init(&bars->p_full[b], 5);    // the tile's softmax warps and warp 2
       tc::mbar_init(&bars->o_done[b], 1);
       tc::mbar_init(&bars->o_empty[b], 4);   // the epilogue warps
       tc::mbar_init(&bars->l_full[b], 4);
@@ -148,9 +149,9 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     for (int i = 0; i < kItems; ++i) {
       tc::mbar_init(&bars->i_full[i], 1);
-      tc::mbar_init(&bars->i_empty[i], 14);  // 2 MMA, 8 softmax, 4 epilogue warps
+      tc::mbar_init(&bars->i_empty[i], 14);  // warps 1, 2, softmax, epilogue
     }
-    tc::mbar_init(&bars->mma_done, 2);
+    tc::mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
     tc::fence_mbar_init();
   }
@@ -171,145 +172,233 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (warp == 0) {
       // ---------------- producer: items and TMA ----------------
       if (lane == 0) {
-        tc::ArmedRing q_armed, kv_armed;
+        tc::ArmedRing q_armed, vk_armed;
+        bool k0_armed = false;
         int stage = 0, qn[2] = {0, 0};
         uint32_t phase = 0;
-        int t = atomicAdd(next_item, 1);
-        for (int ii = 0; !failed; ++ii) {
-          const int slot = ii % kItems;
-          if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) {
-            failed = true;
-            break;
-          }
-          Item& it = bars->item[slot];
-          int b = 0, k0 = 0, g = 0;
-          if (t < P.pairs) make_item(P, t, &it, &b, &k0, &g);
-          else it.live = 0;
-          const int live = it.live, n = live ? it.n : 0;
+        struct Where {
+          int live, n, b, k0, g;
           int nkt[2], head[2], row0[2];
+        } cur, nxt;
+        int ii = 0;  // items
+        // the next item to the other warps, and what the copies need of it
+        auto publish = [&](Where* w) -> bool {
+          const int t = atomicAdd(next_item, 1), slot = ii % kItems;
+          if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) return false;
+          ++ii;
+          Item& it = bars->item[slot];
+          w->live = t < P.pairs;
+          it.live = w->live;
+          if (w->live) {
+            make_item(P, t, &it, &w->b, &w->k0, &w->g);
+            w->n = it.n;
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            nkt[e] = it.nkt[e];
-            head[e] = it.head[e];
-            row0[e] = it.row0[e];
+            for (int e = 0; e < 2; ++e) {
+              w->nkt[e] = it.nkt[e];
+              w->head[e] = it.head[e];
+              w->row0[e] = it.row0[e];
+            }
           }
           tc::mbar_arrive(&bars->i_full[slot]);
-          if (!live) break;
-          t = atomicAdd(next_item, 1);  // the next one, on its way during this item's copies
-          auto load = [&](const CUtensorMap* map, int row) -> bool {
-            if (!tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1, abort)) return false;
-            uint64_t* fb = &bars->kv_full[stage];
-            uint8_t* dst = kvbuf + stage * C::kTileBytes;
-            tc::mbar_arrive_expect_tx(fb, C::kTileBytes);
-            kv_armed.note(stage, phase);
+          return true;
+        };
+        auto copy = [&](const CUtensorMap* map, uint8_t* dst, uint64_t* bar, const Where& w, int j) {
+          const int row = int(tile_row(P, w.b, w.k0, j));
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              tc::tma_load_3d(dst + h * C::kHalf, map, fb, 64 * h, g, row);
-            if (++stage == C::kStages) { stage = 0; phase ^= 1; }
-            return true;
-          };
-          auto load_q = [&](int e) -> bool {
-            if (nkt[e] == 0) return true;
-            if (!tc::mbar_wait(&bars->q_empty[e], (qn[e] & 1) ^ 1, abort)) return false;
-            tc::mbar_arrive_expect_tx(&bars->q_full[e], C::kTileBytes);
-            q_armed.note(e, qn[e] & 1);
-            ++qn[e];
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(dst + h * C::kHalf, map, bar, 64 * h, w.g, row);
+        };
+        failed = !publish(&cur);
+        bool start = true;
+        while (!failed && cur.live) {
 #pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              tc::tma_load_3d(qbuf + e * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[e],
-                              64 * h, head[e], row0[e]);
-            return true;
-          };
-          bool good = true;
-          for (int j = 0; j < n && good; ++j) {
-            const int row = int(tile_row(P, b, k0, j));
-            if (j == 0) good = load_q(0);
-            good = good && load(&tmap_k, row);
-            if (j == 0) good = good && load_q(1);
-            good = good && load(&tmap_v, row);
+          for (int e = 0; e < 2; ++e) {
+            if (cur.nkt[e] > 0 && !failed) {
+              if (!tc::mbar_wait(&bars->q_empty[e], (qn[e] & 1) ^ 1, abort)) { failed = true; break; }
+              tc::mbar_arrive_expect_tx(&bars->q_full[e], C::kTileBytes);
+              q_armed.note(e, qn[e] & 1);
+              ++qn[e];
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tc::tma_load_3d(qbuf + e * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[e],
+                                64 * h, cur.head[e], cur.row0[e]);
+            }
+            if (e == 0 && start) {
+              tc::mbar_arrive_expect_tx(&bars->k0_full, C::kTileBytes);
+              k0_armed = true;
+              copy(&tmap_k, k0buf, &bars->k0_full, cur, 0);
+              start = false;
+            }
           }
-          failed = !good;
+          if (failed || !publish(&nxt)) { failed = true; break; }
+          for (int j = 0; j < cur.n; ++j) {
+            if (!tc::mbar_wait(&bars->vk_empty[stage], phase ^ 1, abort)) { failed = true; break; }
+            const bool more = j + 1 < cur.n || nxt.live;
+            uint64_t* fb = &bars->vk_full[stage];
+            uint8_t* dst = vkbuf + stage * 2 * C::kTileBytes;
+            tc::mbar_arrive_expect_tx(fb, (more ? 2 : 1) * C::kTileBytes);
+            vk_armed.note(stage, phase);
+            copy(&tmap_v, dst, fb, cur, j);
+            if (more)
+              copy(&tmap_k, dst + C::kTileBytes, fb, j + 1 < cur.n ? cur : nxt,
+                   j + 1 < cur.n ? j + 1 : 0);
+            if (++stage == C::kPairs) { stage = 0; phase ^= 1; }
+          }
+          cur = nxt;
         }
         // every copy issued has landed before the CTA can leave
-        if (!(q_armed.drain(bars->q_full) && kv_armed.drain(bars->kv_full))) failed = true;
+        if (k0_armed && !tc::mbar_drain(&bars->k0_full, 0)) failed = true;
+        if (!(q_armed.drain(bars->q_full) && vk_armed.drain(bars->vk_full))) failed = true;
       }
-    } else if (warp < 3) {
-      // ---------------- MMA issuer of query tile e ----------------
-      const int e = warp - 1;
-      const uint32_t st = tmem + e * 256, ot = st + 128;
-      int stage = 0, qn = 0, on = 0;   // ring position; items and key tiles of this tile so far
-      uint32_t phase = 0;
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool ok = lane != 0 || tc::mbar_spin(bar, parity, abort);
-        return __shfl_sync(MSA_FULL_MASK, ok ? 1 : 0, 0) != 0;
-      };
-      for (int ii = 0; !failed; ++ii) {
+    } else if (warp == 1) {
+      // ---------------- MMA issuer ----------------
+      // In the fixed order P V of tile 0, its next S, P V of tile 1, its next S (the next
+      // item's first S at an item's end): the two tiles stay half a step apart, each in
+      // its softmax while the other's products run.  The pipe queues one instruction
+      // only, so whatever this thread waits for or does between them shows: it waits for
+      // one barrier per pair of products, which warp 2 completes once all else that they
+      // need is there.
+      if (lane == 0) {
+        int ii = 0;               // items
+        int ps = 0;               // stage
+        uint32_t pp = 0;
+        uint32_t qn[2] = {0, 0}, on[2] = {0, 0};  // items, key tiles of each query tile so far
+        // descriptors of the first rows; a step of 16 columns or rows is a constant
+        const uint64_t qd = tc::sdesc_sw128(tc::smem_addr(qbuf), 16, 1024);
+        const uint64_t k0d = tc::sdesc_sw128(tc::smem_addr(k0buf), 16, 1024);
+        const uint64_t kd = tc::sdesc_sw128(tc::smem_addr(vkbuf + C::kTileBytes), 16, 1024);
+        const uint64_t vd = tc::sdesc_sw128(tc::smem_addr(vkbuf), C::kHalf, 1024);
+        constexpr uint32_t kTile16 = C::kTileBytes / 16, kHalf16 = C::kHalf / 16;
+        auto fetch = [&](Item* it) -> bool {
+          const int slot = ii % kItems;
+          if (!tc::mbar_spin(&bars->i_full[slot], (ii++ / kItems) & 1, abort)) return false;
+          *it = bars->item[slot];
+          tc::mbar_arrive(&bars->i_empty[slot]);
+          return true;
+        };
+        // S of query tile e
+        auto scores = [&](int e, uint64_t b, bool last) {
+          const uint64_t a = qd + e * kTile16;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
+            tc::mma_ss(tmem + e * 256, a + off, b + off, C::kIdescS, kk > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&bars->s_full[e]);
+          if (last) tc::mma_commit(&bars->q_empty[e]);
+        };
+        Item cur{};
+        failed = !fetch(&cur);
+        if (!failed && cur.live) {
+          failed = !tc::mbar_spin(&bars->k0_full, 0, abort);
+#pragma unroll
+          for (int e = 0; e < 2; ++e)
+            if (cur.nkt[e] > 0 && !failed) {
+              failed = !tc::mbar_spin(&bars->q_full[e], qn[e]++ & 1, abort);
+              tc::tc_fence_after();
+              if (!failed) scores(e, k0d, cur.nkt[e] == 1);
+            }
+        }
+        while (!failed && cur.live) {
+          const int nkt[2] = {cur.nkt[0], cur.nkt[1]}, n = cur.n;
+          int seen[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) seen[e] = min(cur.nk, cur.pos[e] + cur.rows[e]);
+          for (int j = 0; j < n && !failed; ++j) {
+            const bool end = j == n - 1;
+            if (end && !fetch(&cur)) { failed = true; break; }
+            const uint64_t v = vd + ps * 2 * kTile16, k = kd + ps * 2 * kTile16;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t st = tmem + e * 256;
+              const int left = end ? (cur.live ? cur.nkt[e] : 0) : nkt[e] - j - 1;
+              if (j < nkt[e]) {
+                if (!tc::mbar_spin(&bars->p_full[e], on[e]++ & 1, abort)) { failed = true; break; }
+                tc::tc_fence_after();
+                const int groups = (min(128, seen[e] - j * 128) + 15) >> 4;
+                if (groups == 8) {
+#pragma unroll
+                  for (int kk = 0; kk < 8; ++kk)
+                    tc::mma_ts(st + 128, st + kk * 8, v + kk * 128, C::kIdescO,
+                               (kk > 0 || j > 0) ? 1u : 0u);
+                } else {
+#pragma unroll 1
+                  for (int kk = 0; kk < groups; ++kk)
+                    tc::mma_ts(st + 128, st + kk * 8, v + kk * 128, C::kIdescO,
+                               (kk > 0 || j > 0) ? 1u : 0u);
+                }
+                if (j == nkt[e] - 1) tc::mma_commit(&bars->o_done[e]);
+              } else if (left > 0) {  // only scores: this tile's products were shorter
+                if (!tc::mbar_spin(&bars->vk_full[ps], pp, abort) ||
+                    !tc::mbar_spin(&bars->q_full[e], qn[e] & 1, abort)) {
+                  failed = true;
+                  break;
+                }
+                tc::tc_fence_after();
+              }
+              if (left > 0) {
+                if (end) ++qn[e];
+                scores(e, k, left == 1);
+              }
+            }
+            tc::mma_commit(&bars->vk_empty[ps]);
+            if (++ps == C::kPairs) { ps = 0; pp ^= 1; }
+          }
+        }
+        // every MMA issued has completed before TMEM is freed
+        if (!tc::mma_drain(&bars->mma_done)) failed = true;
+      }
+    } else if (warp == 2) {
+      // ---------------- what else the products need ----------------
+      // Per key tile and query tile, one arrival at p_full: the V tile and the K tile
+      // after it have landed (V's rows behind the last key zeroed), the epilogue has read
+      // the previous O, the next item's Q has landed.
+      int ii = 0, ps = 0;
+      uint32_t pp = 0;
+      uint32_t qn[2] = {0, 0}, on[2] = {0, 0}, in[2] = {0, 0};  // Q tiles, key tiles, items
+      auto fetch = [&](Item* it) -> bool {
         const int slot = ii % kItems;
-        if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
-        const Item& it = bars->item[slot];
-        const int live = it.live, n = it.n, nkt = it.nkt[e], nk = it.nk;
-        const int seen = it.pos[e] + it.rows[e];  // keys that the tile's last row sees
+        if (!warp_wait(&bars->i_full[slot], (ii++ / kItems) & 1, abort)) return false;
+        *it = bars->item[slot];
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
-        if (!live) break;
-        for (int j = 0; j < n; ++j) {
-          const int ks = stage;
-          const uint32_t kp = phase;
-          if (++stage == C::kStages) { stage = 0; phase ^= 1; }
-          const int vs = stage;
-          const uint32_t vp = phase;
-          if (++stage == C::kStages) { stage = 0; phase ^= 1; }
-          if (!wait(&bars->kv_full[ks], kp)) { failed = true; break; }
-          if (j >= nkt) {  // the other tile's keys: hand the stages back
-            if (!wait(&bars->kv_full[vs], vp)) { failed = true; break; }
-            if (lane == 0) {
-              tc::mbar_arrive(&bars->kv_empty[ks]);
-              tc::mbar_arrive(&bars->kv_empty[vs]);
-            }
-            continue;
-          }
-          if (j == 0 && !wait(&bars->q_full[e], qn & 1)) { failed = true; break; }
-          if (lane == 0) {
-            tc::tc_fence_after();
-            const uint32_t qa = tc::smem_addr(qbuf + e * C::kTileBytes);
-            const uint32_t ka = tc::smem_addr(kvbuf + ks * C::kTileBytes);
+        return true;
+      };
+      Item cur{}, nxt{};
+      failed = !fetch(&cur);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-              tc::mma_ss(st, tc::sdesc_sw128(qa + off, 16, 1024),
-                         tc::sdesc_sw128(ka + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
+      for (int e = 0; e < 2; ++e) qn[e] = !failed && cur.live && cur.nkt[e] > 0;
+      while (!failed && cur.live) {
+        int all = 0;  // keys that some row of the item sees
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+          if (cur.nkt[e] > 0) all = max(all, min(cur.nk, cur.pos[e] + cur.rows[e]));
+        for (int j = 0; j < cur.n && !failed; ++j) {
+          const bool end = j == cur.n - 1;
+          if (end && !fetch(&nxt)) { failed = true; break; }
+          if (!warp_wait(&bars->vk_full[ps], pp, abort)) { failed = true; break; }
+          const int keys = min(128, all - j * 128);
+          if (keys & 15) zero_rows<D>(vkbuf + ps * 2 * C::kTileBytes, keys, (keys + 15) & ~15);
+          if (++ps == C::kPairs) { ps = 0; pp ^= 1; }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const bool follow = end && nxt.live && nxt.nkt[e] > 0;
+            if (j < cur.nkt[e] && !failed) {
+              // the arrival belongs to the phase of this key tile: the one before is over
+              if ((on[e] > 0 && !warp_wait(&bars->p_full[e], (on[e] & 1) ^ 1, abort)) ||
+                  (j == 0 && !warp_wait(&bars->o_empty[e], (in[e]++ & 1) ^ 1, abort)) ||
+                  (follow && !warp_wait(&bars->q_full[e], qn[e] & 1, abort))) {
+                failed = true;
+                break;
+              }
+              ++on[e];
+              if (lane == 0) tc::mbar_arrive(&bars->p_full[e]);
             }
-            tc::mma_commit(&bars->s_full[e]);
-            tc::mma_commit(&bars->kv_empty[ks]);
-            if (j == nkt - 1) tc::mma_commit(&bars->q_empty[e]);
+            if (follow) ++qn[e];
           }
-          // P V over the keys that exist and that some row of the tile sees
-          const int keys = min(128, min(nk, seen) - j * 128);
-          if (!wait(&bars->kv_full[vs], vp)) { failed = true; break; }
-          const uint32_t va = tc::smem_addr(kvbuf + vs * C::kTileBytes);
-          if (keys & 15)
-            zero_rows<D>(kvbuf + vs * C::kTileBytes, keys, (keys + 15) & ~15);
-          if (!wait(&bars->p_full[e], on & 1) ||
-              (j == 0 && !wait(&bars->o_empty[e], (qn & 1) ^ 1))) {
-            failed = true;
-            break;
-          }
-          if (lane == 0) {
-            tc::tc_fence_after();
-            const int groups = (keys + 15) >> 4;
-            for (int kk = 0; kk < groups; ++kk)
-              tc::mma_ts(ot, st + kk * 8, tc::sdesc_sw128(va + kk * 2048, C::kHalf, 1024),
-                         C::kIdescO, (j > 0 || kk > 0) ? 1u : 0u);
-            tc::mma_commit(&bars->kv_empty[vs]);
-            tc::mma_commit(&bars->o_step[e]);
-            if (j == nkt - 1) tc::mma_commit(&bars->o_done[e]);
-          }
-          ++on;
         }
-        if (nkt > 0) ++qn;
+        cur = nxt;
       }
-      // every MMA issued has completed before TMEM is freed
-      if (lane == 0 && !tc::mma_drain(&bars->mma_done)) failed = true;
     }
   } else if (warp < 12) {
     // ---------------- softmax of query tile e ----------------
@@ -381,9 +470,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           }
         }
         if (j > 0 && __any_sync(MSA_FULL_MASK, grow)) {
-          // the tile's previous P V has written O: scale it
-          if (!warp_wait(&bars->o_step[e], (on & 1) ^ 1, abort)) { failed = true; break; }
-          tc::tc_fence_after();
+          // the previous P V was issued before this S: O is there; scale it
           const uint64_t k2 = f2(keep, keep);
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {

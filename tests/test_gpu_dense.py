@@ -29,6 +29,8 @@ BATCHED = [
     (2, 257, 257, 0, 10, 2, 64),      # an odd number of heads per group
     (1, 300, 520, 220, 16, 1, 128),
     (1, 385, 640, 0, 3, 1, 128),      # whole key tiles that no row sees
+    (2, 290, 341, 45, 3, 1, 64),      # pairs of tiles that end inside different key groups
+    (1, 300, 555, 241, 5, 5, 128),
 ]
 
 
@@ -49,6 +51,7 @@ PACKED = {
     "empty_ones": ([0, 33, 0, 7, 0], [0, 33, 150, 7, 0], 6, 2, 64),
     "equal": ([96, 96, 96], [96, 96, 96], 16, 1, 128),
     "many": ([3] * 150, [4] * 150, 2, 1, 64),       # more than one launch's records
+    "odd_groups": ([200, 131, 300], [233, 131, 411], 6, 2, 128),
     "one": ([260], [260], 12, 4, 128),
 }
 
