@@ -258,16 +258,15 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // only, so whatever this thread waits for or does between them shows: it waits for
       // one barrier per pair of products, which warp 2 completes once all else that they
       // need is there.
-      if (lane == 0) {
-        int ii = 0;               // items
-        int ps = 0;               // stage
-        uint32_t pp = 0;
-        uint32_t qn[2] = {0, 0}, on[2] = {0, 0};  // items, key tiles of each query tile so far
-        // descriptors of the first rows; a step of 16 columns or rows is a constant
-        const uint64_t qd = tc::sdesc_sw128(tc::smem_addr(qbuf), 16, 1024);
-        const uint64_t k0d = tc::sdesc_sw128(tc::smem_addr(k0buf), 16, 1024);
-        const uint64_t kd = tc::sdesc_sw128(tc::smem_addr(vkbuf + C::kTileBytes), 16, 1024);
-        const uint64_t vd = tc::sdesc_sw128(tc::smem_addr(vkbuf), C::kHalf, 1024);
+      if (tc::elect_one()) {
+        int ii = 0, ps = 0;                  // items, stage
+        uint32_t pp = 0, qpar = 0, ppar = 0; // parities: stage; per query tile Q and P (bit e)
+        // low words of the descriptors; steps of 16 columns or rows are added to them
+        const uint32_t qd = uint32_t(tc::sdesc_sw128(tc::smem_addr(qbuf), 16, 1024));
+        const uint32_t k0d = uint32_t(tc::sdesc_sw128(tc::smem_addr(k0buf), 16, 1024));
+        const uint32_t kd = uint32_t(tc::sdesc_sw128(tc::smem_addr(vkbuf + C::kTileBytes), 16, 1024));
+        const uint32_t vd = uint32_t(tc::sdesc_sw128(tc::smem_addr(vkbuf), C::kHalf, 1024));
+        constexpr uint32_t kHi = uint32_t(tc::kDescHi | (1024 >> 4));
         constexpr uint32_t kTile16 = C::kTileBytes / 16, kHalf16 = C::kHalf / 16;
         auto fetch = [&](Item* it) -> bool {
           const int slot = ii % kItems;
@@ -277,12 +276,13 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           return true;
         };
         // S of query tile e
-        auto scores = [&](int e, uint64_t b, bool last) {
-          const uint64_t a = qd + e * kTile16;
+        auto scores = [&](int e, uint32_t b, bool last) {
+          const uint32_t st = tmem + e * 256;
+          const uint32_t a = qd + e * kTile16;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             const uint32_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
-            tc::mma_ss(tmem + e * 256, a + off, b + off, C::kIdescS, kk > 0 ? 1u : 0u);
+            tc::mma_ss_lo(st, a + off, b + off, kHi, C::kIdescS, kk > 0 ? 1u : 0u);
           }
           tc::mma_commit(&bars->s_full[e]);
           if (last) tc::mma_commit(&bars->q_empty[e]);
@@ -291,54 +291,58 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         failed = !fetch(&cur);
         if (!failed && cur.live) {
           failed = !tc::mbar_spin(&bars->k0_full, 0, abort);
-#pragma unroll
-          for (int e = 0; e < 2; ++e)
-            if (cur.nkt[e] > 0 && !failed) {
-              failed = !tc::mbar_spin(&bars->q_full[e], qn[e]++ & 1, abort);
-              tc::tc_fence_after();
-              if (!failed) scores(e, k0d, cur.nkt[e] == 1);
-            }
+#pragma unroll 1
+          for (int e = 0; e < 2; ++e) {
+            const int nkt = e ? cur.nkt[1] : cur.nkt[0];
+            if (nkt == 0 || failed) continue;
+            failed = !tc::mbar_spin(&bars->q_full[e], 0, abort);
+            qpar ^= 1u << e;
+            tc::tc_fence_after();
+            if (!failed) scores(e, k0d, nkt == 1);
+          }
         }
         while (!failed && cur.live) {
-          const int nkt[2] = {cur.nkt[0], cur.nkt[1]}, n = cur.n;
-          int seen[2];
-#pragma unroll
-          for (int e = 0; e < 2; ++e) seen[e] = min(cur.nk, cur.pos[e] + cur.rows[e]);
+          const int nkt0 = cur.nkt[0], nkt1 = cur.nkt[1], n = cur.n;
+          const int seen0 = min(cur.nk, cur.pos[0] + cur.rows[0]);
+          const int seen1 = min(cur.nk, cur.pos[1] + cur.rows[1]);
+#pragma unroll 1
           for (int j = 0; j < n && !failed; ++j) {
             const bool end = j == n - 1;
             if (end && !fetch(&cur)) { failed = true; break; }
-            const uint64_t v = vd + ps * 2 * kTile16, k = kd + ps * 2 * kTile16;
-#pragma unroll
+#pragma unroll 1
             for (int e = 0; e < 2; ++e) {
               const uint32_t st = tmem + e * 256;
-              const int left = end ? (cur.live ? cur.nkt[e] : 0) : nkt[e] - j - 1;
-              if (j < nkt[e]) {
-                if (!tc::mbar_spin(&bars->p_full[e], on[e]++ & 1, abort)) { failed = true; break; }
+              const int nkt = e ? nkt1 : nkt0;
+              const int left = !end ? nkt - j - 1 : cur.live ? (e ? cur.nkt[1] : cur.nkt[0]) : 0;
+              if (j < nkt) {
+                if (!tc::mbar_spin(&bars->p_full[e], (ppar >> e) & 1, abort)) { failed = true; break; }
+                ppar ^= 1u << e;
                 tc::tc_fence_after();
-                const int groups = (min(128, seen[e] - j * 128) + 15) >> 4;
+                const int groups = (min(128, (e ? seen1 : seen0) - j * 128) + 15) >> 4;
+                const uint32_t v = vd + ps * 2 * kTile16;
                 if (groups == 8) {
 #pragma unroll
                   for (int kk = 0; kk < 8; ++kk)
-                    tc::mma_ts(st + 128, st + kk * 8, v + kk * 128, C::kIdescO,
-                               (kk > 0 || j > 0) ? 1u : 0u);
+                    tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
+                                  kk > 0 ? 1u : uint32_t(j));
                 } else {
 #pragma unroll 1
                   for (int kk = 0; kk < groups; ++kk)
-                    tc::mma_ts(st + 128, st + kk * 8, v + kk * 128, C::kIdescO,
-                               (kk > 0 || j > 0) ? 1u : 0u);
+                    tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
+                                  uint32_t(kk + j));
                 }
-                if (j == nkt[e] - 1) tc::mma_commit(&bars->o_done[e]);
+                if (j == nkt - 1) tc::mma_commit(&bars->o_done[e]);
               } else if (left > 0) {  // only scores: this tile's products were shorter
                 if (!tc::mbar_spin(&bars->vk_full[ps], pp, abort) ||
-                    !tc::mbar_spin(&bars->q_full[e], qn[e] & 1, abort)) {
+                    !tc::mbar_spin(&bars->q_full[e], (qpar >> e) & 1, abort)) {
                   failed = true;
                   break;
                 }
                 tc::tc_fence_after();
               }
               if (left > 0) {
-                if (end) ++qn[e];
-                scores(e, k, left == 1);
+                if (end) qpar ^= 1u << e;
+                scores(e, kd + ps * 2 * kTile16, left == 1);
               }
             }
             tc::mma_commit(&bars->vk_empty[ps]);
