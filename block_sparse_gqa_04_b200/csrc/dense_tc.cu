@@ -63,9 +63,9 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t k0_full;                     // the CTA's first K tile
   uint64_t vk_full[4], vk_empty[4];     // a V tile and the K tile after it
-  // per query tile: S computed, P written (and what its products need is there), the
-  // tile's last P V done, O read by the epilogue, sums written, sums read
-  uint64_t s_full[2], p_full[2], o_done[2], o_empty[2], l_full[2], l_empty[2];
+  // per query tile: S computed, the first half of P written (and what else its products
+  // need is there), all of P written, the tile's last P V done, O read by the epilogue, sums written, sums read
+  uint64_t s_full[2], p_half[2], p_full[2], o_done[2], o_empty[2], l_full[2], l_empty[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint64_t mma_done;
   Item item[kItems];
@@ -141,7 +141,8 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       tc::mbar_init(&bars->q_full[b], 1);
       tc::mbar_init(&bars->q_empty[b], 1);
       tc::mbar_init(&bars->s_full[b], 1);
-      tc::mbar_init(&bars->p_full[b], 5);    // the tile's softmax warps and warp 2
+      tc::mbar_init(&bars->p_half[b], 5);    // the tile's softmax warps and warp 2
+      tc::mbar_init(&bars->p_full[b], 4);
       tc::mbar_init(&bars->o_done[b], 1);
       tc::mbar_init(&bars->o_empty[b], 4);   // the epilogue warps
       tc::mbar_init(&bars->l_full[b], 4);
@@ -315,14 +316,14 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
               const int nkt = e ? nkt1 : nkt0;
               const int left = !end ? nkt - j - 1 : cur.live ? (e ? cur.nkt[1] : cur.nkt[0]) : 0;
               if (j < nkt) {
-                if (!tc::mbar_spin(&bars->p_full[e], (ppar >> e) & 1, abort)) { failed = true; break; }
-                ppar ^= 1u << e;
-                tc::tc_fence_after();
+                // keys 0-63 run while the softmax finishes keys 64-127
                 const int groups = (min(128, (e ? seen1 : seen0) - j * 128) + 15) >> 4;
                 const uint32_t v = vd + ps * 2 * kTile16;
-                if (groups == 8) {
+                if (!tc::mbar_spin(&bars->p_half[e], (ppar >> e) & 1, abort)) { failed = true; break; }
+                tc::tc_fence_after();
+                if (groups >= 4) {
 #pragma unroll
-                  for (int kk = 0; kk < 8; ++kk)
+                  for (int kk = 0; kk < 4; ++kk)
                     tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
                                   kk > 0 ? 1u : uint32_t(j));
                 } else {
@@ -330,6 +331,18 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                   for (int kk = 0; kk < groups; ++kk)
                     tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
                                   uint32_t(kk + j));
+                }
+                if (!tc::mbar_spin(&bars->p_full[e], (ppar >> e) & 1, abort)) { failed = true; break; }
+                ppar ^= 1u << e;
+                tc::tc_fence_after();
+                if (groups == 8) {
+#pragma unroll
+                  for (int kk = 4; kk < 8; ++kk)
+                    tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO, 1u);
+                } else {
+#pragma unroll 1
+                  for (int kk = 4; kk < groups; ++kk)
+                    tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO, 1u);
                 }
                 if (j == nkt - 1) tc::mma_commit(&bars->o_done[e]);
               } else if (left > 0) {  // only scores: this tile's products were shorter
@@ -354,7 +367,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
     } else if (warp == 2) {
       // ---------------- what else the products need ----------------
-      // Per key tile and query tile, one arrival at p_full: the V tile and the K tile
+      // Per key tile and query tile, one arrival at p_half: the V tile and the K tile
       // after it have landed (V's rows behind the last key zeroed), the epilogue has read
       // the previous O, the next item's Q has landed.
       int ii = 0, ps = 0;
@@ -389,14 +402,14 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             const bool follow = end && nxt.live && nxt.nkt[e] > 0;
             if (j < cur.nkt[e] && !failed) {
               // the arrival belongs to the phase of this key tile: the one before is over
-              if ((on[e] > 0 && !warp_wait(&bars->p_full[e], (on[e] & 1) ^ 1, abort)) ||
+              if ((on[e] > 0 && !warp_wait(&bars->p_half[e], (on[e] & 1) ^ 1, abort)) ||
                   (j == 0 && !warp_wait(&bars->o_empty[e], (in[e]++ & 1) ^ 1, abort)) ||
                   (follow && !warp_wait(&bars->q_full[e], qn[e] & 1, abort))) {
                 failed = true;
                 break;
               }
               ++on[e];
-              if (lane == 0) tc::mbar_arrive(&bars->p_full[e]);
+              if (lane == 0) tc::mbar_arrive(&bars->p_half[e]);
             }
             if (follow) ++qn[e];
           }
@@ -454,6 +467,24 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           m = top;
           ms = nms;
         }
+        if (j > 0 && __any_sync(MSA_FULL_MASK, grow)) {
+          // the previous P V was issued before this S: O is there; scale it
+          const uint64_t k2 = f2(keep, keep);
+#pragma unroll 1
+          for (int c = 0; c < D; c += 16) {
+            uint32_t o[16];
+            tc::tmem_ld16(ot + c, o);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 16; x += 2) {
+              const uint64_t y = mul2((uint64_t(o[x + 1]) << 32) | o[x], k2);
+              o[x] = uint32_t(y);
+              o[x + 1] = uint32_t(y >> 32);
+            }
+            tmem_st8(ot + c, o);
+            tmem_st8(ot + c + 8, o + 8);
+          }
+        }
         const uint64_t nmsx2 = f2(-ms, -ms);
         uint64_t lsum[2] = {0, 0};
 #pragma unroll
@@ -472,28 +503,13 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             tmem_st8(st + q4 * 16 + x8 * 8, pw);
           }
-        }
-        if (j > 0 && __any_sync(MSA_FULL_MASK, grow)) {
-          // the previous P V was issued before this S: O is there; scale it
-          const uint64_t k2 = f2(keep, keep);
-#pragma unroll 1
-          for (int c = 0; c < D; c += 32) {
-            uint32_t o[32];
-            tc::tmem_ld32(ot + c, o);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int x = 0; x < 32; x += 2) {
-              const uint64_t y = mul2((uint64_t(o[x + 1]) << 32) | o[x], k2);
-              o[x] = uint32_t(y);
-              o[x + 1] = uint32_t(y >> 32);
-            }
-            tc::tmem_st32(ot + c, o);
+          if (q4 & 1) {
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(q4 == 1 ? &bars->p_half[e] : &bars->p_full[e]);
           }
         }
-        tc::tmem_st_wait();
-        tc::tc_fence_before();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->p_full[e]);
         const uint64_t lsx = add2(lsum[0], lsum[1]);
         l = l * keep + (__uint_as_float(uint32_t(lsx)) + __uint_as_float(uint32_t(lsx >> 32)));
       }
