@@ -117,7 +117,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
 dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     const __grid_constant__ CUtensorMap tmap_k,
-                    const __grid_constant__ CUtensorMap tmap_v, Dense P,
+                    const __grid_constant__ CUtensorMap tmap_v,
+                    const __grid_constant__ CUtensorMap tmap_o, Dense P,
                     __nv_bfloat16* __restrict__ out, float* __restrict__ lse,
                     int* __restrict__ next_item, int* __restrict__ status) {
   using C = Cfg<D>;
@@ -160,6 +161,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     tc::tma_prefetch(&tmap_q);
     tc::tma_prefetch(&tmap_k);
     tc::tma_prefetch(&tmap_v);
+    tc::tma_prefetch(&tmap_o);
   }
   if (warp == 1) tc::tmem_alloc(&bars->tmem_base, kTmemCols);
   tc::tc_fence_before();
@@ -181,10 +183,12 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           int live, n, b, k0, g;
           int nkt[2], head[2], row0[2];
         } cur, nxt;
-        int ii = 0;  // items
+        // The first item is the CTA's own, the others are taken late, two key tiles before
+        // the copies need them, so that no CTA holds an item while another has none.
+        int ii = 0, ticket = blockIdx.x;  // items, the next one's number
         // the next item to the other warps, and what the copies need of it
         auto publish = [&](Where* w) -> bool {
-          const int t = atomicAdd(next_item, 1), slot = ii % kItems;
+          const int slot = ii % kItems, t = ticket;
           if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) return false;
           ++ii;
           Item& it = bars->item[slot];
@@ -212,27 +216,27 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         failed = !publish(&cur);
         bool start = true;
         while (!failed && cur.live) {
+          if (start) {
+            tc::mbar_arrive_expect_tx(&bars->k0_full, C::kTileBytes);
+            k0_armed = true;
+            copy(&tmap_k, k0buf, &bars->k0_full, cur, 0);
+          }
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            if (cur.nkt[e] > 0 && !failed) {
-              if (!tc::mbar_wait(&bars->q_empty[e], (qn[e] & 1) ^ 1, abort)) { failed = true; break; }
-              tc::mbar_arrive_expect_tx(&bars->q_full[e], C::kTileBytes);
-              q_armed.note(e, qn[e] & 1);
-              ++qn[e];
+            if (cur.nkt[e] == 0 || failed) continue;
+            if (!tc::mbar_wait(&bars->q_empty[e], (qn[e] & 1) ^ 1, abort)) { failed = true; continue; }
+            tc::mbar_arrive_expect_tx(&bars->q_full[e], C::kTileBytes);
+            q_armed.note(e, qn[e] & 1);
+            ++qn[e];
 #pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                tc::tma_load_3d(qbuf + e * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[e],
-                                64 * h, cur.head[e], cur.row0[e]);
-            }
-            if (e == 0 && start) {
-              tc::mbar_arrive_expect_tx(&bars->k0_full, C::kTileBytes);
-              k0_armed = true;
-              copy(&tmap_k, k0buf, &bars->k0_full, cur, 0);
-              start = false;
-            }
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_load_3d(qbuf + e * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[e],
+                              64 * h, cur.head[e], cur.row0[e]);
           }
-          if (failed || !publish(&nxt)) { failed = true; break; }
-          for (int j = 0; j < cur.n; ++j) {
+          start = false;
+          for (int j = 0; j < cur.n && !failed; ++j) {
+            if (j == max(cur.n - 3, 0)) ticket = gridDim.x + atomicAdd(next_item, 1);
+            if (j == cur.n - 1 && !publish(&nxt)) { failed = true; break; }
             if (!tc::mbar_wait(&bars->vk_empty[stage], phase ^ 1, abort)) { failed = true; break; }
             const bool more = j + 1 < cur.n || nxt.live;
             uint64_t* fb = &bars->vk_full[stage];
@@ -306,8 +310,41 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const int nkt0 = cur.nkt[0], nkt1 = cur.nkt[1], n = cur.n;
           const int seen0 = min(cur.nk, cur.pos[0] + cur.rows[0]);
           const int seen1 = min(cur.nk, cur.pos[1] + cur.rows[1]);
-#pragma unroll 1
-          for (int j = 0; j < n && !failed; ++j) {
+          int j = 0;
+          // Steps in which both tiles have whole key tiles left run without a decision on
+          // the way: the general form below takes hundreds of cycles more.
+          for (const int fast = min(nkt0, nkt1) - 1; j < fast && (ppar == 0 || ppar == 3); ++j) {
+            const uint32_t par = ppar & 1;
+            const uint32_t v = vd + ps * 2 * kTile16, k = kd + ps * 2 * kTile16;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const uint32_t st = tmem + e * 256, q = qd + e * kTile16;
+              if (!tc::mbar_spin(&bars->p_half[e], par, abort)) { failed = true; break; }
+              tc::tc_fence_after();
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
+                              kk > 0 ? 1u : uint32_t(j));
+              if (!tc::mbar_spin(&bars->p_full[e], par, abort)) { failed = true; break; }
+              tc::tc_fence_after();
+#pragma unroll
+              for (int kk = 4; kk < 8; ++kk)
+                tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO, 1u);
+#pragma unroll
+              for (int kk = 0; kk < D / 16; ++kk) {
+                const uint32_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
+                tc::mma_ss_lo(st, q + off, k + off, kHi, C::kIdescS, kk > 0 ? 1u : 0u);
+              }
+              tc::mma_commit(&bars->s_full[e]);
+            }
+            if (failed) break;
+            tc::mma_commit(&bars->vk_empty[ps]);
+            ppar ^= 3;
+            if (++ps == C::kPairs) { ps = 0; pp ^= 1; }
+            if (j + 2 == nkt0) tc::mma_commit(&bars->q_empty[0]);
+            if (j + 2 == nkt1) tc::mma_commit(&bars->q_empty[1]);
+          }
+          for (; j < n && !failed; ++j) {
             const bool end = j == n - 1;
             if (end && !fetch(&cur)) { failed = true; break; }
 #pragma unroll 1
@@ -525,6 +562,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     regs_dec<kRegsEpi>();
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
+    uint8_t* wst = k0buf + quarter * (32 * D * 2);  // free once the first item's scores are done
     int qn[2] = {0, 0};
     for (int ii = 0; !failed; ++ii) {
       const int slot = ii % kItems;
@@ -554,10 +592,12 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (!warp_wait(&bars->o_done[e], par, abort)) { failed = true; continue; }
         tc::tc_fence_after();
         const uint32_t ot = tmem + (uint32_t(quarter * 32) << 16) + e * 256 + 128;
-        const long long at = (long long)(row0[e] + row) * P.Hq + head[e];
-        const bool mine = row < rows[e];
+        // Each warp owns 32 rows and stores them itself with TMA, from a staging area in
+        // the 128-byte swizzle (16-byte chunk k of a row at chunk k ^ (row % 8)); plain
+        // 16-byte stores of a row per thread kept the softmax warps' TMEM accesses waiting
+        // behind them.
+        if (lane == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
         const uint64_t inv2 = f2(inv, inv);
-        uint4* dst = reinterpret_cast<uint4*>(out + at * D);
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -569,21 +609,44 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(&bars->o_empty[e]);
           }
-          if (mine) {
+          uint8_t* hp = wst + (c >> 1) * 4096 + lane * 128;
 #pragma unroll
-            for (int k8 = 0; k8 < 4; ++k8) {
-              const uint32_t* w8 = o + 8 * k8;
-              uint4 u;
-              u.x = to_bf16x2(mul2((uint64_t(w8[1]) << 32) | w8[0], inv2));
-              u.y = to_bf16x2(mul2((uint64_t(w8[3]) << 32) | w8[2], inv2));
-              u.z = to_bf16x2(mul2((uint64_t(w8[5]) << 32) | w8[4], inv2));
-              u.w = to_bf16x2(mul2((uint64_t(w8[7]) << 32) | w8[6], inv2));
-              dst[c * 4 + k8] = u;
-            }
+          for (int k8 = 0; k8 < 4; ++k8) {
+            const uint32_t* w8 = o + 8 * k8;
+            uint4 u;
+            u.x = to_bf16x2(mul2((uint64_t(w8[1]) << 32) | w8[0], inv2));
+            u.y = to_bf16x2(mul2((uint64_t(w8[3]) << 32) | w8[2], inv2));
+            u.z = to_bf16x2(mul2((uint64_t(w8[5]) << 32) | w8[4], inv2));
+            u.w = to_bf16x2(mul2((uint64_t(w8[7]) << 32) | w8[6], inv2));
+            *reinterpret_cast<uint4*>(hp + ((((c & 1) * 4 + k8) ^ (lane & 7)) << 4)) = u;
           }
+        }
+        const int left = rows[e] - quarter * 32;  // rows of the warp that exist
+        if (left >= 32) {
+          tc::fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_store_3d(&tmap_o, wst + h * 4096, 64 * h, head[e], row0[e] + quarter * 32);
+            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+          }
+        } else {
+          __syncwarp();
+          constexpr int per = D / 8;
+          for (int i = lane; i < left * per; i += 32) {
+            const int r = i / per, c = i % per;
+            const uint4 u = *reinterpret_cast<const uint4*>(wst + (c >> 3) * 4096 + r * 128 +
+                                                            (((c & 7) ^ (r & 7)) << 4));
+            *reinterpret_cast<uint4*>(
+                out + ((long long)(row0[e] + quarter * 32 + r) * P.Hq + head[e]) * D + c * 8) = u;
+          }
+          __syncwarp();
         }
       }
     }
+    // every store has completed before the CTA exits
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   if (failed) {
     bars->abort = 1;
@@ -600,8 +663,9 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 template <int D>
 cudaError_t fwd_tc(const Dense& P, const void* q, const void* k, const void* v, void* out,
                    float* lse, int32_t* counter, int32_t* status, cudaStream_t s) {
-  CUtensorMap mq, mk, mv;
+  CUtensorMap mq, mk, mv, mo;
   cudaError_t e = encode_rows(&mq, q, D, P.Hq, P.rows_q);
+  if (e == cudaSuccess) e = encode_rows(&mo, out, D, P.Hq, P.rows_q, 32);
   if (e == cudaSuccess) e = encode_rows(&mk, k, D, P.Hkv, P.rows_k);
   if (e == cudaSuccess) e = encode_rows(&mv, v, D, P.Hkv, P.rows_k);
   if (e == cudaSuccess)
@@ -609,7 +673,7 @@ cudaError_t fwd_tc(const Dense& P, const void* q, const void* k, const void* v, 
                        kRegsCtl + kRegsEpi + 2 * kRegsSoftmax, kThreads);
   if (e != cudaSuccess) return e;
   dense_fwd_tc_kernel<D><<<std::min(sm_count(), P.pairs), kThreads, smem_bytes<D>(), s>>>(
-      mq, mk, mv, P, static_cast<__nv_bfloat16*>(out), lse, counter, status);
+      mq, mk, mv, mo, P, static_cast<__nv_bfloat16*>(out), lse, counter, status);
   return cudaGetLastError();
 }
 
