@@ -28,7 +28,7 @@
 namespace msa {
 namespace {
 
-// warp 0 items and TMA, warp 1 MMA, warps 2-3 idle, warps 4-11 elementwise
+// warp 0 items and TMA, warp 1 MMA, warp 2 waits for it, warp 3 idle, warps 4-11 elementwise
 constexpr int kThreads = 384;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItems = 2;
@@ -38,7 +38,6 @@ struct Cfg {
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kHalf = 128 * 64 * 2;
   static constexpr int kStages = 2;                     // dkv: of Q and of dO
-  static constexpr int kRing = D == 128 ? 5 : 8;        // dq: of K and V tiles in turn
   static constexpr uint32_t kIdescS = tc::idesc_bf16_f32(128, 128, 0, 0);
   static constexpr uint32_t kIdescG = tc::idesc_bf16_f32(128, D, 0, 1);
 };
@@ -49,14 +48,23 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t* v) {
 __device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float(uint32_t(x)); }
 __device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float(uint32_t(x >> 32)); }
 
+// Low words of the tiles' descriptors, and the upper word that they share.
+constexpr uint32_t kHi = uint32_t(tc::kDescHi | (1024 >> 4));
+__device__ __forceinline__ uint32_t kmajor(const uint8_t* tile) {
+  return uint32_t(tc::sdesc_sw128(tc::smem_addr(tile), 16, 1024));
+}
+template <int D>
+__device__ __forceinline__ uint32_t mnmajor(const uint8_t* tile) {
+  return uint32_t(tc::sdesc_sw128(tc::smem_addr(tile), Cfg<D>::kHalf, 1024));
+}
+
 // S = A B^T over D, both tiles K-major.
 template <int D>
 __device__ __forceinline__ void issue_nt(uint32_t d, uint32_t a, uint32_t b) {
 #pragma unroll
   for (int kk = 0; kk < D / 16; ++kk) {
-    const uint32_t off = (kk >> 2) * Cfg<D>::kHalf + (kk & 3) * 32;
-    tc::mma_ss(d, tc::sdesc_sw128(a + off, 16, 1024), tc::sdesc_sw128(b + off, 16, 1024),
-               Cfg<D>::kIdescS, kk > 0 ? 1u : 0u);
+    const uint32_t off = (kk >> 2) * (Cfg<D>::kHalf / 16) + (kk & 3) * 2;
+    tc::mma_ss_lo(d, a + off, b + off, kHi, Cfg<D>::kIdescS, kk > 0 ? 1u : 0u);
   }
 }
 
@@ -64,11 +72,18 @@ __device__ __forceinline__ void issue_nt(uint32_t d, uint32_t a, uint32_t b) {
 // first 64 columns of elements at a, the others 64 TMEM columns on.
 template <int D>
 __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint32_t b, int groups,
-                                         bool fresh) {
-  for (int kk = 0; kk < groups; ++kk)
-    tc::mma_ts(d, a + (kk >> 2) * 64 + (kk & 3) * 8,
-               tc::sdesc_sw128(b + kk * 2048, Cfg<D>::kHalf, 1024), Cfg<D>::kIdescG,
-               (!fresh || kk > 0) ? 1u : 0u);
+                                         uint32_t accumulate) {
+  if (groups == 8) {
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      tc::mma_ts_lo(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * 128, kHi, Cfg<D>::kIdescG,
+                    kk > 0 ? 1u : accumulate);
+  } else {
+#pragma unroll 1
+    for (int kk = 0; kk < groups; ++kk)
+      tc::mma_ts_lo(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * 128, kHi, Cfg<D>::kIdescG,
+                    kk > 0 ? 1u : accumulate);
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -135,7 +150,9 @@ struct KeyItem {
 struct KeyBars {
   uint64_t kv_full, kv_empty;
   uint64_t q_full[2], q_empty[2], g_full[2], g_empty[2];  // Q (with lse, delta) and dO stages
-  uint64_t s_full, p_full, dp_full, ds_full, acc_full, acc_empty;
+  // first_full: the item's K, V and first Q, dO are there; p_full, ds_full: P and dS
+  // written, and the next step's Q and dO are there
+  uint64_t first_full, s_full, p_full, dp_full, ds_full, acc_full, acc_empty;
   uint64_t i_full[kItems], i_empty[kItems];
   uint64_t mma_done;
   KeyItem item[kItems];
@@ -207,15 +224,16 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       tc::mbar_init(&bars->g_full[s], 1);
       tc::mbar_init(&bars->g_empty[s], 1);
     }
+    tc::mbar_init(&bars->first_full, 1);
     tc::mbar_init(&bars->s_full, 1);
-    tc::mbar_init(&bars->p_full, 8);
+    tc::mbar_init(&bars->p_full, 9);   // 8 elementwise warps and warp 2
     tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->ds_full, 9);
     tc::mbar_init(&bars->acc_full, 1);
     tc::mbar_init(&bars->acc_empty, 8);
     for (int i = 0; i < kItems; ++i) {
       tc::mbar_init(&bars->i_full[i], 1);
-      tc::mbar_init(&bars->i_empty[i], 9);  // the MMA warp and 8 elementwise warps
+      tc::mbar_init(&bars->i_empty[i], 10);  // warps 1, 2 and 8 elementwise warps
     }
     tc::mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
@@ -241,7 +259,7 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     if (lane == 0) {
       tc::ArmedRing kv_armed, q_armed, g_armed;
       int n = 0, used = 0;  // steps and items with steps so far
-      int t = atomicAdd(next_item, 1);
+      int t = blockIdx.x;   // the first item is the CTA's own
       for (int ii = 0; !failed; ++ii) {
         const int slot = ii % kItems;
         if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) {
@@ -253,8 +271,10 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const KeyItem it = bars->item[slot];
         tc::mbar_arrive(&bars->i_full[slot]);
         if (!it.live) break;
-        t = atomicAdd(next_item, 1);
-        if (it.heads == 0 || it.qt0 >= it.nqt) continue;
+        if (it.heads == 0 || it.qt0 >= it.nqt) {
+          t = gridDim.x + atomicAdd(next_item, 1);
+          continue;
+        }
         if (!tc::mbar_wait(&bars->kv_empty, (used & 1) ^ 1, abort)) { failed = true; break; }
         tc::mbar_arrive_expect_tx(&bars->kv_full, 2 * C::kTileBytes);
         kv_armed.note(0, used & 1);
@@ -286,6 +306,7 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                               64 * h, hh, row);
           }
         }
+        t = gridDim.x + atomicAdd(next_item, 1);  // late, so that no CTA holds two items
       }
       if (!(kv_armed.drain(&bars->kv_full) && q_armed.drain(bars->q_full) &&
             g_armed.drain(bars->g_full)))
@@ -293,11 +314,60 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      const bool ok = lane != 0 || tc::mbar_spin(bar, parity, abort);
-      return __shfl_sync(MSA_FULL_MASK, ok ? 1 : 0, 0) != 0;
-    };
-    int n = 0, used = 0;
+    if (tc::elect_one()) {
+      const uint32_t ka = kmajor(kbuf), va = kmajor(vbuf);
+      const uint32_t qa = kmajor(qbuf), ga = kmajor(gbuf);
+      const uint32_t qb = mnmajor<D>(qbuf), gb = mnmajor<D>(gbuf);
+      constexpr uint32_t kTile16 = C::kTileBytes / 16;
+      uint32_t n = 0, used = 0;
+      for (int ii = 0; !failed; ++ii) {
+        const int slot = ii % kItems;
+        if (!tc::mbar_spin(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+        const KeyItem it = bars->item[slot];
+        tc::mbar_arrive(&bars->i_empty[slot]);
+        if (!it.live) break;
+        const int tiles = it.nqt - it.qt0, steps = it.heads * tiles;
+        if (steps <= 0) continue;
+        const int last = (min(128, it.nq - (it.nqt - 1) * 128) + 15) >> 4;
+        if (!tc::mbar_spin(&bars->first_full, used & 1, abort)) { failed = true; break; }
+        tc::tc_fence_after();
+        uint32_t off = (n & 1) * kTile16;  // of this step's stage
+        issue_nt<D>(ts, ka, qa + off);
+        tc::mma_commit(&bars->s_full);
+        issue_nt<D>(tp, va, ga + off);
+        tc::mma_commit(&bars->dp_full);
+        int left = tiles;  // query tiles left of the head
+        for (int i = 0; i < steps; ++i, ++n, off ^= kTile16) {
+          const int s = n & 1;
+          const int groups = --left == 0 ? last : 8;
+          if (left == 0) left = tiles;
+          if (!tc::mbar_spin(&bars->p_full, n & 1, abort)) { failed = true; break; }
+          tc::tc_fence_after();
+          issue_ts<D>(tv, ts, gb + off, groups, i > 0);
+          tc::mma_commit(&bars->g_empty[s]);
+          if (i + 1 < steps) {
+            issue_nt<D>(ts, ka, qa + (off ^ kTile16));
+            tc::mma_commit(&bars->s_full);
+          }
+          if (!tc::mbar_spin(&bars->ds_full, n & 1, abort)) { failed = true; break; }
+          tc::tc_fence_after();
+          issue_ts<D>(tk, tp, qb + off, groups, i > 0);
+          tc::mma_commit(&bars->q_empty[s]);
+          if (i + 1 < steps) {
+            issue_nt<D>(tp, va, ga + (off ^ kTile16));
+            tc::mma_commit(&bars->dp_full);
+          }
+        }
+        if (failed) break;
+        tc::mma_commit(&bars->kv_empty);
+        tc::mma_commit(&bars->acc_full);
+        ++used;
+      }
+      if (!tc::mma_drain(&bars->mma_done)) failed = true;
+    }
+  } else if (warp == 2) {
+    // ---------------- what else the products need ----------------
+    uint32_t n = 0, used = 0;
     for (int ii = 0; !failed; ++ii) {
       const int slot = ii % kItems;
       if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
@@ -307,64 +377,40 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (!it.live) break;
       const int tiles = it.nqt - it.qt0, steps = it.heads * tiles;
       if (steps <= 0) continue;
-      const uint32_t ka = tc::smem_addr(kbuf), va = tc::smem_addr(vbuf);
-      // S(i) and dP(i): the tile's rows are there, those behind the sequence zero
-      auto first = [&](int i) -> bool {
-        const int s = (n + i) & 1, rows = min(128, it.nq - (it.qt0 + i % tiles) * 128);
-        if (!wait(&bars->q_full[s], ((n + i) >> 1) & 1)) return false;
-        uint8_t* q = qbuf + s * C::kTileBytes;
-        if (rows & 15) zero_rows<D>(q, rows, (rows + 15) & ~15);
-        if (lane == 0) {
-          tc::tc_fence_after();
-          issue_nt<D>(ts, ka, tc::smem_addr(q));
-          tc::mma_commit(&bars->s_full);
-        }
+      const int rows = min(128, it.nq - (it.nqt - 1) * 128);  // of each head's last tile
+      // tile of step x has landed; rows behind the sequence are zero
+      auto landed = [&](uint64_t* full, uint8_t* buf, uint32_t x, bool tail) -> bool {
+        if (!warp_wait(&full[x & 1], (x >> 1) & 1, abort)) return false;
+        if (tail && (rows & 15)) zero_rows<D>(buf + (x & 1) * C::kTileBytes, rows, (rows + 15) & ~15);
         return true;
       };
-      auto second = [&](int i) -> bool {
-        const int s = (n + i) & 1, rows = min(128, it.nq - (it.qt0 + i % tiles) * 128);
-        if (!wait(&bars->g_full[s], ((n + i) >> 1) & 1)) return false;
-        uint8_t* g = gbuf + s * C::kTileBytes;
-        if (rows & 15) zero_rows<D>(g, rows, (rows + 15) & ~15);
-        if (lane == 0) {
-          tc::tc_fence_after();
-          issue_nt<D>(tp, va, tc::smem_addr(g));
-          tc::mma_commit(&bars->dp_full);
-        }
-        return true;
-      };
-      if (!wait(&bars->kv_full, used & 1) || !first(0) || !second(0)) { failed = true; break; }
-      for (int i = 0; i < steps; ++i) {
-        const int s = (n + i) & 1, rows = min(128, it.nq - (it.qt0 + i % tiles) * 128);
-        const int groups = (rows + 15) >> 4;
-        if (!wait(&bars->p_full, (n + i) & 1) ||
-            (i == 0 && !wait(&bars->acc_empty, (used & 1) ^ 1))) {
+      if (!warp_wait(&bars->kv_full, used & 1, abort) ||
+          !landed(bars->q_full, qbuf, n, tiles == 1) || !landed(bars->g_full, gbuf, n, tiles == 1)) {
+        failed = true;
+        break;
+      }
+      if (lane == 0) tc::mbar_arrive(&bars->first_full);
+      int left = tiles;
+      for (int i = 0; i < steps; ++i, ++n) {
+        if (--left == 0) left = tiles;
+        const bool tail = left == 1;  // the next step's tile is its head's last
+        // an arrival belongs to this step: the step before is over
+        if ((n > 0 && !warp_wait(&bars->p_full, (n & 1) ^ 1, abort)) ||
+            (i == 0 && !warp_wait(&bars->acc_empty, (used & 1) ^ 1, abort)) ||
+            (i + 1 < steps && !landed(bars->q_full, qbuf, n + 1, tail))) {
           failed = true;
           break;
         }
-        if (lane == 0) {
-          tc::tc_fence_after();
-          issue_ts<D>(tv, ts, tc::smem_addr(gbuf + s * C::kTileBytes), groups, i == 0);
-          tc::mma_commit(&bars->g_empty[s]);
+        if (lane == 0) tc::mbar_arrive(&bars->p_full);
+        if ((n > 0 && !warp_wait(&bars->ds_full, (n & 1) ^ 1, abort)) ||
+            (i + 1 < steps && !landed(bars->g_full, gbuf, n + 1, tail))) {
+          failed = true;
+          break;
         }
-        if (i + 1 < steps && !first(i + 1)) { failed = true; break; }
-        if (!wait(&bars->ds_full, (n + i) & 1)) { failed = true; break; }
-        if (lane == 0) {
-          tc::tc_fence_after();
-          issue_ts<D>(tk, tp, tc::smem_addr(qbuf + s * C::kTileBytes), groups, i == 0);
-          tc::mma_commit(&bars->q_empty[s]);
-        }
-        if (i + 1 < steps && !second(i + 1)) { failed = true; break; }
+        if (lane == 0) tc::mbar_arrive(&bars->ds_full);
       }
-      if (failed) break;
-      if (lane == 0) {
-        tc::mma_commit(&bars->kv_empty);
-        tc::mma_commit(&bars->acc_full);
-      }
-      n += steps;
       ++used;
     }
-    if (lane == 0 && !tc::mma_drain(&bars->mma_done)) failed = true;
   } else if (warp >= 4) {
     // ---------------- elementwise: P, dS, then the tile's dV (first warpgroup) or dK ----------------
     const int half = (warp - 4) >> 2, quarter = warp & 3;
@@ -544,8 +590,10 @@ struct RowItem {
 
 struct RowBars {
   uint64_t q_full, q_empty;
-  uint64_t kv_full[8], kv_empty[8];
-  uint64_t s_full[2], dp_full, ds_full, acc_full, acc_empty;
+  uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
+  // first_full: Q, dO and the first K and V tiles are there; ds_full: dS written, and the
+  // K and V tiles of the products after it are there
+  uint64_t first_full, s_full[2], dp_full, ds_full, acc_full, acc_empty;
   uint64_t i_full[kItems], i_empty[kItems];
   uint64_t mma_done;
   RowItem item[kItems];
@@ -555,7 +603,7 @@ struct RowBars {
 
 template <int D>
 constexpr size_t row_smem() {
-  return 1024 + size_t(2 + Cfg<D>::kRing) * Cfg<D>::kTileBytes + sizeof(RowBars) + 64;
+  return 1024 + size_t(7) * Cfg<D>::kTileBytes + sizeof(RowBars) + 64;
 }
 static_assert(row_smem<128>() <= 232448 && row_smem<64>() <= 232448, "shared memory of a CTA");
 
@@ -574,27 +622,33 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* qbuf = smem;
   uint8_t* gbuf = qbuf + C::kTileBytes;
-  uint8_t* kvbuf = gbuf + C::kTileBytes;     // [ring], K and V tiles in turn
-  RowBars* bars = reinterpret_cast<RowBars*>(kvbuf + C::kRing * C::kTileBytes);
+  uint8_t* kbuf = gbuf + C::kTileBytes;      // [3]
+  uint8_t* vbuf = kbuf + 3 * C::kTileBytes;  // [2]
+  RowBars* bars = reinterpret_cast<RowBars*>(vbuf + 2 * C::kTileBytes);
   volatile int* abort = &bars->abort;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->q_full, 1);
     tc::mbar_init(&bars->q_empty, 1);
-    for (int s = 0; s < C::kRing; ++s) {
-      tc::mbar_init(&bars->kv_full[s], 1);
-      tc::mbar_init(&bars->kv_empty[s], 1);
+    for (int s = 0; s < 3; ++s) {
+      tc::mbar_init(&bars->k_full[s], 1);
+      tc::mbar_init(&bars->k_empty[s], 1);
     }
+    for (int s = 0; s < 2; ++s) {
+      tc::mbar_init(&bars->v_full[s], 1);
+      tc::mbar_init(&bars->v_empty[s], 1);
+    }
+    tc::mbar_init(&bars->first_full, 1);
     tc::mbar_init(&bars->s_full[0], 1);
     tc::mbar_init(&bars->s_full[1], 1);
     tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->ds_full, 8);
+    tc::mbar_init(&bars->ds_full, 9);   // 8 elementwise warps and warp 2
     tc::mbar_init(&bars->acc_full, 1);
     tc::mbar_init(&bars->acc_empty, 8);
     for (int i = 0; i < kItems; ++i) {
       tc::mbar_init(&bars->i_full[i], 1);
-      tc::mbar_init(&bars->i_empty[i], 9);
+      tc::mbar_init(&bars->i_empty[i], 10);
     }
     tc::mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
@@ -618,10 +672,10 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   if (warp == 0) {
     // ---------------- producer ----------------
     if (lane == 0) {
-      tc::ArmedRing q_armed, kv_armed;
-      int stage = 0;
-      uint32_t phase = 0;
-      int t = atomicAdd(next_item, 1);
+      tc::ArmedRing q_armed, k_armed, v_armed;
+      int ks = 0, vs = 0;
+      uint32_t kp = 0, vp = 0;
+      int t = blockIdx.x;  // the first item is the CTA's own
       for (int ii = 0; !failed; ++ii) {
         const int slot = ii % kItems;
         if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) {
@@ -647,19 +701,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         bars->item[slot] = it;
         tc::mbar_arrive(&bars->i_full[slot]);
         if (!it.live) break;
-        t = atomicAdd(next_item, 1);
         const int g = it.head / P.G;
-        auto load = [&](const CUtensorMap* map, int row) -> bool {
-          if (!tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1, abort)) return false;
-          uint64_t* fb = &bars->kv_full[stage];
-          tc::mbar_arrive_expect_tx(fb, C::kTileBytes);
-          kv_armed.note(stage, phase);
-#pragma unroll
-          for (int h = 0; h < D / 64; ++h)
-            tc::tma_load_3d(kvbuf + stage * C::kTileBytes + h * C::kHalf, map, fb, 64 * h, g, row);
-          if (++stage == C::kRing) { stage = 0; phase ^= 1; }
-          return true;
-        };
         if (!tc::mbar_wait(&bars->q_empty, (ii & 1) ^ 1, abort)) { failed = true; break; }
         tc::mbar_arrive_expect_tx(&bars->q_full, 2 * C::kTileBytes);
         q_armed.note(0, ii & 1);
@@ -668,20 +710,81 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           tc::tma_load_3d(qbuf + h * C::kHalf, &tmap_q, &bars->q_full, 64 * h, it.head, it.row0);
           tc::tma_load_3d(gbuf + h * C::kHalf, &tmap_g, &bars->q_full, 64 * h, it.head, it.row0);
         }
-        bool good = true;
-        for (int j = 0; j < it.n && good; ++j)
-          good = load(&tmap_k, k0 + j * 128) && load(&tmap_v, k0 + j * 128);
-        failed = !good;
+        for (int j = 0; j < it.n && !failed; ++j) {
+          if (!tc::mbar_wait(&bars->k_empty[ks], kp ^ 1, abort)) { failed = true; break; }
+          tc::mbar_arrive_expect_tx(&bars->k_full[ks], C::kTileBytes);
+          k_armed.note(ks, kp);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(kbuf + ks * C::kTileBytes + h * C::kHalf, &tmap_k, &bars->k_full[ks],
+                            64 * h, g, k0 + j * 128);
+          if (++ks == 3) { ks = 0; kp ^= 1; }
+          if (!tc::mbar_wait(&bars->v_empty[vs], vp ^ 1, abort)) { failed = true; break; }
+          tc::mbar_arrive_expect_tx(&bars->v_full[vs], C::kTileBytes);
+          v_armed.note(vs, vp);
+#pragma unroll
+          for (int h = 0; h < D / 64; ++h)
+            tc::tma_load_3d(vbuf + vs * C::kTileBytes + h * C::kHalf, &tmap_v, &bars->v_full[vs],
+                            64 * h, g, k0 + j * 128);
+          if (++vs == 2) { vs = 0; vp ^= 1; }
+        }
+        t = gridDim.x + atomicAdd(next_item, 1);
       }
-      if (!(q_armed.drain(&bars->q_full) && kv_armed.drain(bars->kv_full))) failed = true;
+      if (!(q_armed.drain(&bars->q_full) && k_armed.drain(bars->k_full) &&
+            v_armed.drain(bars->v_full)))
+        failed = true;
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
-    auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-      const bool ok = lane != 0 || tc::mbar_spin(bar, parity, abort);
-      return __shfl_sync(MSA_FULL_MASK, ok ? 1 : 0, 0) != 0;
-    };
-    long long n = 0;  // key tiles so far; tile x of K is load 2x of the ring, of V 2x + 1
+    if (tc::elect_one()) {
+      const uint32_t qa = kmajor(qbuf), ga = kmajor(gbuf), ka = kmajor(kbuf), va = kmajor(vbuf);
+      const uint32_t kb = mnmajor<D>(kbuf);
+      constexpr uint32_t kTile16 = C::kTileBytes / 16;
+      uint32_t n = 0;
+      int k0 = 0, k2 = 0, vs = 0;  // K stages of dQ and of S, V stage of dP
+      for (int ii = 0; !failed; ++ii) {
+        const int slot = ii % kItems;
+        if (!tc::mbar_spin(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
+        const RowItem it = bars->item[slot];
+        tc::mbar_arrive(&bars->i_empty[slot]);
+        if (!it.live) break;
+        const int last = (min(128, min(it.nk, it.pos + it.rows) - (it.n - 1) * 128) + 15) >> 4;
+        if (!tc::mbar_spin(&bars->first_full, ii & 1, abort)) { failed = true; break; }
+        tc::tc_fence_after();
+        auto scores = [&](int j) {
+          issue_nt<D>(tmem + uint32_t(j & 1) * 128, qa, ka + k2 * kTile16);
+          tc::mma_commit(&bars->s_full[j & 1]);
+          k2 = k2 == 2 ? 0 : k2 + 1;
+        };
+        auto products = [&]() {
+          issue_nt<D>(tp, ga, va + vs * kTile16);
+          tc::mma_commit(&bars->dp_full);
+          tc::mma_commit(&bars->v_empty[vs]);
+          vs ^= 1;
+        };
+        scores(0);
+        products();
+        if (it.n > 1) scores(1);
+        for (int j = 0; j < it.n; ++j, ++n) {
+          if (!tc::mbar_spin(&bars->ds_full, n & 1, abort)) { failed = true; break; }
+          tc::tc_fence_after();
+          issue_ts<D>(tq, tp, kb + k0 * kTile16, j == it.n - 1 ? last : 8, j > 0);
+          tc::mma_commit(&bars->k_empty[k0]);
+          k0 = k0 == 2 ? 0 : k0 + 1;
+          if (j + 1 < it.n) products();
+          if (j + 2 < it.n) scores(j + 2);
+        }
+        if (failed) break;
+        tc::mma_commit(&bars->q_empty);
+        tc::mma_commit(&bars->acc_full);
+      }
+      if (!tc::mma_drain(&bars->mma_done)) failed = true;
+    }
+  } else if (warp == 2) {
+    // ---------------- what else the products need ----------------
+    uint32_t n = 0;
+    int ks = 0, vs = 0;
+    uint32_t kp = 0, vp = 0;
     for (int ii = 0; !failed; ++ii) {
       const int slot = ii % kItems;
       if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
@@ -689,65 +792,37 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
       if (!it.live) break;
-      const int seen = min(it.nk, it.pos + it.rows);
-      const uint32_t qa = tc::smem_addr(qbuf), ga = tc::smem_addr(gbuf);
-      auto stage_of = [&](long long load) { return int(load % C::kRing); };
-      auto par_of = [&](long long load) { return uint32_t((load / C::kRing) & 1); };
-      auto scores = [&](int j) -> bool {
-        const long long x = 2 * (n + j);
-        const int s = stage_of(x), keys = min(128, seen - j * 128);
-        if (!wait(&bars->kv_full[s], par_of(x))) return false;
-        uint8_t* k = kvbuf + s * C::kTileBytes;
-        if (keys & 15) zero_rows<D>(k, keys, (keys + 15) & ~15);
-        if (lane == 0) {
-          tc::tc_fence_after();
-          issue_nt<D>(tmem + uint32_t(j & 1) * 128, qa, tc::smem_addr(k));
-          tc::mma_commit(&bars->s_full[j & 1]);
-        }
+      const int keys = min(128, min(it.nk, it.pos + it.rows) - (it.n - 1) * 128);  // last tile's
+      // K tile j has landed; rows behind what is seen are zero
+      auto key_tile = [&](int j) -> bool {
+        if (!warp_wait(&bars->k_full[ks], kp, abort)) return false;
+        if (j == it.n - 1 && (keys & 15))
+          zero_rows<D>(kbuf + ks * C::kTileBytes, keys, (keys + 15) & ~15);
+        if (++ks == 3) { ks = 0; kp ^= 1; }
         return true;
       };
-      auto products = [&](int j) -> bool {
-        const long long x = 2 * (n + j) + 1;
-        const int s = stage_of(x);
-        if (!wait(&bars->kv_full[s], par_of(x))) return false;
-        if (lane == 0) {
-          tc::tc_fence_after();
-          issue_nt<D>(tp, ga, tc::smem_addr(kvbuf + s * C::kTileBytes));
-          tc::mma_commit(&bars->dp_full);
-          tc::mma_commit(&bars->kv_empty[s]);
-        }
+      auto value_tile = [&]() -> bool {
+        if (!warp_wait(&bars->v_full[vs], vp, abort)) return false;
+        if (++vs == 2) { vs = 0; vp ^= 1; }
         return true;
       };
-      if (!wait(&bars->q_full, ii & 1) || !scores(0) || !products(0) ||
-          (it.n > 1 && !scores(1))) {
+      if (!warp_wait(&bars->q_full, ii & 1, abort) || !key_tile(0) || !value_tile() ||
+          (it.n > 1 && !key_tile(1))) {
         failed = true;
         break;
       }
-      for (int j = 0; j < it.n; ++j) {
-        if (!wait(&bars->ds_full, uint32_t((n + j) & 1)) ||
-            (j == 0 && !wait(&bars->acc_empty, (ii & 1) ^ 1))) {
+      if (lane == 0) tc::mbar_arrive(&bars->first_full);
+      for (int j = 0; j < it.n; ++j, ++n) {
+        // the arrival belongs to this step: the step before is over
+        if ((n > 0 && !warp_wait(&bars->ds_full, (n & 1) ^ 1, abort)) ||
+            (j == 0 && !warp_wait(&bars->acc_empty, (ii & 1) ^ 1, abort)) ||
+            (j + 1 < it.n && !value_tile()) || (j + 2 < it.n && !key_tile(j + 2))) {
           failed = true;
           break;
         }
-        const int s = stage_of(2 * (n + j)), keys = min(128, seen - j * 128);
-        if (lane == 0) {
-          tc::tc_fence_after();
-          issue_ts<D>(tq, tp, tc::smem_addr(kvbuf + s * C::kTileBytes), (keys + 15) >> 4, j == 0);
-          tc::mma_commit(&bars->kv_empty[s]);
-        }
-        if ((j + 1 < it.n && !products(j + 1)) || (j + 2 < it.n && !scores(j + 2))) {
-          failed = true;
-          break;
-        }
+        if (lane == 0) tc::mbar_arrive(&bars->ds_full);
       }
-      if (failed) break;
-      if (lane == 0) {
-        tc::mma_commit(&bars->q_empty);
-        tc::mma_commit(&bars->acc_full);
-      }
-      n += it.n;
     }
-    if (lane == 0 && !tc::mma_drain(&bars->mma_done)) failed = true;
   } else if (warp >= 4) {
     // ---------------- elementwise, then half of the tile's dQ columns ----------------
     const int half = (warp - 4) >> 2, quarter = warp & 3;
