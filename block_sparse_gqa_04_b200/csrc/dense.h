@@ -52,7 +52,7 @@ struct Tree {
   int rows;              // (node, head) rows of one work unit
   int groups;            // units per (sequence, key head)
   uint4* bits;           // tensor cores: the masks as bits, [masks, nodes + 1]
-  float* part_o;         // [2 * CTAs, rows, D] unnormalised partial outputs
+  float* part_o;         // [2 * CTAs, D, rows] unnormalised partial outputs
   float2* part_ml;       // [2 * CTAs, rows] base-2 running maximum and sum
 };
 

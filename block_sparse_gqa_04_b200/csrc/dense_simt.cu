@@ -491,11 +491,11 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
       const int r = ty + 16 * i;
       if (r >= rows) continue;
       if (p.slot >= 0) {
-        const long long at = (long long)(blockIdx.x * 2 + p.slot) * A.rows + r;
+        const long long at = (long long)(blockIdx.x * 2 + p.slot) * A.rows;
 #pragma unroll
-        for (int c = 0; c < D / 16; c += 4)
-          store4(A.part_o + at * D + tx * 4 + c * 16, &R.o[i][c], 1.f);
-        if (tx == 0) A.part_ml[at] = make_float2(R.m[i], R.l[i]);
+        for (int c = 0; c < D / 16; ++c)
+          A.part_o[at * D + (tx * 4 + (c / 4) * 64 + c % 4) * A.rows + r] = R.o[i][c];
+        if (tx == 0) A.part_ml[at + r] = make_float2(R.m[i], R.l[i]);
         continue;
       }
       const long long at = ((long long)p.b * nodes + (row0 + r) / P.G) * P.Hq + p.g * P.G +
@@ -511,16 +511,16 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Merge of the partial states of units that a share's border cut: a warp per row.
+// Merge of the partial states of units that a share's border cut: a block per unit and
+// 32 of its columns, a thread per row (the partial outputs have rows innermost).
 // ---------------------------------------------------------------------------
 template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kTcTreeRows)
 tree_combine_kernel(Tree A, int ctas, T* __restrict__ out, float* __restrict__ lse) {
   const Dense& P = A.d;
   const int nodes = P.Sq, per = P.Hkv * A.groups;
-  const int chunks = (A.rows + 7) / 8;
-  const int chunk = blockIdx.x % chunks, unit = (blockIdx.x / chunks) % per;
-  const int b = blockIdx.x / chunks / per, lane = threadIdx.x & 31;
+  const int c0d = (blockIdx.x % (D / 32)) * 32, unit = (blockIdx.x / (D / 32)) % per;
+  const int b = blockIdx.x / (D / 32) / per, lane = threadIdx.x & 31;
   const TreeSpan span = tree_span(A, ctas);
   long long before = 0;  // key tiles of the sequences before b
   for (int i = lane; i < b; i += 32) before += tree_seq(A, i).tiles;
@@ -530,32 +530,35 @@ tree_combine_kernel(Tree A, int ctas, T* __restrict__ out, float* __restrict__ l
   const long long t0 = before * per + (long long)unit * n;
   const int c0 = int(t0 / span.share), c1 = int((t0 + n - 1) / span.share);
   if (c0 == c1) return;
-  const int g = unit / A.groups, row0 = (unit % A.groups) * A.rows;
-  const int r = chunk * 8 + (threadIdx.x >> 5);
+  const int g = unit / A.groups, row0 = (unit % A.groups) * A.rows, r = threadIdx.x;
   if (r >= min(A.rows, nodes * P.G - row0)) return;
   // the unit's first piece lies in c0's slot 1, the others in their CTA's slot 0
-  auto at = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * A.rows + r; };
+  auto at = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * A.rows; };
   float m = -INFINITY;
-  for (int c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, A.part_ml[at(c)].x);
-  m = warp_max_f32(m);
+  for (int c = c0; c <= c1; ++c) m = fmaxf(m, A.part_ml[at(c) + r].x);
   const float base = m == -INFINITY ? 0.f : m;
-  constexpr int N = D / 32;
-  float o[N] = {}, l = 0.f;
-#pragma unroll 4
+  float o[32] = {}, l = 0.f;
   for (int c = c0; c <= c1; ++c) {
-    const float2 ml = A.part_ml[at(c)];
+    const float2 ml = A.part_ml[at(c) + r];
+    const float* x = A.part_o + at(c) * D + (long long)c0d * A.rows + r;
     const float w = exp2f(ml.x - base);
-    float x[N];
-    load_vec<float, N>(A.part_o + at(c) * D + lane * N, x);
     l += w * ml.y;
 #pragma unroll
-    for (int i = 0; i < N; ++i) o[i] += w * x[i];
+    for (int i = 0; i < 32; ++i) o[i] += w * x[i * A.rows];
   }
   const long long row = ((long long)b * nodes + (row0 + r) / P.G) * P.Hq + g * P.G + (row0 + r) % P.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
+  T* dst = out + row * D + c0d;
+  constexpr int vec = 16 / int(sizeof(T));
 #pragma unroll
-  for (int i = 0; i < N; ++i) out[row * D + lane * N + i] = from_f32<T>(o[i] * inv);
-  if (lse && lane == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+  for (int i = 0; i < 32; i += vec) {
+    uint4 u;
+    T* e = reinterpret_cast<T*>(&u);
+#pragma unroll
+    for (int x = 0; x < vec; ++x) e[x] = from_f32<T>(o[i + x] * inv);
+    *reinterpret_cast<uint4*>(dst + i) = u;
+  }
+  if (lse && c0d == 0) lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 namespace {
@@ -614,15 +617,15 @@ cudaError_t tree(const Tree& A, const void* q, const void* k, const void* v, voi
 }  // namespace
 
 cudaError_t launch_tree_combine(const Tree& A, void* out, float* lse, cudaStream_t s) {
-  const long long blocks = (long long)A.d.B * A.d.Hkv * A.groups * ((A.rows + 7) / 8);
+  const long long blocks = (long long)A.d.B * A.d.Hkv * A.groups * (A.d.D / 32);
   const int ctas = tree_ctas();
   if (A.d.f32) {
     auto kern = A.d.D == 128 ? tree_combine_kernel<float, 128> : tree_combine_kernel<float, 64>;
-    kern<<<unsigned(blocks), kThreads, 0, s>>>(A, ctas, static_cast<float*>(out), lse);
+    kern<<<unsigned(blocks), A.rows, 0, s>>>(A, ctas, static_cast<float*>(out), lse);
   } else {
     auto kern = A.d.D == 128 ? tree_combine_kernel<__nv_bfloat16, 128>
                              : tree_combine_kernel<__nv_bfloat16, 64>;
-    kern<<<unsigned(blocks), kThreads, 0, s>>>(A, ctas, static_cast<__nv_bfloat16*>(out), lse);
+    kern<<<unsigned(blocks), A.rows, 0, s>>>(A, ctas, static_cast<__nv_bfloat16*>(out), lse);
   }
   return cudaGetLastError();
 }

@@ -9,8 +9,7 @@
 // launch to join.
 //
 // Inside a CTA the even and the odd key tiles of a piece are two independent chains,
-// each with its own MMA-issuing thread, softmax warpgroup, running maximum and sum, and
-// accumulator O, so that one chain's MMAs and copies run under the other's softmax;
+// each with its own softmax warpgroup, running maximum and sum, and accumulator O, so that one chain's MMAs and copies run under the other's softmax;
 // the epilogue joins the two.  Scores, probabilities and the moving maximum are as in
 // the forward pass over whole prompts.  K and V tiles come through a ring of TMA
 // stages (160 KB in flight); Q rows are gathered by one warp, a piece ahead.
@@ -25,7 +24,7 @@
 namespace msa {
 namespace {
 
-// warp 0 pieces and TMA, warps 1-2 MMA, warp 3 Q rows, warps 4-11 softmax, 12-15 epilogue
+// warp 0 pieces and TMA, warp 1 MMA, warp 2 waits for it, warp 3 Q rows, warps 4-11 softmax, 12-15 epilogue
 constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItems = 2;
@@ -52,9 +51,10 @@ struct Item {
 struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t kv_full[8], kv_empty[8];
-  // per chain: S computed, P written, each P V done, the piece's last P V done, O read,
-  // (maximum, sum) written, read
-  uint64_t s_full[2], p_full[2], o_step[2], o_done[2], o_empty[2], l_full[2], l_empty[2];
+  // first_full: the CTA's first Q and K tiles are there; per chain: S computed, P written
+  // (and what its products need is there), the piece's last P V done, O read, (maximum,
+  // sum) written, read
+  uint64_t first_full, s_full[2], p_full[2], o_done[2], o_empty[2], l_full[2], l_empty[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint64_t mma_done;
   Item item[kItems];
@@ -137,10 +137,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     for (int b = 0; b < 2; ++b) {
       tc::mbar_init(&bars->q_full[b], 1);
-      tc::mbar_init(&bars->q_empty[b], 2);   // both chains' issuers
+      tc::mbar_init(&bars->q_empty[b], 1);
       tc::mbar_init(&bars->s_full[b], 1);
-      tc::mbar_init(&bars->p_full[b], 4);
-      tc::mbar_init(&bars->o_step[b], 1);
+      tc::mbar_init(&bars->p_full[b], 5);    // the chain's softmax warps and warp 2
       tc::mbar_init(&bars->o_done[b], 1);
       tc::mbar_init(&bars->o_empty[b], 4);
       tc::mbar_init(&bars->l_full[b], 4);
@@ -148,9 +147,10 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
     }
     for (int i = 0; i < kItems; ++i) {
       tc::mbar_init(&bars->i_full[i], 1);
-      tc::mbar_init(&bars->i_empty[i], 15);  // 2 MMA, Q, 8 softmax, 4 epilogue warps
+      tc::mbar_init(&bars->i_empty[i], 15);  // warps 1-3, 8 softmax, 4 epilogue warps
     }
-    tc::mbar_init(&bars->mma_done, 2);
+    tc::mbar_init(&bars->first_full, 1);
+    tc::mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
     tc::fence_mbar_init();
   }
@@ -169,115 +169,176 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
     regs_dec<kRegsCtl>();
     if (warp == 0) {
       // ---------------- producer: pieces and TMA ----------------
-      tc::ArmedRing kv_armed;
-      int stage = 0;
-      uint32_t phase = 0;
       if (blockIdx.x == 0)
         for (int b = lane; b < P.B; b += 32)
           if (A.kv_lens[b] < 0 || A.kv_lens[b] > P.Skv - nodes) atomicOr(status, kStatusBadLength);
       TreeWalk w;
       w.begin(A, blockIdx.x, tree_span(A, gridDim.x));
-      for (int ii = 0; !failed; ++ii) {
-        const int slot = ii % kItems;
-        TreeWalk::Piece p{};
-        const bool live = w.next(A, &p);
-        bool good = true;
-        if (lane == 0) {
-          good = tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort);
-          if (good) {
-            const int row0 = p.group * 128;
-            bars->item[slot] = Item{live, p.b, p.g, row0, min(128, nodes * P.G - row0),
-                                    p.kt0, p.kt1 - p.kt0, p.len, p.slot};
-            tc::mbar_arrive(&bars->i_full[slot]);
-          }
-        }
-        if (!__shfl_sync(MSA_FULL_MASK, good, 0)) { failed = true; break; }
-        if (!live) break;
-        for (int j0 = p.kt0; j0 < p.kt1 && !failed; j0 += 32) {
-          // the rows of 32 tiles at a time: their pages come with one load
-          int row = 0;
-          if (j0 + lane < p.kt1) {
-            if (P.table) {
-              const int pg = P.table[(long long)p.b * P.table_w + j0 + lane];
-              const bool in = pg >= 0 && pg < P.pages;
-              if (!in) atomicOr(status, kStatusBadPage);
-              row = in ? pg * kDenseTile : 0;
-            } else {
-              row = p.b * P.Skv + (j0 + lane) * kDenseTile;
-            }
-          }
-          for (int j = 0; j < 32 && j0 + j < p.kt1; ++j) {
-            const int r = __shfl_sync(MSA_FULL_MASK, row, j);
-            if (lane == 0) {
-#pragma unroll
-              for (int x = 0; x < 2; ++x) {
-                good = good && tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1, abort);
-                if (!good) break;
-                uint64_t* fb = &bars->kv_full[stage];
-                uint8_t* dst = kvbuf + stage * C::kTileBytes;
-                tc::mbar_arrive_expect_tx(fb, C::kTileBytes);
-                kv_armed.note(stage, phase);
-#pragma unroll
-                for (int h = 0; h < D / 64; ++h)
-                  tc::tma_load_3d(dst + h * C::kHalf, x ? &tmap_v : &tmap_k, fb, 64 * h, p.g, r);
-                if (++stage == C::kStages) { stage = 0; phase ^= 1; }
-              }
-            }
-            if (!__shfl_sync(MSA_FULL_MASK, good, 0)) { failed = true; break; }
-          }
-        }
-      }
-      if (lane == 0 && !kv_armed.drain(bars->kv_full)) failed = true;
-    } else if (warp < 3) {
-      // ---------------- MMA issuer of chain e ----------------
-      const int e = warp - 1;
-      const uint32_t st = tmem + e * 256, ot = st + 128;
-      long long n0 = 0;      // key tiles of the pieces before
-      int on = 0, un = 0;    // key tiles of this chain, pieces in which it has any
-      auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-        const bool ok = lane != 0 || tc::mbar_spin(bar, parity, abort);
-        return __shfl_sync(MSA_FULL_MASK, ok ? 1 : 0, 0) != 0;
-      };
-      for (int ii = 0; !failed; ++ii) {
-        const int slot = ii % kItems;
-        if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
-        const Item it = bars->item[slot];
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
-        if (!it.live) break;
-        const int qs = ii & 1;
-        if (!wait(&bars->q_full[qs], (ii >> 1) & 1)) { failed = true; break; }
-        const int last = it.n - 1 - ((it.n - 1 - e) & 1);  // the chain's last tile, if any
-        for (int j = e; j < it.n; j += 2) {
-          const long long x = 2 * (n0 + j);
-          const int ks = int(x % C::kStages), vs = int((x + 1) % C::kStages);
-          if (!wait(&bars->kv_full[ks], uint32_t((x / C::kStages) & 1))) { failed = true; break; }
-          if (lane == 0) {
-            tc::tc_fence_after();
-            const uint32_t qa = tc::smem_addr(qbuf + qs * C::kTileBytes);
-            const uint32_t ka = tc::smem_addr(kvbuf + ks * C::kTileBytes);
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t off = (kk >> 2) * C::kHalf + (kk & 3) * 32;
-              tc::mma_ss(st, tc::sdesc_sw128(qa + off, 16, 1024),
-                         tc::sdesc_sw128(ka + off, 16, 1024), C::kIdescS, kk > 0 ? 1u : 0u);
-            }
-            tc::mma_commit(&bars->s_full[e]);
-            tc::mma_commit(&bars->kv_empty[ks]);
-          }
-          if (!wait(&bars->kv_full[vs], uint32_t(((x + 1) / C::kStages) & 1))) {
+      if (tc::elect_one()) {
+        tc::ArmedRing kv_armed;
+        int stage = 0;
+        uint32_t phase = 0;
+        for (int ii = 0; !failed; ++ii) {
+          const int slot = ii % kItems;
+          TreeWalk::Piece p{};
+          const bool live = w.next(A, &p);
+          if (!tc::mbar_wait(&bars->i_empty[slot], ((ii / kItems) & 1) ^ 1, abort)) {
             failed = true;
             break;
           }
-          uint8_t* v = kvbuf + vs * C::kTileBytes;
-          const int off = it.len - (it.kt0 + j) * 128;     // tile's row of drafted token 0
-          const int keys = min(128, off + nodes), groups = (keys + 15) >> 4;
+          const int row0 = p.group * 128;
+          bars->item[slot] = Item{live, p.b, p.g, row0, min(128, nodes * P.G - row0),
+                                  p.kt0, p.kt1 - p.kt0, p.len, p.slot};
+          tc::mbar_arrive(&bars->i_full[slot]);
+          if (!live) break;
+          const int32_t* pages = P.table ? P.table + (long long)p.b * P.table_w : nullptr;
+          int page = pages ? pages[p.kt0] : 0;
+          for (int j = p.kt0; j < p.kt1 && !failed; ++j) {
+            int row = p.b * P.Skv + j * kDenseTile;
+            if (pages) {
+              const bool in = page >= 0 && page < P.pages;
+              if (!in) atomicOr(status, kStatusBadPage);
+              row = in ? page * kDenseTile : 0;
+              if (j + 1 < p.kt1) page = pages[j + 1];  // on its way during this tile's copies
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              if (!tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1, abort)) { failed = true; break; }
+              uint64_t* fb = &bars->kv_full[stage];
+              uint8_t* dst = kvbuf + stage * C::kTileBytes;
+              tc::mbar_arrive_expect_tx(fb, C::kTileBytes);
+              kv_armed.note(stage, phase);
+#pragma unroll
+              for (int h = 0; h < D / 64; ++h)
+                tc::tma_load_3d(dst + h * C::kHalf, x ? &tmap_v : &tmap_k, fb, 64 * h, p.g, row);
+              if (++stage == C::kStages) { stage = 0; phase ^= 1; }
+            }
+          }
+        }
+        if (!kv_armed.drain(bars->kv_full)) failed = true;
+      }
+    } else if (warp == 1) {
+      // ---------------- MMA issuer ----------------
+      // S of tiles 0 and 1, then P V of tile x followed by S of tile x + 2 (of the next
+      // piece's first tiles at the end); one barrier per pair of products (warp 2).
+      if (tc::elect_one()) {
+        constexpr uint32_t kHi = uint32_t(tc::kDescHi | (1024 >> 4));
+        constexpr uint32_t kTile16 = C::kTileBytes / 16, kHalf16 = C::kHalf / 16;
+        const uint32_t qd = uint32_t(tc::sdesc_sw128(tc::smem_addr(qbuf), 16, 1024));
+        const uint32_t kd = uint32_t(tc::sdesc_sw128(tc::smem_addr(kvbuf), 16, 1024));
+        const uint32_t vd = uint32_t(tc::sdesc_sw128(tc::smem_addr(kvbuf), C::kHalf, 1024));
+        int ii = 0, kx = 0, vx = 1;   // pieces; ring positions of the next K and V tile
+        uint32_t ppar = 0;
+        auto advance = [](int x) { return x + 2 >= C::kStages ? x + 2 - C::kStages : x + 2; };
+        auto fetch = [&](Item* it) -> bool {
+          const int slot = ii % kItems;
+          if (!tc::mbar_spin(&bars->i_full[slot], (ii / kItems) & 1, abort)) return false;
+          *it = bars->item[slot];
+          tc::mbar_arrive(&bars->i_empty[slot]);
+          ++ii;
+          return true;
+        };
+        // S of tile x of the piece whose Q stage is qs
+        auto scores = [&](int x, int qs, bool last) {
+          const uint32_t a = qd + qs * kTile16, b = kd + kx * kTile16;
+          const uint32_t st = tmem + (x & 1) * 256;
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf16 + (kk & 3) * 2;
+            tc::mma_ss_lo(st, a + off, b + off, kHi, C::kIdescS, kk > 0 ? 1u : 0u);
+          }
+          tc::mma_commit(&bars->s_full[x & 1]);
+          tc::mma_commit(&bars->kv_empty[kx]);
+          if (last) tc::mma_commit(&bars->q_empty[qs]);
+          kx = advance(kx);
+        };
+        Item cur{};
+        failed = !fetch(&cur);
+        if (!failed && cur.live) {
+          failed = !tc::mbar_spin(&bars->first_full, 0, abort);
+          tc::tc_fence_after();
+          if (!failed) {
+            scores(0, 0, cur.n == 1);
+            if (cur.n > 1) scores(1, 0, cur.n == 2);
+          }
+        }
+        while (!failed && cur.live) {
+          const int n = cur.n, qs = (ii - 1) & 1;
+          int off = cur.len - cur.kt0 * 128;   // tile's row of drafted token 0
+          for (int x = 0; x < n; ++x, off -= 128) {
+            const int e = x & 1;
+            const uint32_t st = tmem + e * 256, v = vd + vx * kTile16;
+            if (x == n - 1 && !fetch(&cur)) { failed = true; break; }
+            if (!tc::mbar_spin(&bars->p_full[e], (ppar >> e) & 1, abort)) { failed = true; break; }
+            ppar ^= 1u << e;
+            tc::tc_fence_after();
+            const int groups = (min(128, off + nodes) + 15) >> 4;
+            if (groups == 8) {
+#pragma unroll
+              for (int kk = 0; kk < 8; ++kk)
+                tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
+                              kk > 0 ? 1u : uint32_t(x >= 2));
+            } else {
+#pragma unroll 1
+              for (int kk = 0; kk < groups; ++kk)
+                tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
+                              kk > 0 ? 1u : uint32_t(x >= 2));
+            }
+            tc::mma_commit(&bars->kv_empty[vx]);
+            vx = advance(vx);
+            if (x + 2 >= n) tc::mma_commit(&bars->o_done[e]);
+            if (x + 2 < n) {
+              scores(x + 2, qs, x + 3 == n);
+            } else if (x == n - 1 && cur.live) {
+              scores(0, qs ^ 1, cur.n == 1);
+              if (cur.n > 1) scores(1, qs ^ 1, cur.n == 2);
+            }
+          }
+        }
+        if (!tc::mma_drain(&bars->mma_done)) failed = true;
+      }
+    } else if (warp == 2) {
+      // ---------------- what else the products need ----------------
+      // One arrival per tile at p_full of its chain: V has landed, with the rows that no
+      // node sees zeroed, K of the scores that follow too, the epilogue has read the
+      // chain's previous O.
+      int ii = 0, kx = 0, vx = 1;
+      uint32_t kp = 0, vp = 0, un[2] = {0, 0}, on[2] = {0, 0};
+      auto fetch = [&](Item* it) -> bool {
+        const int slot = ii % kItems;
+        if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) return false;
+        *it = bars->item[slot];
+        __syncwarp();
+        if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
+        ++ii;
+        return true;
+      };
+      auto landed = [&](int* x, uint32_t* ph) -> bool {
+        if (!warp_wait(&bars->kv_full[*x], *ph, abort)) return false;
+        *x += 2;
+        if (*x >= C::kStages) { *x -= C::kStages; *ph ^= 1; }
+        return true;
+      };
+      // Q of the piece just fetched, and its first K tiles
+      auto start = [&](const Item& it) -> bool {
+        return warp_wait(&bars->q_full[(ii - 1) & 1], ((ii - 1) >> 1) & 1, abort) &&
+               landed(&kx, &kp) && (it.n == 1 || landed(&kx, &kp));
+      };
+      Item cur{}, nxt{};
+      failed = !fetch(&cur) || (cur.live && !start(cur));
+      if (!failed && cur.live && lane == 0) tc::mbar_arrive(&bars->first_full);
+      while (!failed && cur.live) {
+        int off = cur.len - cur.kt0 * 128;
+        for (int x = 0; x < cur.n; ++x, off -= 128) {
+          const int e = x & 1, vs = vx;
+          if (!landed(&vx, &vp)) { failed = true; break; }
           if (off < 128) {
-            // drafted tokens that nobody sees, and what is behind them
-            const uint4 seen = A.bits[(long long)(A.mask_stride ? it.b : 0) * (nodes + 1) + nodes];
-            for (int r0 = max(0, off) & ~31; r0 < groups * 16; r0 += 32) {
+            uint8_t* v = kvbuf + vs * C::kTileBytes;
+            const int rows = (min(128, off + nodes) + 15) & ~15;
+            const uint4 seen = A.bits[(long long)(A.mask_stride ? cur.b : 0) * (nodes + 1) + nodes];
+            for (int r0 = max(0, off) & ~31; r0 < rows; r0 += 32) {
               uint32_t w = ~bits_at(seen, r0 - off);
-              if (groups * 16 - r0 < 32) w &= (1u << (groups * 16 - r0)) - 1u;
+              if (rows - r0 < 32) w &= (1u << (rows - r0)) - 1u;
               while (w) {
                 const int r = r0 + __ffs(w) - 1;
                 w &= w - 1;
@@ -289,33 +350,19 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
             tc::fence_async_smem();
             __syncwarp();
           }
-          if (!wait(&bars->p_full[e], on & 1) ||
-              (j == e && !wait(&bars->o_empty[e], (un & 1) ^ 1))) {
+          // the arrival belongs to this tile: the chain's tile before is over
+          if ((on[e] > 0 && !warp_wait(&bars->p_full[e], (on[e] & 1) ^ 1, abort)) ||
+              (x < 2 && !warp_wait(&bars->o_empty[e], (un[e]++ & 1) ^ 1, abort)) ||
+              (x + 2 < cur.n && !landed(&kx, &kp)) ||
+              (x == cur.n - 1 && (!fetch(&nxt) || (nxt.live && !start(nxt))))) {
             failed = true;
             break;
           }
-          if (lane == 0) {
-            tc::tc_fence_after();
-            const uint32_t va = tc::smem_addr(v);
-            for (int kk = 0; kk < groups; ++kk)
-              tc::mma_ts(ot, st + kk * 8, tc::sdesc_sw128(va + kk * 2048, C::kHalf, 1024),
-                         C::kIdescO, (j > e || kk > 0) ? 1u : 0u);
-            tc::mma_commit(&bars->kv_empty[vs]);
-            tc::mma_commit(&bars->o_step[e]);
-            if (j == last) tc::mma_commit(&bars->o_done[e]);
-          }
-          ++on;
+          ++on[e];
+          if (lane == 0) tc::mbar_arrive(&bars->p_full[e]);
         }
-        if (failed) break;
-        // the chain is done with the piece's Q
-        if (lane == 0) {
-          if (it.n > e) tc::mma_commit(&bars->q_empty[qs]);
-          else tc::mbar_arrive(&bars->q_empty[qs]);
-        }
-        if (it.n > e) ++un;
-        n0 += it.n;
+        cur = nxt;
       }
-      if (lane == 0 && !tc::mma_drain(&bars->mma_done)) failed = true;
     } else {
       // ---------------- Q rows ----------------
       constexpr int kChunks = D / 8;   // 16-byte chunks of a row
@@ -425,8 +472,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
             }
           }
           if (j > e && __any_sync(MSA_FULL_MASK, grow)) {
-            if (!warp_wait(&bars->o_step[e], (on & 1) ^ 1, abort)) { failed = true; break; }
-            tc::tc_fence_after();
+            // the previous P V was issued before this S: O is there
             const uint64_t k2 = f2(keep, keep);
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -491,6 +537,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
       const int r = it.row0 + row;
       const long long at = whole ? ((long long)it.b * nodes + r / P.G) * P.Hq + it.g * P.G + r % P.G
                                  : (long long)(blockIdx.x * 2 + it.slot) * 128 + row;
+      float* part = A.part_o + (long long)(blockIdx.x * 2 + it.slot) * 128 * D + row;
       if (mine) {
         if (!whole) A.part_ml[at] = make_float2(m, l);
         else if (lse) lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -528,9 +575,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                              pack_bf16(o[i + 4], o[i + 5]), pack_bf16(o[i + 6], o[i + 7]));
           } else if (mine) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 4)
-              *reinterpret_cast<float4*>(A.part_o + at * D + c + i) =
-                  make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+            for (int i = 0; i < 16; ++i) part[(c + i) * 128] = o[i];
           }
         }
       }
