@@ -202,7 +202,7 @@ msa_status_t resolve_tree(const msa_problem_t* p, Tree* T) {
   if (p->q_len > kMaxNodes || T->d.G > 128) return MSA_ERR_UNSUPPORTED;
   T->rows = T->d.f32 ? msa::kSimtTreeRows : msa::kTcTreeRows;
   T->groups = (T->d.Sq * T->d.G + T->rows - 1) / T->rows;
-  if ((long long)T->d.B * T->d.Hkv * T->groups * (T->d.D / 32) >= (1LL << 31) ||
+  if ((long long)T->d.B * T->d.Hkv * T->groups * (T->d.D / 8) >= (1LL << 31) ||
       (long long)T->d.B * T->d.Hkv * T->groups >= (1LL << 31))
     return MSA_ERR_UNSUPPORTED;
   return MSA_OK;

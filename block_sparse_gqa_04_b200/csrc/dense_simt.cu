@@ -512,15 +512,15 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
 
 // ---------------------------------------------------------------------------
 // Merge of the partial states of units that a share's border cut: a block per unit and
-// 32 of its columns, a thread per row (the partial outputs have rows innermost).
+// 8 of its columns, a thread per row (the partial outputs have rows innermost).
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 __global__ void __launch_bounds__(kTcTreeRows)
 tree_combine_kernel(Tree A, int ctas, T* __restrict__ out, float* __restrict__ lse) {
   const Dense& P = A.d;
   const int nodes = P.Sq, per = P.Hkv * A.groups;
-  const int c0d = (blockIdx.x % (D / 32)) * 32, unit = (blockIdx.x / (D / 32)) % per;
-  const int b = blockIdx.x / (D / 32) / per, lane = threadIdx.x & 31;
+  const int c0d = (blockIdx.x % (D / 8)) * 8, unit = (blockIdx.x / (D / 8)) % per;
+  const int b = blockIdx.x / (D / 8) / per, lane = threadIdx.x & 31;
   const TreeSpan span = tree_span(A, ctas);
   long long before = 0;  // key tiles of the sequences before b
   for (int i = lane; i < b; i += 32) before += tree_seq(A, i).tiles;
@@ -537,21 +537,22 @@ tree_combine_kernel(Tree A, int ctas, T* __restrict__ out, float* __restrict__ l
   float m = -INFINITY;
   for (int c = c0; c <= c1; ++c) m = fmaxf(m, A.part_ml[at(c) + r].x);
   const float base = m == -INFINITY ? 0.f : m;
-  float o[32] = {}, l = 0.f;
+  float o[8] = {}, l = 0.f;
+#pragma unroll 4
   for (int c = c0; c <= c1; ++c) {
     const float2 ml = A.part_ml[at(c) + r];
     const float* x = A.part_o + at(c) * D + (long long)c0d * A.rows + r;
     const float w = exp2f(ml.x - base);
     l += w * ml.y;
 #pragma unroll
-    for (int i = 0; i < 32; ++i) o[i] += w * x[i * A.rows];
+    for (int i = 0; i < 8; ++i) o[i] += w * x[i * A.rows];
   }
   const long long row = ((long long)b * nodes + (row0 + r) / P.G) * P.Hq + g * P.G + (row0 + r) % P.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
   T* dst = out + row * D + c0d;
   constexpr int vec = 16 / int(sizeof(T));
 #pragma unroll
-  for (int i = 0; i < 32; i += vec) {
+  for (int i = 0; i < 8; i += vec) {
     uint4 u;
     T* e = reinterpret_cast<T*>(&u);
 #pragma unroll
@@ -617,7 +618,7 @@ cudaError_t tree(const Tree& A, const void* q, const void* k, const void* v, voi
 }  // namespace
 
 cudaError_t launch_tree_combine(const Tree& A, void* out, float* lse, cudaStream_t s) {
-  const long long blocks = (long long)A.d.B * A.d.Hkv * A.groups * (A.d.D / 32);
+  const long long blocks = (long long)A.d.B * A.d.Hkv * A.groups * (A.d.D / 8);
   const int ctas = tree_ctas();
   if (A.d.f32) {
     auto kern = A.d.D == 128 ? tree_combine_kernel<float, 128> : tree_combine_kernel<float, 64>;

@@ -663,13 +663,14 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 template <int D>
 cudaError_t fwd_tc(const Dense& P, const void* q, const void* k, const void* v, void* out,
                    float* lse, int32_t* counter, int32_t* status, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
   CUtensorMap mq, mk, mv, mo;
   cudaError_t e = encode_rows(&mq, q, D, P.Hq, P.rows_q);
   if (e == cudaSuccess) e = encode_rows(&mo, out, D, P.Hq, P.rows_q, 32);
   if (e == cudaSuccess) e = encode_rows(&mk, k, D, P.Hkv, P.rows_k);
   if (e == cudaSuccess) e = encode_rows(&mv, v, D, P.Hkv, P.rows_k);
   if (e == cudaSuccess)
-    e = prepare_kernel(dense_fwd_tc_kernel<D>, smem_bytes<D>(),
+    e = prepare_kernel(&done, dense_fwd_tc_kernel<D>, smem_bytes<D>(),
                        kRegsCtl + kRegsEpi + 2 * kRegsSoftmax, kThreads);
   if (e != cudaSuccess) return e;
   dense_fwd_tc_kernel<D><<<std::min(sm_count(), P.pairs), kThreads, smem_bytes<D>(), s>>>(

@@ -1,6 +1,8 @@
 // Shared pieces of the tensor-core kernels of the dense operators.
 #pragma once
 
+#include <atomic>
+
 #include "dense_common.cuh"
 #include "tc_warp.cuh"
 
@@ -43,14 +45,23 @@ inline cudaError_t encode_rows(CUtensorMap* map, const void* base, int D, int he
 
 // Shared memory of a kernel, and the registers that its setmaxnreg split needs, 0
 // without one (a build with fewer would leave warpgroups waiting for registers forever).
+// Done once per device (`done`: a bit per device, one word per kernel).
 template <typename K>
-inline cudaError_t prepare_kernel(K kern, size_t smem, int split, int threads) {
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+inline cudaError_t prepare_kernel(std::atomic<uint64_t>* done, K kern, size_t smem, int split,
+                                  int threads) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done->load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
   if (e != cudaSuccess) return e;
   cudaFuncAttributes fa;
   e = cudaFuncGetAttributes(&fa, kern);
   if (e != cudaSuccess) return e;
-  return fa.numRegs * (threads / 128) < split ? cudaErrorInvalidConfiguration : cudaSuccess;
+  if (fa.numRegs * (threads / 128) < split) return cudaErrorInvalidConfiguration;
+  done->fetch_or(bit, std::memory_order_release);
+  return cudaSuccess;
 }
 
 }  // namespace msa

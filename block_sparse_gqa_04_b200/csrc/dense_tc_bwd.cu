@@ -943,14 +943,16 @@ cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* 
     e = cudaMemsetAsync(dk, 0, kelems * 2, s);
     return e == cudaSuccess ? cudaMemsetAsync(dv, 0, kelems * 2, s) : e;
   }
+  static std::atomic<uint64_t> done[3];
   CUtensorMap mq, mg, mk, mv;
   e = encode_rows(&mq, q, D, P.Hq, P.rows_q);
   if (e == cudaSuccess) e = encode_rows(&mg, dout, D, P.Hq, P.rows_q);
   if (e == cudaSuccess) e = encode_rows(&mk, k, D, P.Hkv, P.rows_k);
   if (e == cudaSuccess) e = encode_rows(&mv, v, D, P.Hkv, P.rows_k);
   auto dkv = splits > 1 ? dense_dkv_tc_kernel<D, true> : dense_dkv_tc_kernel<D, false>;
-  if (e == cudaSuccess) e = prepare_kernel(dkv, key_smem<D>(), 0, kThreads);
-  if (e == cudaSuccess) e = prepare_kernel(dense_dq_tc_kernel<D>, row_smem<D>(), 0, kThreads);
+  if (e == cudaSuccess) e = prepare_kernel(&done[splits > 1], dkv, key_smem<D>(), 0, kThreads);
+  if (e == cudaSuccess)
+    e = prepare_kernel(&done[2], dense_dq_tc_kernel<D>, row_smem<D>(), 0, kThreads);
   if (e != cudaSuccess) return e;
   const long long warps = P.rows_pad / 16 * P.Hq;
   dense_prep_kernel<D><<<unsigned((warps + 7) / 8), 256, 0, s>>>(

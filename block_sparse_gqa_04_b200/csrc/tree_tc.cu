@@ -603,11 +603,12 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
 template <int D>
 cudaError_t tree_tc(const Tree& A, const void* q, const void* k, const void* v, void* out,
                     float* lse, int32_t* status, cudaStream_t s) {
+  static std::atomic<uint64_t> done{0};
   CUtensorMap mk, mv;
   cudaError_t e = encode_rows(&mk, k, D, A.d.Hkv, A.d.rows_k);
   if (e == cudaSuccess) e = encode_rows(&mv, v, D, A.d.Hkv, A.d.rows_k);
   if (e == cudaSuccess)
-    e = prepare_kernel(tree_tc_kernel<D>, smem_bytes<D>(), kRegsCtl + kRegsEpi + 2 * kRegsSoftmax,
+    e = prepare_kernel(&done, tree_tc_kernel<D>, smem_bytes<D>(), kRegsCtl + kRegsEpi + 2 * kRegsSoftmax,
                        kThreads);
   if (e != cudaSuccess) return e;
   tree_prep_kernel<<<A.mask_stride ? A.d.B : 1, 256, 0, s>>>(A.mask, A.mask_stride, A.d.Sq, A.bits,

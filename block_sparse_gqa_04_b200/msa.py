@@ -10,6 +10,7 @@ to the device and back), the call raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Tuple
 
@@ -692,16 +693,19 @@ def forward_varlen(q, k, v, q_idx, k_idx, cu_seqlens_q, cu_seqlens_k, *, block_s
 # Dense attention, tree attention and the norm and rotation of heads
 # ---------------------------------------------------------------------------
 def _one_device(first, *ts):
-    """All tensors on the first one's CUDA device."""
-    for t in (first,) + ts:
-        if t is not None and not t.is_cuda:
-            raise ValueError("libmsa takes CUDA tensors")
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and on {t.device}")
+    """All tensors on the first one's CUDA device; its index."""
+    dev = first.get_device()
+    if dev < 0:
+        raise ValueError("libmsa takes CUDA tensors")
+    for t in ts:
+        if t is not None and t.get_device() != dev:
+            raise ValueError("libmsa takes CUDA tensors" if not t.is_cuda else
+                             f"tensors on {first.device} and on {t.device}")
+    return dev
 
 
 def _want(name, t, shape, dtype):
-    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}, got "
                          f"{t.dtype} {tuple(t.shape)}")
 
@@ -711,72 +715,112 @@ def _main_dtype(t):
         raise ValueError(f"expected bf16 or fp32 tensors, got {t.dtype}")
 
 
-def _new_ws(nbytes, workspace, dev, where):
+def _addr(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
+
+
+def _run(where, dev, fn, *args):
+    """fn(*args, the current stream of CUDA device `dev`) with that device current."""
+    stream = torch._C._cuda_getCurrentRawStream(dev)
+    if torch.cuda.current_device() == dev:
+        code = fn(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            code = fn(*args, stream)
+    if code:
+        raise MsaError(code, where)
+
+
+def _new_ws(nbytes, workspace, like, where):
+    """(address, bytes) of the workspace, and the tensor that holds it."""
     if nbytes == 0:
         raise MsaError(1, where)
     if workspace is None:
-        workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=dev)
-    elif workspace.device != dev or workspace.dtype != torch.uint8:
-        raise ValueError(f"workspace must be a uint8 tensor on {dev}")
-    return _ws_view(workspace)
+        workspace = torch.empty(nbytes + 256, dtype=torch.uint8, device=like.device)
+    elif workspace.device != like.device or workspace.dtype != torch.uint8:
+        raise ValueError(f"workspace must be a uint8 tensor on {like.device}")
+    wp, wn = _ws_view(workspace)
+    return wp, wn, workspace
 
 
 def _raise_device_status(wp, dev, where):
     code = ctypes.c_int32(0)
-    _check(load().msa_device_status(ctypes.c_void_p(wp), ctypes.byref(code), _stream(dev)),
-           f"{where} (device status)")
+    _run(f"{where} (device status)", dev, load().msa_device_status, wp, ctypes.byref(code))
 
 
-def _dense_setup(q, k, v, cu_q, cu_k, q_pos0, softmax_scale, block_table=None, kv_len=None):
-    """(Problem, cu_q, cu_k as ctypes arrays or None) of a dense call, all checked."""
+@functools.lru_cache(maxsize=512)
+def _plan(op, B, Sq, Skv, Hq, Hkv, D, dtype, q_pos0, scale, pages):
+    """(Problem, workspace bytes) of a call on these sizes; a paged call fills its block
+    table into a copy."""
+    p = make_problem(B, Sq, Skv, Hq, Hkv, D, 32, dtype=dtype, q_pos0=q_pos0, softmax_scale=scale)
+    if pages:
+        p.num_pages, p.block_table = pages, 256  # any address: only sizes are looked at here
+    lib = load()
+    n = (lib.msa_tree_workspace_size(ctypes.byref(p)) if op == "tree" else
+         lib.msa_dense_workspace_size(ctypes.byref(p), None, None, int(op == "backward")))
+    return p, n
+
+
+def _with_table(p, block_table):
+    if block_table is None:
+        return p
+    p = Problem.from_buffer_copy(p)
+    p.block_table = block_table.data_ptr()
+    return p
+
+
+def _dense_setup(op, q, k, v, cu_q, cu_k, q_pos0, softmax_scale, block_table=None, kv_len=None):
+    """(Problem, cu_q, cu_k as ctypes arrays or None, workspace bytes, device index) of a
+    dense call, all checked."""
     _main_dtype(q)
     packed = cu_q is not None
     lead = 1 if packed else 2
-    if q.dim() != lead + 2 or k.dim() != (4 if block_table is not None else lead + 2):
+    qs, ks = q.shape, k.shape
+    if len(qs) != lead + 2 or len(ks) != (4 if block_table is not None else lead + 2):
         raise ValueError("dense attention takes q [B, Sq, Hq, D] with k, v [B, Skv, Hkv, D], or "
                          "packed q [total_q, Hq, D] with k, v [total_k, Hkv, D]")
-    Hq, D = q.shape[-2:]
-    Hkv = k.shape[-2]
+    Hq, D = qs[-2:]
+    Hkv = ks[-2]
     if packed:
-        kshape = (k.shape[0], Hkv, D)
+        kshape = (ks[0], Hkv, D)
     elif block_table is not None:
-        kshape = (k.shape[0], 128, Hkv, D)
+        kshape = (ks[0], 128, Hkv, D)
     else:
-        kshape = (q.shape[0], k.shape[1], Hkv, D)
-    _want("q", q, q.shape, q.dtype)
-    _want("k", k, kshape, q.dtype)
-    _want("v", v, kshape, q.dtype)
-    _one_device(q, k, v, block_table)
+        kshape = (qs[0], ks[1], Hkv, D)
+    dt = q.dtype
+    _want("q", q, qs, dt)
+    _want("k", k, kshape, dt)
+    _want("v", v, kshape, dt)
+    dev = _one_device(q, k, v, block_table)
     if packed:
-        p, cq, ck = varlen_problem(cu_q, cu_k, Hq, Hkv, D, 32, dtype=q.dtype,
+        p, cq, ck = varlen_problem(cu_q, cu_k, Hq, Hkv, D, 32, dtype=dt,
                                    softmax_scale=softmax_scale)
-        if cq[len(cq) - 1] != q.shape[0] or ck[len(ck) - 1] != k.shape[0]:
+        if cq[len(cq) - 1] != qs[0] or ck[len(ck) - 1] != ks[0]:
             raise ValueError(f"the prefix sums end at {cq[len(cq) - 1]} / {ck[len(ck) - 1]}, "
-                             f"the tensors hold {q.shape[0]} / {k.shape[0]} rows")
-        return p, cq, ck
-    pg = _paged(block_table, kv_len, q.shape[0], k.shape[0], 128)
-    p = make_problem(q.shape[0], q.shape[1], int(kv_len) if pg else k.shape[1], Hq, Hkv, D, 32,
-                     dtype=q.dtype, q_pos0=q_pos0, softmax_scale=softmax_scale, **pg)
-    return p, None, None
+                             f"the tensors hold {qs[0]} / {ks[0]} rows")
+        n = load().msa_dense_workspace_size(ctypes.byref(p), cq, ck, int(op == "backward"))
+        return p, cq, ck, n, dev
+    pages = _paged(block_table, kv_len, qs[0], ks[0], 128).get("num_pages", 0)
+    p, n = _plan(op, qs[0], qs[1], int(kv_len) if pages else ks[1], Hq, Hkv, D, dt, int(q_pos0),
+                 float(softmax_scale), pages)
+    return _with_table(p, block_table), None, None, n, dev
 
 
 def _dense_forward(where, q, k, v, cu_q, cu_k, q_pos0, softmax_scale, return_lse, workspace, out,
                    check_device_status, block_table=None, kv_len=None):
-    p, cq, ck = _dense_setup(q, k, v, cu_q, cu_k, q_pos0, softmax_scale, block_table, kv_len)
-    dev = q.device
+    p, cq, ck, n, dev = _dense_setup("forward", q, k, v, cu_q, cu_k, q_pos0, softmax_scale,
+                                     block_table, kv_len)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _want("out", out, q.shape, q.dtype)
-    _one_device(q, out)
-    lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=dev) if return_lse else None
-    lib = load()
-    wp, wn = _new_ws(lib.msa_dense_workspace_size(ctypes.byref(p), cq, ck, 0), workspace, dev,
-                     where)
-    with torch.cuda.device(dev):
-        _check(lib.msa_dense_attend(ctypes.byref(p), cq, ck, _ptr(q), _ptr(k), _ptr(v), _ptr(out),
-                                    _ptr(lse), ctypes.c_void_p(wp), wn, _stream(dev)), where)
-        if check_device_status:
-            _raise_device_status(wp, dev, where)
+        out = torch.empty_like(q)
+    else:
+        _want("out", out, q.shape, q.dtype)
+        _one_device(q, out)
+    lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if return_lse else None
+    wp, wn, workspace = _new_ws(n, workspace, q, where)
+    _run(where, dev, load().msa_dense_attend, ctypes.byref(p), cq, ck, q.data_ptr(), k.data_ptr(),
+         v.data_ptr(), out.data_ptr(), _addr(lse), wp, wn)
+    if check_device_status:
+        _raise_device_status(wp, dev, where)
     return (out, lse) if return_lse else out
 
 
@@ -806,22 +850,18 @@ def dense_attend_varlen(q, k, v, cu_seqlens_q, cu_seqlens_k, *, softmax_scale: f
 def _dense_grads(dout, q, k, v, out, lse, cu_q, cu_k, q_pos0, softmax_scale, workspace,
                  check_device_status):
     where = "msa_dense_backward"
-    p, cq, ck = _dense_setup(q, k, v, cu_q, cu_k, q_pos0, softmax_scale)
-    dev = q.device
+    p, cq, ck, n, dev = _dense_setup("backward", q, k, v, cu_q, cu_k, q_pos0, softmax_scale)
     _want("dout", dout, q.shape, q.dtype)
     _want("out", out, q.shape, q.dtype)
     _want("lse", lse, q.shape[:-1], torch.float32)
     _one_device(q, dout, out, lse)
     dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
-    lib = load()
-    wp, wn = _new_ws(lib.msa_dense_workspace_size(ctypes.byref(p), cq, ck, 1), workspace, dev,
-                     where)
-    with torch.cuda.device(dev):
-        _check(lib.msa_dense_backward(ctypes.byref(p), cq, ck, _ptr(dout), _ptr(q), _ptr(k),
-                                      _ptr(v), _ptr(out), _ptr(lse), _ptr(dq), _ptr(dk), _ptr(dv),
-                                      ctypes.c_void_p(wp), wn, _stream(dev)), where)
-        if check_device_status:
-            _raise_device_status(wp, dev, where)
+    wp, wn, workspace = _new_ws(n, workspace, q, where)
+    _run(where, dev, load().msa_dense_backward, ctypes.byref(p), cq, ck, dout.data_ptr(),
+         q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(), lse.data_ptr(), dq.data_ptr(),
+         dk.data_ptr(), dv.data_ptr(), wp, wn)
+    if check_device_status:
+        _raise_device_status(wp, dev, where)
     return dq, dk, dv
 
 
@@ -856,35 +896,36 @@ def tree_attend(q, k, v, tree_mask, kv_lens, *, softmax_scale: float = 0.0,
     gets zeros and lse -inf.  With n = 1 and a mask of one True this is a decoding step.
     Returns out like q (and lse [B, n, Hq])."""
     where = "msa_tree_attend"
-    if q.dim() != 4 or k.dim() != 4:
+    qs, ks = q.shape, k.shape
+    if len(qs) != 4 or len(ks) != 4:
         raise ValueError("tree attention takes q [B, n, Hq, D] and a cache [B, capacity, Hkv, D] "
                          "or [pages, 128, Hkv, D]")
     _main_dtype(q)
-    B, n, Hq, D = q.shape
-    Hkv = k.shape[2]
-    kshape = (k.shape[0], 128, Hkv, D) if block_table is not None else (B, k.shape[1], Hkv, D)
-    _want("q", q, q.shape, q.dtype)
-    _want("k", k, kshape, q.dtype)
-    _want("v", v, kshape, q.dtype)
+    B, n, Hq, D = qs
+    Hkv, dt = ks[2], q.dtype
+    kshape = (ks[0], 128, Hkv, D) if block_table is not None else (B, ks[1], Hkv, D)
+    each = tree_mask.dim() == 3
+    _want("q", q, qs, dt)
+    _want("k", k, kshape, dt)
+    _want("v", v, kshape, dt)
     _want("kv_lens", kv_lens, (B,), torch.int32)
-    _want("tree_mask", tree_mask, (n, n) if tree_mask.dim() == 2 else (B, n, n), torch.bool)
-    _one_device(q, k, v, kv_lens, tree_mask, block_table, out)
-    pg = _paged(block_table, kv_len, B, k.shape[0], 128)
-    p = make_problem(B, n, int(kv_len) if pg else k.shape[1], Hq, Hkv, D, 32, dtype=q.dtype,
-                     softmax_scale=softmax_scale, **pg)
-    dev = q.device
+    _want("tree_mask", tree_mask, (B, n, n) if each else (n, n), torch.bool)
+    dev = _one_device(q, k, v, kv_lens, tree_mask, block_table, out)
+    pages = _paged(block_table, kv_len, B, ks[0], 128).get("num_pages", 0)
+    p, nbytes = _plan("tree", B, n, int(kv_len) if pages else ks[1], Hq, Hkv, D, dt, 0,
+                      float(softmax_scale), pages)
+    p = _with_table(p, block_table)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    _want("out", out, q.shape, q.dtype)
-    lse = torch.empty((B, n, Hq), dtype=torch.float32, device=dev) if return_lse else None
-    lib = load()
-    wp, wn = _new_ws(lib.msa_tree_workspace_size(ctypes.byref(p)), workspace, dev, where)
-    with torch.cuda.device(dev):
-        _check(lib.msa_tree_attend(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(v), _ptr(tree_mask),
-                                   n * n if tree_mask.dim() == 3 else 0, _ptr(kv_lens), _ptr(out),
-                                   _ptr(lse), ctypes.c_void_p(wp), wn, _stream(dev)), where)
-        if check_device_status:
-            _raise_device_status(wp, dev, where)
+        out = torch.empty_like(q)
+    else:
+        _want("out", out, qs, dt)
+    lse = q.new_empty((B, n, Hq), dtype=torch.float32) if return_lse else None
+    wp, wn, workspace = _new_ws(nbytes, workspace, q, where)
+    _run(where, dev, load().msa_tree_attend, ctypes.byref(p), q.data_ptr(), k.data_ptr(),
+         v.data_ptr(), tree_mask.data_ptr(), n * n if each else 0, kv_lens.data_ptr(),
+         out.data_ptr(), _addr(lse), wp, wn)
+    if check_device_status:
+        _raise_device_status(wp, dev, where)
     return (out, lse) if return_lse else out
 
 
@@ -901,33 +942,36 @@ class NormRope(ctypes.Structure):
     ]
 
 
-def _row_stride(name, t, lead, dtype):
-    """Elements between the rows of t [*lead, H, D]: heads contiguous, rows evenly
-    spaced on 16-byte boundaries (t may be a slice of a fused projection's output)."""
-    H, D = t.shape[-2:]
-    if tuple(t.shape[:-2]) != tuple(lead) or t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype} {tuple(lead) + (H, D)}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
-    rows = 1
-    for n in lead:
-        rows *= n
-    if rows == 0:
+@functools.lru_cache(maxsize=1024)
+def _rows_of(shape, stride, esz):
+    """Elements between the rows of a [.., H, D] layout: heads contiguous, rows evenly
+    spaced on 16-byte boundaries (a slice of a fused projection's output, say).  None if it
+    is not such a layout."""
+    H, D = shape[-2:]
+    if 0 in shape[:-2]:
         return H * D
-    want, stride = None, H * D
-    for n, st in zip(reversed(t.shape[:-2]), reversed(t.stride()[:-2])):
+    want, step = None, H * D
+    for n, st in zip(reversed(shape[:-2]), reversed(stride[:-2])):
         if n == 1:
             continue
         if want is None:
-            stride, want = st, st * n
+            step = st
         elif st != want:
-            raise ValueError(f"{name}'s rows are not evenly spaced: strides {t.stride()}")
-        else:
-            want = st * n
-    heads_ok = (H == 1 or t.stride(-2) == D) and t.stride(-1) == 1
-    if not heads_ok or stride < H * D or stride * t.element_size() % 16:
-        raise ValueError(f"{name} needs contiguous heads and rows on 16-byte boundaries: "
-                         f"shape {tuple(t.shape)}, strides {t.stride()}")
-    return stride
+            return None
+        want = st * n
+    heads_ok = (H == 1 or stride[-2] == D) and stride[-1] == 1
+    return step if heads_ok and step >= H * D and step * esz % 16 == 0 else None
+
+
+def _row_stride(name, t, lead, dtype):
+    if t.shape[:-2] != lead or t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype} {tuple(lead) + tuple(t.shape[-2:])}, got "
+                         f"{t.dtype} {tuple(t.shape)}")
+    step = _rows_of(t.shape, t.stride(), t.element_size())
+    if step is None:
+        raise ValueError(f"{name} needs contiguous heads and evenly spaced rows on 16-byte "
+                         f"boundaries: shape {tuple(t.shape)}, strides {t.stride()}")
+    return step
 
 
 def _span(t, stride):
@@ -955,25 +999,28 @@ def _check_overlap(name, dst, stride, *others):
 
 
 def _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
+    """(NormRope with the strides of q and k, device index), all checked."""
     _main_dtype(q)
-    lead, (Hq, D) = q.shape[:-2], q.shape[-2:]
-    if q.dim() < 3 or (k is not None and (k.dim() != q.dim() or k.shape[-1] != D)):
+    dt, qs = q.dtype, q.shape
+    lead, (Hq, D) = qs[:-2], qs[-2:]
+    if len(qs) < 3 or (k is not None and (k.dim() != len(qs) or k.shape[-1] != D)):
         raise ValueError("q and k are [.., heads, D] with the same leading sizes and D")
     if (k is None) != (k_weight is None):
         raise ValueError("k and k_weight come together")
-    _one_device(q, k, q_weight, k_weight, inv_freq, positions)
-    _want("q_weight", q_weight, (D,), q.dtype)
+    dev = _one_device(q, k, q_weight, k_weight, inv_freq, positions)
+    _want("q_weight", q_weight, (D,), dt)
+    Hk = kstep = 0
     if k is not None:
-        _want("k_weight", k_weight, (D,), q.dtype)
+        _want("k_weight", k_weight, (D,), dt)
+        Hk, kstep = k.shape[-2], _row_stride("k", k, lead, dt)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a vector")
     _want("inv_freq", inv_freq, inv_freq.shape, torch.float64)
     _want("positions", positions, lead, torch.int64)
-    rows = positions.numel()
-    return NormRope(rows, Hq, k.shape[-2] if k is not None else 0, D, 2 * inv_freq.numel(),
-                    int(interleaved), MSA_F32 if q.dtype == torch.float32 else MSA_BF16, eps, 0,
-                    _row_stride("q", q, lead, q.dtype),
-                    _row_stride("k", k, lead, q.dtype) if k is not None else 0, 0, 0, 0, 0)
+    p = NormRope(positions.numel(), Hq, Hk, D, 2 * inv_freq.numel(), interleaved,
+                 MSA_F32 if dt == torch.float32 else MSA_BF16, eps, 0,
+                 _row_stride("q", q, lead, dt), kstep, Hq * D, Hk * D, Hq * D, Hk * D)
+    return p, dev
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps: float = 1e-6,
@@ -986,29 +1033,26 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps: float = 
     elements (i, i + rotary_dim/2), or (2i, 2i + 1) if interleaved.  Serves the index
     branch's q_idx and k_idx (as [.., 1, D]) too.  Returns (q_out, k_out), new tensors
     or out=(q_out, k_out), which may be q and k themselves."""
-    p = _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
-    lead = q.shape[:-2]
+    p, dev = _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
     if out is None:
-        out = (torch.empty(q.shape, dtype=q.dtype, device=q.device),
-               None if k is None else torch.empty(k.shape, dtype=q.dtype, device=q.device))
+        qo = q.new_empty(q.shape)
+        ko = None if k is None else k.new_empty(k.shape)
     else:
         qo, ko = out
         if qo.shape != q.shape or (ko is None) != (k is None) or (
                 k is not None and ko.shape != k.shape):
             raise ValueError("out must be (q_out, k_out) shaped like q and k")
         _one_device(q, qo, ko)
-    qo, ko = out
-    p.q_out_stride = _row_stride("q_out", qo, lead, q.dtype)
-    if k is not None:
-        p.k_out_stride = _row_stride("k_out", ko, lead, q.dtype)
-    ins = [(q, p.q_stride)] + ([(k, p.k_stride)] if k is not None else [])
-    _check_overlap("q_out", qo, p.q_out_stride, *ins)
-    if k is not None:
-        _check_overlap("k_out", ko, p.k_out_stride, (qo, p.q_out_stride), *ins)
-    with torch.cuda.device(q.device):
-        _check(load().msa_qk_norm_rope(ctypes.byref(p), _ptr(q), _ptr(k), _ptr(q_weight),
-                                       _ptr(k_weight), _ptr(inv_freq), _ptr(positions), _ptr(qo),
-                                       _ptr(ko), _stream(q.device)), "msa_qk_norm_rope")
+        lead, ins = q.shape[:-2], [(q, p.q_stride)]
+        p.q_out_stride = _row_stride("q_out", qo, lead, q.dtype)
+        if k is not None:
+            ins.append((k, p.k_stride))
+            p.k_out_stride = _row_stride("k_out", ko, lead, q.dtype)
+            _check_overlap("k_out", ko, p.k_out_stride, (qo, p.q_out_stride), *ins)
+        _check_overlap("q_out", qo, p.q_out_stride, *ins)
+    _run("msa_qk_norm_rope", dev, load().msa_qk_norm_rope, ctypes.byref(p), q.data_ptr(), _addr(k),
+         q_weight.data_ptr(), _addr(k_weight), inv_freq.data_ptr(), positions.data_ptr(),
+         qo.data_ptr(), _addr(ko))
     return qo, ko
 
 
@@ -1019,27 +1063,23 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, po
     dq_weight, dk_weight): dq and dk contiguous in the inputs' dtype, the weights'
     gradients fp32 [D] (dk, dk_weight None without k)."""
     where = "msa_qk_norm_rope_backward"
-    p = _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
-    lead, dev = q.shape[:-2], q.device
+    p, dev = _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
+    lead, D = q.shape[:-2], q.shape[-1]
     if dq_out.shape != q.shape or (dk_out is None) != (k is None) or (
             k is not None and dk_out.shape != k.shape):
         raise ValueError("dq_out and dk_out must be shaped like q and k")
     _one_device(q, dq_out, dk_out)
     p.q_out_stride = _row_stride("dq_out", dq_out, lead, q.dtype)
-    p.dq_stride = q.shape[-2] * q.shape[-1]
-    dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-    dqw = torch.empty(q.shape[-1], dtype=torch.float32, device=dev)
+    dq, dqw = q.new_empty(q.shape), q.new_empty((D,), dtype=torch.float32)
     dk = dkw = None
     if k is not None:
         p.k_out_stride = _row_stride("dk_out", dk_out, lead, q.dtype)
-        p.dk_stride = k.shape[-2] * k.shape[-1]
-        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        dkw = torch.empty(k.shape[-1], dtype=torch.float32, device=dev)
+        dk, dkw = k.new_empty(k.shape), k.new_empty((D,), dtype=torch.float32)
     lib = load()
-    wp, wn = _new_ws(lib.msa_norm_rope_workspace_size(ctypes.byref(p)), workspace, dev, where)
-    with torch.cuda.device(dev):
-        _check(lib.msa_qk_norm_rope_backward(
-            ctypes.byref(p), _ptr(dq_out), _ptr(dk_out), _ptr(q), _ptr(k), _ptr(q_weight),
-            _ptr(k_weight), _ptr(inv_freq), _ptr(positions), _ptr(dq), _ptr(dk), _ptr(dqw),
-            _ptr(dkw), ctypes.c_void_p(wp), wn, _stream(dev)), where)
+    wp, wn, workspace = _new_ws(lib.msa_norm_rope_workspace_size(ctypes.byref(p)), workspace, q,
+                                where)
+    _run(where, dev, lib.msa_qk_norm_rope_backward, ctypes.byref(p), dq_out.data_ptr(),
+         _addr(dk_out), q.data_ptr(), _addr(k), q_weight.data_ptr(), _addr(k_weight),
+         inv_freq.data_ptr(), positions.data_ptr(), dq.data_ptr(), _addr(dk), dqw.data_ptr(),
+         _addr(dkw), wp, wn)
     return dq, dk, dqw, dkw
