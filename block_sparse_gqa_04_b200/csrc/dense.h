@@ -68,8 +68,8 @@ cudaError_t launch_dense_fwd_simt(const Dense& P, const void* q, const void* k, 
 cudaError_t launch_dense_fwd_tc(const Dense& P, const void* q, const void* k, const void* v,
                                 void* out, float* lse, int32_t* counter, int32_t* status,
                                 cudaStream_t s);
-// Scratch of the tensor-core gradients: -lse log2 e and delta, [Hq, rows_pad] + 128
-// values each, and with several splits their partial sums, [splits][2][rows_k, Hkv, D].
+// Scratch of the gradients: on the tensor cores -lse log2 e and delta, [Hq, rows_pad] +
+// 128 values each, in fp32 delta [rows_q, Hq]; with several splits their partial sums, [splits][2][rows_k, Hkv, D].
 struct DenseBwdSpace {
   float *nl, *dl, *part;
 };
@@ -79,13 +79,19 @@ cudaError_t launch_dense_bwd_tc(const Dense& P, const void* dout, const void* q,
                                 const void* v, const void* out, const float* lse,
                                 const DenseBwdSpace& W, void* dq, void* dk, void* dv,
                                 int32_t* counters, int32_t* status, cudaStream_t s);
+// fp32 on the CUDA cores (nl unused).
 cudaError_t launch_dense_bwd_simt(const Dense& P, const void* dout, const void* q, const void* k,
-                                  const void* v, const void* out, const float* lse, float* delta,
-                                  void* dq, void* dk, void* dv, cudaStream_t s);
+                                  const void* v, const void* out, const float* lse,
+                                  const DenseBwdSpace& W, void* dq, void* dk, void* dv,
+                                  cudaStream_t s);
+// dk, dv = the sum of the splits' partial sums [splits][dv, dk][n], dk scaled.
+template <typename T>
+cudaError_t launch_dkv_sum(const float* part, int splits, long long n, float scale, T* dk, T* dv,
+                           cudaStream_t s);
 
-constexpr int kSimtTreeRows = 64;  // rows of a work unit on the CUDA cores
+constexpr int kSimtTreeRows = 32;  // rows of a work unit on the CUDA cores
 constexpr int kTcTreeRows = 128;   // and on the tensor cores
-int tree_ctas();                   // CTAs of a tree launch: one per SM
+int tree_ctas(bool f32);           // CTAs of a tree launch
 // Joins the partial states (second launch of either tree kernel).
 cudaError_t launch_tree_combine(const Tree& T, void* out, float* lse, cudaStream_t s);
 cudaError_t launch_tree_simt(const Tree& T, const void* q, const void* k, const void* v, void* out,

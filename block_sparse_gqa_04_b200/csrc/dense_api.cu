@@ -149,13 +149,12 @@ DenseLayout dense_layout(const Dense& P, bool packed, bool backward) {
   auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
   L.status = take(kHeadBytes);
   if (packed) L.recs = take(size_t(P.B) * sizeof(SeqRec));
-  if (backward && P.f32) {
-    L.delta = take(size_t(P.rows_q) * P.Hq * sizeof(float));
-  } else if (backward) {
-    const size_t rows = (size_t(P.rows_pad) * P.Hq + msa::kDenseTile) * sizeof(float);
+  if (backward) {
+    const size_t rows = P.f32 ? size_t(P.rows_q) * P.Hq
+                              : size_t(P.rows_pad) * P.Hq + msa::kDenseTile;
     const int splits = msa::dense_bwd_splits(P);
-    L.nl = take(rows);
-    L.delta = take(rows);
+    if (!P.f32) L.nl = take(rows * sizeof(float));
+    L.delta = take(rows * sizeof(float));
     if (splits > 1) L.part = take(size_t(splits) * 2 * P.rows_k * P.Hkv * P.D * sizeof(float));
   }
   L.total = off;
@@ -216,7 +215,7 @@ TreeLayout tree_layout(const Tree& T) {
   TreeLayout L{};
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
-  const size_t rows = size_t(msa::tree_ctas()) * 2 * T.rows;
+  const size_t rows = size_t(msa::tree_ctas(T.d.f32)) * 2 * T.rows;
   L.status = take(sizeof(int32_t));
   if (!T.d.f32) L.bits = take(size_t(T.d.B) * (T.d.Sq + 1) * sizeof(uint4));
   L.part_o = take(rows * T.d.D * sizeof(float));
@@ -297,11 +296,11 @@ msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlen
   if ((st = check_ws(ws, ws_bytes, L.total)) != MSA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
   if ((st = begin(&P, R, L, ws, s)) != MSA_OK) return st;
-  if (P.f32)
-    return msa::status_of(msa::launch_dense_bwd_simt(P, dout, q, k, v, out, lse,
-                                                     at<float>(ws, L.delta), dq, dk, dv, s));
   int32_t* head = at<int32_t>(ws, L.status);
   const msa::DenseBwdSpace W{at<float>(ws, L.nl), at<float>(ws, L.delta), at<float>(ws, L.part)};
+  if (P.f32)
+    return msa::status_of(
+        msa::launch_dense_bwd_simt(P, dout, q, k, v, out, lse, W, dq, dk, dv, s));
   return msa::status_of(
       msa::launch_dense_bwd_tc(P, dout, q, k, v, out, lse, W, dq, dk, dv, head + 1, head, s));
 }
@@ -345,7 +344,7 @@ msa_status_t msa_tree_attend(const msa_problem_t* p, const void* q, const void* 
 size_t msa_norm_rope_workspace_size(const msa_norm_rope_t* p) {
   msa::NormRope P;
   if (resolve_norm(p, &P) != MSA_OK) return 0;
-  return align_up(size_t(std::max(1, msa::norm_rope_partials(P))) * 2 * P.D * sizeof(float));
+  return align_up(size_t(std::max(1, msa::norm_rope_partials(P))) * P.D * sizeof(float));
 }
 
 msa_status_t msa_qk_norm_rope(const msa_norm_rope_t* p, const void* q, const void* k,
@@ -441,10 +440,11 @@ cudaError_t launch_dense_check_table(const Dense& P, int32_t* status, cudaStream
   return cudaGetLastError();
 }
 
-int tree_ctas() {
+int tree_ctas(bool f32) {
   // the SM count of a B200: a fixed number, so that the workspace size and the way
-  // the work is cut do not depend on the device that happens to be current
-  return 148;
+  // the work is cut do not depend on the device that happens to be current; the small
+  // blocks of the fp32 kernel run two to an SM
+  return f32 ? 2 * 148 : 148;
 }
 
 }  // namespace msa

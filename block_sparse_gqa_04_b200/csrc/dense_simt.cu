@@ -1,38 +1,44 @@
 // Dense attention in fp32 on the CUDA cores: forward, gradients, and the tree form
 // over a cache.
 //
-// One block holds a tile of 64 query rows and walks the 64-key tiles those rows can
-// see, with the running maximum and sum of the softmax (one pass over the keys):
+// One block holds 32 rows (queries, or keys for their gradients) and walks the 64-row
+// tiles of the other side that they see, with the running maximum and sum of the softmax
+// (one pass over the keys):
 //   S = Q K^T, m' = max(m, max S), P = 2^(S - m'), l = l 2^(m - m') + sum P,
 //   O = O 2^(m - m') + P V
-// in base 2 with the scale folded into the exponent.  256 threads form a 16 x 16
-// grid; a thread owns 4 rows x 4 keys of S (rows and keys 16 apart) and the same
-// rows of D/16 columns of O.  The products are register-tiled from shared memory:
-// 64 FMAs per 8 16-byte loads for S.  Bound by the FMA pipe and those loads.
+// in base 2 with the scale folded into the exponent.  128 threads form an 8 x 16 grid; a
+// thread owns 4 rows (8 apart) x 4 columns (16 apart) of S and the same rows of D/16
+// columns of O.  The products are register-tiled from shared memory: 64 FMAs per 8
+// 16-byte loads.  Bound by the FMA pipe and those loads; 32 rows rather than 64 give small
+// problems twice the blocks and half the longest one.
+#include <algorithm>
+
 #include "dense_common.cuh"
 
 namespace msa {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 64;
+constexpr int kThreads = 128;
+constexpr int kRows = 32;    // rows of a block
+constexpr int kTile = 64;    // columns at a time
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
 template <int D>
 struct Smem {
   static constexpr int kPitch = D + 4;  // rows 4 banks apart: 16-byte loads of 8 rows do not collide
-  static constexpr int kTileFloats = kTile * kPitch;
+  static constexpr int kRowFloats = kRows * kPitch, kTileFloats = kTile * kPitch;
   static constexpr int kPPitch = kTile + 4;
-  static constexpr int kPFloats = kTile * kPPitch;
+  static constexpr int kPFloats = kRows * kPPitch;
 };
 
-// Rows 0..63 of `src` (row r at src + r * stride elements) into an fp32 tile; rows
+// Rows 0 .. N-1 of `src` (row r at src + r * stride elements) into an fp32 tile; rows
 // from `valid` on are zero.
-template <typename T, int D>
+template <typename T, int D, int N>
 __device__ __forceinline__ void load_tile(float* dst, const T* src, long long stride, int valid) {
   constexpr int vec = 16 / int(sizeof(T)), lanes = D / vec;
-  for (int i = threadIdx.x; i < kTile * lanes; i += kThreads) {
+#pragma unroll 8
+  for (int i = threadIdx.x; i < N * lanes; i += kThreads) {
     const int r = i / lanes, c = (i % lanes) * vec;
     float x[vec];
     if (r < valid) {
@@ -48,7 +54,7 @@ __device__ __forceinline__ void load_tile(float* dst, const T* src, long long st
   }
 }
 
-// acc[i][j] += A[row ty + 16 i] . B[row tx + 16 j] over D columns.
+// acc[i][j] += A[row ty + 8 i] . B[row tx + 16 j] over D columns.
 template <int D>
 __device__ __forceinline__ void product_nt(const float* A, const float* B, int ty, int tx,
                                            float (&acc)[4][4]) {
@@ -58,7 +64,7 @@ __device__ __forceinline__ void product_nt(const float* A, const float* B, int t
     float4 a[4], b[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      a[i] = *reinterpret_cast<const float4*>(A + (ty + 16 * i) * P + d);
+      a[i] = *reinterpret_cast<const float4*>(A + (ty + 8 * i) * P + d);
       b[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * P + d);
     }
 #pragma unroll
@@ -73,7 +79,7 @@ __device__ __forceinline__ void product_nt(const float* A, const float* B, int t
   }
 }
 
-// acc[i][c] += sum_k W[row ty + 16 i][k] * B[k][col], W [64][kPPitch], columns
+// acc[i][c] += sum_k W[row ty + 8 i][k] * B[k][col], W [32][kPPitch], columns
 // tx * 4 + 64 * (c / 4) + c % 4 (D = 64: 4 columns, 128: 8).
 template <int D>
 __device__ __forceinline__ void product_nn(const float* W, const float* B, int ty, int tx,
@@ -83,7 +89,7 @@ __device__ __forceinline__ void product_nn(const float* W, const float* B, int t
   for (int k = 0; k < kTile; k += 4) {
     float4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty + 16 * i) * PP + k);
+    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty + 8 * i) * PP + k);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
 #pragma unroll
@@ -97,30 +103,6 @@ __device__ __forceinline__ void product_nn(const float* W, const float* B, int t
           acc[i][c + 2] = fmaf(x, b.z, acc[i][c + 2]);
           acc[i][c + 3] = fmaf(x, b.w, acc[i][c + 3]);
         }
-      }
-    }
-  }
-}
-
-// acc[i][c] += sum_r W[r][row ty + 16 i] * B[r][col]: product_nn with W transposed.
-template <int D>
-__device__ __forceinline__ void product_tn(const float* W, const float* B, int ty, int tx,
-                                           float (&acc)[4][D / 16]) {
-  constexpr int P = Smem<D>::kPitch, PP = Smem<D>::kPPitch;
-#pragma unroll 4
-  for (int r = 0; r < kTile; ++r) {
-    float w[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = W[r * PP + ty + 16 * i];
-#pragma unroll
-    for (int c = 0; c < D / 16; c += 4) {
-      const float4 b = *reinterpret_cast<const float4*>(B + r * P + tx * 4 + c * 16);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        acc[i][c] = fmaf(w[i], b.x, acc[i][c]);
-        acc[i][c + 1] = fmaf(w[i], b.y, acc[i][c + 1]);
-        acc[i][c + 2] = fmaf(w[i], b.z, acc[i][c + 2]);
-        acc[i][c + 3] = fmaf(w[i], b.w, acc[i][c + 3]);
       }
     }
   }
@@ -164,7 +146,7 @@ struct Running {
       for (int j = 0; j < 4; ++j) {
         const float p = exp2f(s[i][j] - base);
         sum += p;
-        Ps[(ty + 16 * i) * Smem<D>::kPPitch + tx + 16 * j] = p;
+        Ps[(ty + 8 * i) * Smem<D>::kPPitch + tx + 16 * j] = p;
       }
       l[i] = l[i] * keep + sum16(sum);
 #pragma unroll
@@ -181,11 +163,14 @@ __device__ __forceinline__ void store4(T* dst, const float* x, float scale) {
 
 template <int D>
 constexpr size_t fwd_smem() {
-  return sizeof(float) * (3 * Smem<D>::kTileFloats + Smem<D>::kPFloats);
+  return sizeof(float) * (Smem<D>::kRowFloats + 2 * Smem<D>::kTileFloats + Smem<D>::kPFloats);
 }
 
+// Blocks of a 128-row tile.
+constexpr int kParts = kDenseTile / kRows;
+
 // ---------------------------------------------------------------------------
-// Forward over whole prompts: block = (query tile half, head)
+// Forward over whole prompts: block = (32 query rows, head)
 // ---------------------------------------------------------------------------
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
@@ -193,28 +178,29 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
                       const T* __restrict__ v, T* __restrict__ out, float* __restrict__ lse) {
   extern __shared__ float sm[];
   float* Qs = sm;
-  float* Ks = Qs + Smem<D>::kTileFloats;
+  float* Ks = Qs + Smem<D>::kRowFloats;
   float* Vs = Ks + Smem<D>::kTileFloats;
   float* Ps = Vs + Smem<D>::kTileFloats;
-  const int h = blockIdx.x % P.Hq, t2 = blockIdx.x / P.Hq;
+  const int h = blockIdx.x % P.Hq, t = blockIdx.x / P.Hq;
   int qt;
-  const SeqRec s = query_tile(P, t2 >> 1, &qt);
-  const int i0 = qt * kDenseTile + (1 - (t2 & 1)) * kTile;  // first row of the tile
+  const SeqRec s = query_tile(P, t / kParts, &qt);
+  const int i0 = qt * kDenseTile + (kParts - 1 - t % kParts) * kRows;
   if (i0 >= s.nq) return;
-  const int rows = min(kTile, s.nq - i0), g = h / P.G;
+  const int rows = min(kRows, s.nq - i0), g = h / P.G;
   const int b = P.seqs ? 0 : s.q0 / P.Sq;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  load_tile<T, D>(Qs, q + ((long long)(s.q0 + i0) * P.Hq + h) * D, (long long)P.Hq * D, rows);
+  load_tile<T, D, kRows>(Qs, q + ((long long)(s.q0 + i0) * P.Hq + h) * D, (long long)P.Hq * D,
+                         rows);
   Running<D> R;
   R.clear();
   const float sl2 = P.scale * kLog2e;
-  const int seen = min(s.nk, s.pos0 + i0 + rows);  // keys that the tile's last row sees
+  const int seen = min(s.nk, s.pos0 + i0 + rows);  // keys that the block's last row sees
   for (int j0 = 0; j0 < seen; j0 += kTile) {
     const long long row = tile_row(P, b, s.k0, j0 / kDenseTile) + (j0 % kDenseTile);
     const int valid = min(kTile, s.nk - j0);
     __syncthreads();  // the previous tile's P and V are read
-    load_tile<T, D>(Ks, k + (row * P.Hkv + g) * D, (long long)P.Hkv * D, valid);
-    load_tile<T, D>(Vs, v + (row * P.Hkv + g) * D, (long long)P.Hkv * D, valid);
+    load_tile<T, D, kTile>(Ks, k + (row * P.Hkv + g) * D, (long long)P.Hkv * D, valid);
+    load_tile<T, D, kTile>(Vs, v + (row * P.Hkv + g) * D, (long long)P.Hkv * D, valid);
     __syncthreads();
     float sc[4][4] = {};
     product_nt<D>(Qs, Ks, ty, tx, sc);
@@ -222,7 +208,7 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool sees = j0 + tx + 16 * j <= s.pos0 + i0 + ty + 16 * i;
+        const bool sees = j0 + tx + 16 * j <= s.pos0 + i0 + ty + 8 * i;
         sc[i][j] = sees ? sc[i][j] * sl2 : -INFINITY;
       }
     R.step(sc, Ps, ty, tx);
@@ -231,7 +217,7 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = ty + 16 * i;
+    const int r = ty + 8 * i;
     if (r >= rows) continue;
     const long long at = (long long)(s.q0 + i0 + r) * P.Hq + h;
     const float inv = 1.f / R.l[i];
@@ -262,98 +248,105 @@ dense_delta_kernel(const T* __restrict__ dout, const T* __restrict__ out, float*
   if (lane == 0) delta[r] = s;
 }
 
-// P and dS of one 64 x 64 tile into shared memory (rows = queries).
+// dk and dv: block = (32 keys, key head, split of the group's heads); walks those heads
+// and the 64-query tiles that see the keys, with keys as rows:
+//   P^T = 2^(c K Q^T - c lse), dS^T = P^T (V dO^T - delta), dV += P^T dO, dK += dS^T Q.
 template <int D>
-__device__ __forceinline__ void tile_grads(const float* Qs, const float* Ks, const float* Vs,
-                                           const float* Gs, float* Ps, float* Ss,
-                                           const float* lse_s, const float* delta_s, float scale,
-                                           int pos, int rows, int j0, int ty, int tx) {
-  float s[4][4] = {}, dp[4][4] = {};
-  product_nt<D>(Qs, Ks, ty, tx, s);
-  product_nt<D>(Gs, Vs, ty, tx, dp);
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty + 16 * i;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int c = tx + 16 * j;
-      const bool sees = r < rows && j0 + c <= pos + r;
-      const float p = sees ? exp2f(s[i][j] * (scale * kLog2e) - lse_s[r] * kLog2e) : 0.f;
-      if (Ps) Ps[r * Smem<D>::kPPitch + c] = p;
-      Ss[r * Smem<D>::kPPitch + c] = sees ? p * (dp[i][j] - delta_s[r]) : 0.f;
-    }
-  }
+constexpr size_t dkv_smem() {
+  return sizeof(float) * (2 * Smem<D>::kRowFloats + 2 * Smem<D>::kTileFloats +
+                          2 * Smem<D>::kPFloats + 2 * kTile);
 }
 
-template <int D>
-constexpr size_t bwd_smem() {
-  return sizeof(float) * (4 * Smem<D>::kTileFloats + 2 * Smem<D>::kPFloats + 2 * kTile);
-}
-
-// dk and dv: block = (key tile half, key head); walks the group's heads and the query
-// tiles that see it.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
-dense_dkv_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ q,
+dense_dkv_simt_kernel(Dense P, int splits, const T* __restrict__ dout, const T* __restrict__ q,
                       const T* __restrict__ k, const T* __restrict__ v,
                       const float* __restrict__ lse, const float* __restrict__ delta,
-                      T* __restrict__ dk, T* __restrict__ dv) {
+                      T* __restrict__ dk, T* __restrict__ dv, float* __restrict__ part) {
   extern __shared__ float sm[];
   float* Ks = sm;
-  float* Vs = Ks + Smem<D>::kTileFloats;
-  float* Qs = Vs + Smem<D>::kTileFloats;
+  float* Vs = Ks + Smem<D>::kRowFloats;
+  float* Qs = Vs + Smem<D>::kRowFloats;
   float* Gs = Qs + Smem<D>::kTileFloats;
   float* Ps = Gs + Smem<D>::kTileFloats;
   float* Ss = Ps + Smem<D>::kPFloats;
   float* lse_s = Ss + Smem<D>::kPFloats;
   float* delta_s = lse_s + kTile;
-  const int g = blockIdx.x % P.Hkv, t2 = blockIdx.x / P.Hkv;
+  const int split = blockIdx.x % splits, g = (blockIdx.x / splits) % P.Hkv;
+  const int t = blockIdx.x / splits / P.Hkv;
   int kt;
-  const SeqRec s = key_tile(P, t2 >> 1, &kt);
-  const int j0 = kt * kDenseTile + (t2 & 1) * kTile;
+  const SeqRec s = key_tile(P, t / kParts, &kt);
+  const int j0 = kt * kDenseTile + (t % kParts) * kRows;
   if (j0 >= s.nk) return;
-  const int keys = min(kTile, s.nk - j0);
+  const int keys = min(kRows, s.nk - j0);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const long long kst = (long long)P.Hkv * D, qst = (long long)P.Hq * D;
   const long long kat = ((long long)(s.k0 + j0) * P.Hkv + g) * D;
-  load_tile<T, D>(Ks, k + kat, kst, keys);
-  load_tile<T, D>(Vs, v + kat, kst, keys);
+  load_tile<T, D, kRows>(Ks, k + kat, kst, keys);
+  load_tile<T, D, kRows>(Vs, v + kat, kst, keys);
   float ak[4][D / 16] = {}, av[4][D / 16] = {};
   // the first query row that sees key j0 sits at position j0
   const int i_first = max(0, j0 - s.pos0) / kTile * kTile;
-  for (int h = g * P.G; h < (g + 1) * P.G; ++h) {
+  const int per = (P.G + splits - 1) / splits;
+  const int h0 = g * P.G + split * per, h1 = min(h0 + per, (g + 1) * P.G);
+  for (int h = h0; h < h1; ++h) {
     for (int i0 = i_first; i0 < s.nq; i0 += kTile) {
       const int rows = min(kTile, s.nq - i0);
       const long long at = (long long)(s.q0 + i0) * P.Hq + h;
       __syncthreads();
-      load_tile<T, D>(Qs, q + at * D, qst, rows);
-      load_tile<T, D>(Gs, dout + at * D, qst, rows);
+      load_tile<T, D, kTile>(Qs, q + at * D, qst, rows);
+      load_tile<T, D, kTile>(Gs, dout + at * D, qst, rows);
       if (threadIdx.x < kTile) {
         const bool ok = int(threadIdx.x) < rows;
-        lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] : 0.f;
+        lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] * kLog2e : 0.f;
         delta_s[threadIdx.x] = ok ? delta[at + (long long)threadIdx.x * P.Hq] : 0.f;
       }
       __syncthreads();
-      tile_grads<D>(Qs, Ks, Vs, Gs, Ps, Ss, lse_s, delta_s, P.scale, s.pos0 + i0, rows, j0, ty, tx);
+      float sc[4][4] = {}, dp[4][4] = {};
+      product_nt<D>(Ks, Qs, ty, tx, sc);
+      product_nt<D>(Vs, Gs, ty, tx, dp);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int key = ty + 8 * i, c = tx + 16 * j;
+          const bool sees = c < rows && j0 + key <= s.pos0 + i0 + c;
+          const float p = sees ? exp2f(sc[i][j] * (P.scale * kLog2e) - lse_s[c]) : 0.f;
+          Ps[key * Smem<D>::kPPitch + c] = p;
+          Ss[key * Smem<D>::kPPitch + c] = sees ? p * (dp[i][j] - delta_s[c]) : 0.f;
+        }
       __syncthreads();
-      product_tn<D>(Ps, Gs, ty, tx, av);
-      product_tn<D>(Ss, Qs, ty, tx, ak);
+      product_nn<D>(Ps, Gs, ty, tx, av);
+      product_nn<D>(Ss, Qs, ty, tx, ak);
     }
   }
+  const long long all = P.rows_k * P.Hkv * D;
+  float* pv = part + (long long)split * 2 * all;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = ty + 16 * i;
+    const int r = ty + 8 * i;
     if (r >= keys) continue;
     const long long at = kat + r * kst + tx * 4;
 #pragma unroll
     for (int c = 0; c < D / 16; c += 4) {
-      store4(dk + at + c * 16, &ak[i][c], P.scale);
-      store4(dv + at + c * 16, &av[i][c], 1.f);
+      if (splits > 1) {
+        store4(pv + at + c * 16, &av[i][c], 1.f);
+        store4(pv + all + at + c * 16, &ak[i][c], 1.f);
+      } else {
+        store4(dk + at + c * 16, &ak[i][c], P.scale);
+        store4(dv + at + c * 16, &av[i][c], 1.f);
+      }
     }
   }
 }
 
-// dq: block = (query tile half, head); walks the keys that its rows see.
+// dq: block = (32 query rows, head); walks the keys that its rows see.
+template <int D>
+constexpr size_t dq_smem() {
+  return sizeof(float) * (2 * Smem<D>::kRowFloats + 2 * Smem<D>::kTileFloats +
+                          Smem<D>::kPFloats + 2 * kRows);
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads)
 dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ q,
@@ -361,51 +354,86 @@ dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ 
                      const float* __restrict__ lse, const float* __restrict__ delta,
                      T* __restrict__ dq) {
   extern __shared__ float sm[];
-  float* Ks = sm;
+  float* Qs = sm;
+  float* Gs = Qs + Smem<D>::kRowFloats;
+  float* Ks = Gs + Smem<D>::kRowFloats;
   float* Vs = Ks + Smem<D>::kTileFloats;
-  float* Qs = Vs + Smem<D>::kTileFloats;
-  float* Gs = Qs + Smem<D>::kTileFloats;
-  float* Ss = Gs + Smem<D>::kTileFloats;
+  float* Ss = Vs + Smem<D>::kTileFloats;
   float* lse_s = Ss + Smem<D>::kPFloats;
-  float* delta_s = lse_s + kTile;
-  const int h = blockIdx.x % P.Hq, t2 = blockIdx.x / P.Hq, g = h / P.G;
+  float* delta_s = lse_s + kRows;
+  const int h = blockIdx.x % P.Hq, t = blockIdx.x / P.Hq, g = h / P.G;
   int qt;
-  const SeqRec s = query_tile(P, t2 >> 1, &qt);
-  const int i0 = qt * kDenseTile + (1 - (t2 & 1)) * kTile;
+  const SeqRec s = query_tile(P, t / kParts, &qt);
+  const int i0 = qt * kDenseTile + (kParts - 1 - t % kParts) * kRows;
   if (i0 >= s.nq) return;
-  const int rows = min(kTile, s.nq - i0);
+  const int rows = min(kRows, s.nq - i0);
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const long long kst = (long long)P.Hkv * D, qst = (long long)P.Hq * D;
   const long long at = (long long)(s.q0 + i0) * P.Hq + h;
-  load_tile<T, D>(Qs, q + at * D, qst, rows);
-  load_tile<T, D>(Gs, dout + at * D, qst, rows);
-  if (threadIdx.x < kTile) {
+  load_tile<T, D, kRows>(Qs, q + at * D, qst, rows);
+  load_tile<T, D, kRows>(Gs, dout + at * D, qst, rows);
+  if (threadIdx.x < kRows) {
     const bool ok = int(threadIdx.x) < rows;
-    lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] : 0.f;
+    lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] * kLog2e : 0.f;
     delta_s[threadIdx.x] = ok ? delta[at + (long long)threadIdx.x * P.Hq] : 0.f;
   }
   float aq[4][D / 16] = {};
   const int seen = min(s.nk, s.pos0 + i0 + rows);
   for (int j0 = 0; j0 < seen; j0 += kTile) {
-    const int keys = min(kTile, s.nk - j0);
+    // rows behind what is seen are zero: they must not meet a weight of zero as NaN
+    const int keys = min(kTile, seen - j0);
     const long long kat = ((long long)(s.k0 + j0) * P.Hkv + g) * D;
     __syncthreads();
-    load_tile<T, D>(Ks, k + kat, kst, keys);
-    load_tile<T, D>(Vs, v + kat, kst, keys);
+    load_tile<T, D, kTile>(Ks, k + kat, kst, keys);
+    load_tile<T, D, kTile>(Vs, v + kat, kst, keys);
     __syncthreads();
-    tile_grads<D>(Qs, Ks, Vs, Gs, nullptr, Ss, lse_s, delta_s, P.scale, s.pos0 + i0, rows, j0, ty,
-                  tx);
+    float sc[4][4] = {}, dp[4][4] = {};
+    product_nt<D>(Qs, Ks, ty, tx, sc);
+    product_nt<D>(Gs, Vs, ty, tx, dp);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int r = ty + 8 * i, c = tx + 16 * j;
+        const bool sees = r < rows && j0 + c <= s.pos0 + i0 + r;
+        const float p = sees ? exp2f(sc[i][j] * (P.scale * kLog2e) - lse_s[r]) : 0.f;
+        Ss[r * Smem<D>::kPPitch + c] = sees ? p * (dp[i][j] - delta_s[r]) : 0.f;
+      }
     __syncthreads();
     product_nn<D>(Ss, Ks, ty, tx, aq);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int r = ty + 16 * i;
+    const int r = ty + 8 * i;
     if (r >= rows) continue;
 #pragma unroll
     for (int c = 0; c < D / 16; c += 4)
       store4(dq + (at + (long long)r * P.Hq) * D + tx * 4 + c * 16, &aq[i][c], P.scale);
   }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(256)
+dense_dkv_sum_kernel(const float* __restrict__ part, int splits, long long n, float scale,
+                     T* __restrict__ dk, T* __restrict__ dv) {
+  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
+  if (i >= n) return;
+  const int which = blockIdx.y;
+  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int s = 0; s < splits; ++s) {
+    const float4 x = *reinterpret_cast<const float4*>(part + (s * 2 + which) * n + i);
+    sum.x += x.x;
+    sum.y += x.y;
+    sum.z += x.z;
+    sum.w += x.w;
+  }
+  const float f = which ? scale : 1.f;
+  T* dst = (which ? dk : dv) + i;
+  dst[0] = from_f32<T>(sum.x * f);
+  dst[1] = from_f32<T>(sum.y * f);
+  dst[2] = from_f32<T>(sum.z * f);
+  dst[3] = from_f32<T>(sum.w * f);
 }
 
 // ---------------------------------------------------------------------------
@@ -420,7 +448,7 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
   __shared__ uint8_t seen_s[kTile];  // a draft's row of this key tile is seen by some node
   const Dense& P = A.d;
   float* Qs = sm;
-  float* Ks = Qs + Smem<D>::kTileFloats;
+  float* Ks = Qs + Smem<D>::kRowFloats;
   float* Vs = Ks + Smem<D>::kTileFloats;
   float* Ps = Vs + Smem<D>::kTileFloats;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4, nodes = P.Sq;
@@ -436,7 +464,7 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
     const uint8_t* mask = A.mask + p.b * A.mask_stride;
     const int row0 = p.group * A.rows, rows = min(A.rows, nodes * P.G - row0);
     __syncthreads();
-    for (int i = threadIdx.x; i < kTile * (D / 4); i += kThreads) {
+    for (int i = threadIdx.x; i < kRows * (D / 4); i += kThreads) {
       const int r = i / (D / 4), c = (i % (D / 4)) * 4, node = (row0 + r) / P.G;
       float x[4] = {};
       if (r < rows)
@@ -457,8 +485,8 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
       const int valid = min(kTile, total - j0);
       const bool drafts = j0 + kTile > p.len;  // the tile reaches the drafted tokens
       __syncthreads();
-      load_tile<T, D>(Ks, k + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
-      load_tile<T, D>(Vs, v + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
+      load_tile<T, D, kTile>(Ks, k + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
+      load_tile<T, D, kTile>(Vs, v + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
       if (drafts && threadIdx.x < kTile) {
         const int j = j0 + int(threadIdx.x) - p.len;
         bool any = j < 0;
@@ -474,7 +502,7 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
       product_nt<D>(Qs, Ks, ty, tx, sc);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int node = min((row0 + ty + 16 * i) / P.G, nodes - 1);
+        const int node = min((row0 + ty + 8 * i) / P.G, nodes - 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int draft = j0 + tx + 16 * j - p.len;
@@ -488,7 +516,7 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      const int r = ty + 16 * i;
+      const int r = ty + 8 * i;
       if (r >= rows) continue;
       if (p.slot >= 0) {
         const long long at = (long long)(blockIdx.x * 2 + p.slot) * A.rows;
@@ -574,7 +602,7 @@ cudaError_t fwd(const Dense& P, const void* q, const void* k, const void* v, voi
                 cudaStream_t s) {
   cudaError_t e = allow_smem(dense_fwd_simt_kernel<T, D>, fwd_smem<D>());
   if (e != cudaSuccess) return e;
-  dense_fwd_simt_kernel<T, D><<<unsigned(P.qtiles) * 2 * P.Hq, kThreads, fwd_smem<D>(), s>>>(
+  dense_fwd_simt_kernel<T, D><<<unsigned(P.qtiles) * kParts * P.Hq, kThreads, fwd_smem<D>(), s>>>(
       P, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
       static_cast<T*>(out), lse);
   return cudaGetLastError();
@@ -582,24 +610,29 @@ cudaError_t fwd(const Dense& P, const void* q, const void* k, const void* v, voi
 
 template <typename T, int D>
 cudaError_t bwd(const Dense& P, const void* dout, const void* q, const void* k, const void* v,
-                const void* out, const float* lse, float* delta, void* dq, void* dk, void* dv,
-                cudaStream_t s) {
-  cudaError_t e = allow_smem(dense_dkv_simt_kernel<T, D>, bwd_smem<D>());
-  if (e == cudaSuccess) e = allow_smem(dense_dq_simt_kernel<T, D>, bwd_smem<D>());
+                const void* out, const float* lse, const DenseBwdSpace& W, void* dq, void* dk,
+                void* dv, cudaStream_t s) {
+  cudaError_t e = allow_smem(dense_dkv_simt_kernel<T, D>, dkv_smem<D>());
+  if (e == cudaSuccess) e = allow_smem(dense_dq_simt_kernel<T, D>, dq_smem<D>());
   if (e != cudaSuccess) return e;
   const long long n = P.rows_q * P.Hq;
   const T *g_ = static_cast<const T*>(dout), *q_ = static_cast<const T*>(q);
   const T *k_ = static_cast<const T*>(k), *v_ = static_cast<const T*>(v);
+  T *dk_ = static_cast<T*>(dk), *dv_ = static_cast<T*>(dv);
   if (n > 0)
-    dense_delta_kernel<T, D><<<unsigned((n + 7) / 8), kThreads, 0, s>>>(
-        g_, static_cast<const T*>(out), delta, n);
+    dense_delta_kernel<T, D><<<unsigned((n + 3) / 4), kThreads, 0, s>>>(
+        g_, static_cast<const T*>(out), W.dl, n);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int splits = dense_bwd_splits(P);
+  dense_dkv_simt_kernel<T, D>
+      <<<unsigned(P.ktiles) * kParts * P.Hkv * splits, kThreads, dkv_smem<D>(), s>>>(
+          P, splits, g_, q_, k_, v_, lse, W.dl, dk_, dv_, W.part);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (splits > 1) e = launch_dkv_sum(W.part, splits, P.rows_k * P.Hkv * D, P.scale, dk_, dv_, s);
+  if (e != cudaSuccess) return e;
   if (P.qtiles > 0)
-    dense_dq_simt_kernel<T, D><<<unsigned(P.qtiles) * 2 * P.Hq, kThreads, bwd_smem<D>(), s>>>(
-        P, g_, q_, k_, v_, lse, delta, static_cast<T*>(dq));
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  dense_dkv_simt_kernel<T, D><<<unsigned(P.ktiles) * 2 * P.Hkv, kThreads, bwd_smem<D>(), s>>>(
-      P, g_, q_, k_, v_, lse, delta, static_cast<T*>(dk), static_cast<T*>(dv));
+    dense_dq_simt_kernel<T, D><<<unsigned(P.qtiles) * kParts * P.Hq, kThreads, dq_smem<D>(), s>>>(
+        P, g_, q_, k_, v_, lse, W.dl, static_cast<T*>(dq));
   return cudaGetLastError();
 }
 
@@ -608,7 +641,7 @@ cudaError_t tree(const Tree& A, const void* q, const void* k, const void* v, voi
                  int32_t* status, cudaStream_t s) {
   cudaError_t e = allow_smem(tree_simt_kernel<T, D>, fwd_smem<D>());
   if (e != cudaSuccess) return e;
-  tree_simt_kernel<T, D><<<tree_ctas(), kThreads, fwd_smem<D>(), s>>>(
+  tree_simt_kernel<T, D><<<tree_ctas(A.d.f32), kThreads, fwd_smem<D>(), s>>>(
       A, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(v),
       static_cast<T*>(out), lse, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
@@ -619,7 +652,7 @@ cudaError_t tree(const Tree& A, const void* q, const void* k, const void* v, voi
 
 cudaError_t launch_tree_combine(const Tree& A, void* out, float* lse, cudaStream_t s) {
   const long long blocks = (long long)A.d.B * A.d.Hkv * A.groups * (A.d.D / 8);
-  const int ctas = tree_ctas();
+  const int ctas = tree_ctas(A.d.f32);
   if (A.d.f32) {
     auto kern = A.d.D == 128 ? tree_combine_kernel<float, 128> : tree_combine_kernel<float, 64>;
     kern<<<unsigned(blocks), A.rows, 0, s>>>(A, ctas, static_cast<float*>(out), lse);
@@ -631,26 +664,46 @@ cudaError_t launch_tree_combine(const Tree& A, void* out, float* lse, cudaStream
   return cudaGetLastError();
 }
 
+// bf16 problems run on the tensor cores: only fp32 comes here.
 cudaError_t launch_dense_fwd_simt(const Dense& P, const void* q, const void* k, const void* v,
                                   void* out, float* lse, cudaStream_t s) {
-  auto fn = P.f32 ? (P.D == 128 ? fwd<float, 128> : fwd<float, 64>)
-                  : (P.D == 128 ? fwd<__nv_bfloat16, 128> : fwd<__nv_bfloat16, 64>);
-  return fn(P, q, k, v, out, lse, s);
+  return (P.D == 128 ? fwd<float, 128> : fwd<float, 64>)(P, q, k, v, out, lse, s);
 }
 
 cudaError_t launch_dense_bwd_simt(const Dense& P, const void* dout, const void* q, const void* k,
-                                  const void* v, const void* out, const float* lse, float* delta,
-                                  void* dq, void* dk, void* dv, cudaStream_t s) {
-  auto fn = P.f32 ? (P.D == 128 ? bwd<float, 128> : bwd<float, 64>)
-                  : (P.D == 128 ? bwd<__nv_bfloat16, 128> : bwd<__nv_bfloat16, 64>);
-  return fn(P, dout, q, k, v, out, lse, delta, dq, dk, dv, s);
+                                  const void* v, const void* out, const float* lse,
+                                  const DenseBwdSpace& W, void* dq, void* dk, void* dv,
+                                  cudaStream_t s) {
+  return (P.D == 128 ? bwd<float, 128> : bwd<float, 64>)(P, dout, q, k, v, out, lse, W, dq, dk, dv,
+                                                         s);
 }
 
 cudaError_t launch_tree_simt(const Tree& A, const void* q, const void* k, const void* v, void* out,
                              float* lse, int32_t* status, cudaStream_t s) {
-  auto fn = A.d.f32 ? (A.d.D == 128 ? tree<float, 128> : tree<float, 64>)
-                    : (A.d.D == 128 ? tree<__nv_bfloat16, 128> : tree<__nv_bfloat16, 64>);
-  return fn(A, q, k, v, out, lse, status, s);
+  return (A.d.D == 128 ? tree<float, 128> : tree<float, 64>)(A, q, k, v, out, lse, status, s);
 }
+
+// The heads of a group are split over several items where there would otherwise be
+// fewer than three items (tensor cores; 128 keys each) or four blocks (32 keys each) per
+// SM to balance the load with; each split costs one more write and read of dk and dv in
+// fp32.
+int dense_bwd_splits(const Dense& P) {
+  const long long items = (long long)P.ktiles * P.Hkv * (P.f32 ? kParts : 1);
+  int n = 1;
+  while (n < P.G && items * n < (P.f32 ? 4LL : 3LL) * 148) n *= 2;
+  return std::min(n, P.G);
+}
+
+template <typename T>
+cudaError_t launch_dkv_sum(const float* part, int splits, long long n, float scale, T* dk, T* dv,
+                           cudaStream_t s) {
+  dense_dkv_sum_kernel<<<dim3(unsigned((n / 4 + 255) / 256), 2), 256, 0, s>>>(part, splits, n,
+                                                                              scale, dk, dv);
+  return cudaGetLastError();
+}
+template cudaError_t launch_dkv_sum(const float*, int, long long, float, float*, float*,
+                                    cudaStream_t);
+template cudaError_t launch_dkv_sum(const float*, int, long long, float, __nv_bfloat16*,
+                                    __nv_bfloat16*, cudaStream_t);
 
 }  // namespace msa

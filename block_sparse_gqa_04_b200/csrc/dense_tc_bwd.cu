@@ -559,26 +559,6 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   }
 }
 
-// dk, dv = the sum of the splits' partial sums, in order.  part [splits][dv, dk][n].
-__global__ void __launch_bounds__(256)
-dense_dkv_sum_kernel(const float* __restrict__ part, int splits, long long n, float scale,
-                     __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv) {
-  const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
-  if (i >= n) return;
-  const int which = blockIdx.y;
-  float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < splits; ++s) {
-    const float4 x = *reinterpret_cast<const float4*>(part + (s * 2 + which) * n + i);
-    sum.x += x.x;
-    sum.y += x.y;
-    sum.z += x.z;
-    sum.w += x.w;
-  }
-  const float f = which ? scale : 1.f;
-  *reinterpret_cast<uint2*>((which ? dk : dv) + i) =
-      make_uint2(pack_bf16(sum.x * f, sum.y * f), pack_bf16(sum.z * f, sum.w * f));
-}
-
 // ---------------------------------------------------------------------------
 // dq
 // ---------------------------------------------------------------------------
@@ -964,9 +944,9 @@ cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* 
       static_cast<bf16*>(dv), W.part, counters, status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   if (splits > 1) {
-    dense_dkv_sum_kernel<<<dim3(unsigned((kelems / 4 + 255) / 256), 2), 256, 0, s>>>(
-        W.part, splits, kelems, P.scale, static_cast<bf16*>(dk), static_cast<bf16*>(dv));
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    e = launch_dkv_sum(W.part, splits, kelems, P.scale, static_cast<bf16*>(dk),
+                       static_cast<bf16*>(dv), s);
+    if (e != cudaSuccess) return e;
   }
   const int qitems = P.qtiles * P.Hq;
   dense_dq_tc_kernel<D><<<std::min(sm_count(), qitems), kThreads, row_smem<D>(), s>>>(
@@ -975,15 +955,6 @@ cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* 
 }
 
 }  // namespace
-
-// The heads of a group are split over several items where there would otherwise be
-// fewer than three items per SM to balance the load with; each split costs one more
-// write and read of dk and dv in fp32.
-int dense_bwd_splits(const Dense& P) {
-  int n = 1;
-  while (n < P.G && (long long)P.ktiles * P.Hkv * n < 3LL * 148) n *= 2;
-  return std::min(n, P.G);
-}
 
 cudaError_t launch_dense_bwd_tc(const Dense& P, const void* dout, const void* q, const void* k,
                                 const void* v, const void* out, const float* lse,

@@ -6,14 +6,17 @@
 // rotation undone on the incoming gradient (its transpose): g, u = r x, t = w g,
 //   dw = sum g u,   dx = r (t - u mean(t u)).
 //
-// Both directions read and write every element once and are bound by HBM.  A row
-// is held by D / (16 bytes) neighbouring lanes, 16 bytes each, so its sums and the
-// partners of its pairs are a few shuffles away and nothing but the angles goes
-// through shared memory; a thread has kUnroll rows' loads in flight.  The angles
-// of a token are the same for all its heads: a block takes all heads of a few
-// tokens and forms them once, in fp64 (positions x frequencies reach 10^6 turns,
-// where fp32 keeps no fraction), reduced to a quarter turn before the fp32 sine
-// and cosine.
+// Both directions read and write every element once and are bound by HBM, if little
+// enough else goes through the load/store pipe: shuffles and shared-memory reads were the
+// bound while a row's lanes held neighbouring elements and fetched the partners of their
+// pairs (2.6 TB/s).  So a thread holds both elements of its pairs: of D / 16 lanes per
+// row, each has two chunks of 8 elements, a chunk of the first half of the rotated part
+// and its partner in the second (or two neighbours, where pairs are adjacent or nothing
+// is rotated).  Its 8 angles are the same for all heads of a token: it keeps them in
+// registers and walks the heads, the next rows' loads in flight.  The angles are formed
+// once per block and token, in fp64 (positions x frequencies reach 10^6 turns, where fp32
+// keeps no fraction), reduced to a quarter turn before the fp32 sine and cosine.  Blocks
+// take query heads or key heads, so that a thread needs one set of weights and sums.
 #include "common.cuh"
 #include "dense.h"
 
@@ -21,11 +24,8 @@ namespace msa {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;
 constexpr int kMaxHalf = 64;  // rotated pairs of a head
-// Tokens of a block: one for a decode step's few rows, where every block counts,
-// else enough rows to fill the unrolled loop.
-constexpr int kTokens = 4;
+constexpr int kTokens = 32;   // tokens of a block at a time, at most
 
 // cos and sin of position * freq: turns reduced in fp64, then at most a quarter
 // turn in fp32.
@@ -40,67 +40,65 @@ __device__ __forceinline__ float2 cos_sin(long long pos, double freq) {
   return make_float2((quad == 1 || quad == 2) ? -cc : cc, quad >= 2 ? -ss : ss);
 }
 
-template <typename T, int D>
-struct Shape {
-  static constexpr int kVec = 16 / int(sizeof(T));
-  static constexpr int kLanes = D / kVec;          // lanes of a row
-  static constexpr int kSlots = kThreads / kLanes;  // rows of a block at a time
+// A thread's part of a row: elements a .. a+7 and b .. b+7.
+struct Place {
+  int a, b;
+  bool turned;  // they are rotated, by the angles 8 * lane .. 8 * lane + 7
 };
 
-template <int N, int LANES>
+__device__ __forceinline__ Place place_of(int lane, int rot, bool inter) {
+  if (inter) return Place{16 * lane, 16 * lane + 8, 16 * lane < rot};
+  if (16 * lane < rot) return Place{8 * lane, 8 * lane + rot / 2, true};
+  return Place{16 * lane, 16 * lane + 8, false};
+}
+
+// 16 elements of a row, as stored.
+template <typename T>
+struct Raw {
+  static constexpr int kWords = int(sizeof(T));  // 16-byte words of 16 elements: 2 or 4
+  uint4 w[kWords];
+  __device__ __forceinline__ void load(const T* row, const Place& p) {
+#pragma unroll
+    for (int i = 0; i < kWords / 2; ++i) {
+      w[i] = *reinterpret_cast<const uint4*>(row + p.a + i * (16 / sizeof(T)));
+      w[kWords / 2 + i] = *reinterpret_cast<const uint4*>(row + p.b + i * (16 / sizeof(T)));
+    }
+  }
+  __device__ __forceinline__ void clear() {
+#pragma unroll
+    for (int i = 0; i < kWords; ++i) w[i] = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ void store(T* row, const Place& p) const {
+#pragma unroll
+    for (int i = 0; i < kWords / 2; ++i) {
+      *reinterpret_cast<uint4*>(row + p.a + i * (16 / sizeof(T))) = w[i];
+      *reinterpret_cast<uint4*>(row + p.b + i * (16 / sizeof(T))) = w[kWords / 2 + i];
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {  // i: a constant
+    return to_f32(reinterpret_cast<const T*>(w)[i]);
+  }
+  __device__ __forceinline__ void set(int i, float x) {
+    reinterpret_cast<T*>(w)[i] = from_f32<T>(x);
+  }
+};
+
+template <int LANES>
 __device__ __forceinline__ float row_sum(float v) {
 #pragma unroll
   for (int o = LANES / 2; o > 0; o >>= 1) v += __shfl_xor_sync(MSA_FULL_MASK, v, o);
   return v;
 }
 
-template <typename T, int N>
-__device__ __forceinline__ void widen(const uint4& u, float (&x)[N]) {
-  const T* e = reinterpret_cast<const T*>(&u);
+// Turns y (elements a.. and b.. of a row) by the angles cs, or back with sign -1.
+template <bool INTER>
+__device__ __forceinline__ void rotate(float (&y)[16], const float2 (&cs)[8], float sign) {
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = to_f32(e[i]);
-}
-
-template <typename T, int N>
-__device__ __forceinline__ uint4 narrow(const float (&x)[N]) {
-  uint4 u;
-  T* e = reinterpret_cast<T*>(&u);
-#pragma unroll
-  for (int i = 0; i < N; ++i) e[i] = from_f32<T>(x[i]);
-  return u;
-}
-
-// Turns this lane's elements e0 .. e0+N-1 of a row by the angles cs (sign -1: back).
-// Every lane of the warp takes part.
-template <int N>
-__device__ __forceinline__ void rotate(float (&y)[N], int e0, int rot, bool inter,
-                                       const float2* cs, float sign) {
-  if (rot == 0) return;
-  if (inter) {
-    if (e0 < rot) {
-#pragma unroll
-      for (int i = 0; i < N; i += 2) {
-        const float2 f = cs[(e0 + i) >> 1];
-        const float a = y[i], b = y[i + 1], s = sign * f.y;
-        y[i] = a * f.x - b * s;
-        y[i + 1] = b * f.x + a * s;
-      }
-    }
-    return;
-  }
-  const int half = rot >> 1, lane = threadIdx.x & 31;
-  const bool first = e0 < half, turned = e0 < rot;
-  const int other = turned ? (first ? lane + half / N : lane - half / N) : lane;
-  // first half: a cos - b sin with b the partner; second: b cos + a sin
-  const float s0 = first ? -sign : sign;
-  const int i0 = first ? e0 : e0 - half;
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const float p = __shfl_sync(MSA_FULL_MASK, y[i], other);
-    if (turned) {
-      const float2 f = cs[i0 + i];
-      y[i] = y[i] * f.x + p * (s0 * f.y);
-    }
+  for (int i = 0; i < 8; ++i) {
+    const int u = INTER ? 2 * i : i, v = INTER ? 2 * i + 1 : i + 8;
+    const float a = y[u], b = y[v], s = sign * cs[i].y;
+    y[u] = a * cs[i].x - b * s;
+    y[v] = b * cs[i].x + a * s;
   }
 }
 
@@ -112,194 +110,243 @@ __device__ __forceinline__ void fill_angles(float2 (*cs)[kMaxHalf], long long t0
   }
 }
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
-norm_rope_kernel(NormRope P, int tokens, const T* q, const T* k, const T* qw, const T* kw,
+// A thread's angles of token `tok`; no turn where nothing is rotated.
+__device__ __forceinline__ void my_angles(float2 (&a)[8], const float2 (*cs)[kMaxHalf], int tok,
+                                          int lane, bool turned) {
+#pragma unroll
+  for (int i = 0; i < 8; ++i) a[i] = turned ? cs[tok][8 * lane + i] : make_float2(1.f, 0.f);
+}
+
+// How the query heads (or the key heads) are cut: `tokens` tokens at a time, `span` heads
+// of them (in `chunks` parts), `blocks` blocks that share all of it.
+struct Cut {
+  int heads, tokens, span, chunks;
+  long long sets;  // ceil(rows / tokens) * chunks
+  int blocks;
+};
+
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 3)
+norm_rope_kernel(NormRope P, Cut cq, Cut ck, const T* q, const T* k, const T* qw, const T* kw,
                  const double* inv_freq, const int64_t* pos, T* qo, T* ko) {
-  using S = Shape<T, D>;
+  constexpr int kLanes = D / 16, kGroups = kThreads / kLanes;
   __shared__ float2 cs[kTokens][kMaxHalf];
-  const long long t0 = (long long)blockIdx.x * tokens;
-  const int nt = int(min((long long)tokens, P.rows - t0));
-  const int heads = P.hq + P.hk, items = nt * heads;
-  const int slot = threadIdx.x / S::kLanes, e0 = (threadIdx.x % S::kLanes) * S::kVec;
-  fill_angles(cs, t0, nt, P.rot >> 1, inv_freq, pos);
-  float wq[S::kVec], wk[S::kVec];
-  load_vec<T, S::kVec>(qw + e0, wq);
-  if (P.hk) load_vec<T, S::kVec>(kw + e0, wk);
-  __syncthreads();
-  for (int base = 0; base < items; base += S::kSlots * kUnroll) {
-    uint4 raw[kUnroll];
-    int tok[kUnroll], head[kUnroll];
+  const bool isq = int(blockIdx.x) < cq.blocks;
+  const Cut c = isq ? cq : ck;
+  const T* src = isq ? q : k;
+  T* dst = isq ? qo : ko;
+  const long long ss = isq ? P.qs : P.ks, ds = isq ? P.qos : P.kos;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int per = kGroups / c.tokens, tok = group / per, g = group % per;
+  const Place at = place_of(lane, P.rot, INTER);
+  float w[16];
+  {
+    Raw<T> x;
+    x.load(isq ? qw : kw, at);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int it = base + u * S::kSlots + slot;
-      tok[u] = it < items ? it / heads : -1;
-      head[u] = it - max(tok[u], 0) * heads;
-      raw[u] = make_uint4(0, 0, 0, 0);
-      if (tok[u] >= 0) {
-        const long long r = t0 + tok[u];
-        const T* src = head[u] < P.hq ? q + r * P.qs + head[u] * D
-                                      : k + r * P.ks + (head[u] - P.hq) * D;
-        raw[u] = *reinterpret_cast<const uint4*>(src + e0);
+    for (int i = 0; i < 16; ++i) w[i] = x.get(i);
+  }
+  bool first = true;
+  for (long long set = isq ? blockIdx.x : blockIdx.x - cq.blocks; set < c.sets; set += c.blocks) {
+    const long long t0 = set / c.chunks * c.tokens, r = t0 + tok;
+    const int h0 = int(set % c.chunks) * c.span, h1 = min(c.heads, h0 + c.span);
+    const int nt = int(min((long long)c.tokens, P.rows - t0));
+    const bool there = tok < nt;
+    auto fetch = [&](int base, Raw<T>& x) {
+      const int h = base + g;
+      if (there && h < h1) x.load(src + r * ss + h * D, at); else x.clear();
+    };
+    Raw<T> cur, nxt;
+    fetch(h0, cur);  // the angles are formed under the first loads
+    if (!first) __syncthreads();
+    first = false;
+    fill_angles(cs, t0, nt, P.rot >> 1, inv_freq, pos);
+    __syncthreads();
+    float2 ang[8];
+    my_angles(ang, cs, tok, lane, at.turned);
+    for (int base = h0; base < h1; base += per) {
+      fetch(base + per, nxt);
+      float x[16], sum = 0.f;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        x[i] = cur.get(i);
+        sum += x[i] * x[i];
       }
-    }
+      const float rr = rsqrtf(row_sum<kLanes>(sum) * (1.f / D) + P.eps);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (base + u * S::kSlots >= items) break;
-      float x[S::kVec], ss = 0.f;
-      widen<T>(raw[u], x);
+      for (int i = 0; i < 16; ++i) x[i] = x[i] * rr * w[i];
+      rotate<INTER>(x, ang, 1.f);
 #pragma unroll
-      for (int i = 0; i < S::kVec; ++i) ss += x[i] * x[i];
-      const float r = rsqrtf(row_sum<S::kVec, S::kLanes>(ss) * (1.f / D) + P.eps);
-      const bool isq = head[u] < P.hq;
-#pragma unroll
-      for (int i = 0; i < S::kVec; ++i) x[i] = x[i] * r * (isq ? wq[i] : wk[i]);
-      rotate(x, e0, P.rot, P.inter, cs[max(tok[u], 0)], 1.f);
-      if (tok[u] >= 0) {
-        const long long row = t0 + tok[u];
-        T* dst = isq ? qo + row * P.qos + head[u] * D : ko + row * P.kos + (head[u] - P.hq) * D;
-        *reinterpret_cast<uint4*>(dst + e0) = narrow<T>(x);
-      }
+      for (int i = 0; i < 16; ++i) cur.set(i, x[i]);
+      if (there && base + g < h1) cur.store(dst + r * ds + (base + g) * D, at);
+      cur = nxt;
     }
   }
 }
 
-// Gradients; part[block][2][D] receives the block's sums of the weights' gradients.
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads)
-norm_rope_backward_kernel(NormRope P, int tokens, const T* gq, const T* gk, const T* q, const T* k,
-                          const T* qw, const T* kw, const double* inv_freq, const int64_t* pos,
-                          T* dq, T* dk, float* part) {
-  using S = Shape<T, D>;
-  constexpr int kLoads = 2;  // rows in flight per thread, two loads each
+// Gradients; part[block][D] receives the block's sums of its weight's gradient.
+template <typename T, int D, bool INTER>
+__global__ void __launch_bounds__(kThreads, 2)
+norm_rope_backward_kernel(NormRope P, Cut cq, Cut ck, const T* gq, const T* gk, const T* q,
+                          const T* k, const T* qw, const T* kw, const double* inv_freq,
+                          const int64_t* pos, T* dq, T* dk, float* part) {
+  constexpr int kLanes = D / 16, kGroups = kThreads / kLanes;
   __shared__ float2 cs[kTokens][kMaxHalf];
-  __shared__ float sums[S::kSlots][D];
-  const int heads = P.hq + P.hk;
-  const int slot = threadIdx.x / S::kLanes, e0 = (threadIdx.x % S::kLanes) * S::kVec;
-  float wq[S::kVec], wk[S::kVec], aq[S::kVec], ak[S::kVec];
-  load_vec<T, S::kVec>(qw + e0, wq);
-  if (P.hk) load_vec<T, S::kVec>(kw + e0, wk);
+  __shared__ float sums[kGroups][D];
+  const bool isq = int(blockIdx.x) < cq.blocks;
+  const Cut c = isq ? cq : ck;
+  const T *src = isq ? q : k, *gsrc = isq ? gq : gk;
+  T* dst = isq ? dq : dk;
+  const long long ss = isq ? P.qs : P.ks, gs = isq ? P.qos : P.kos, ds = isq ? P.dqs : P.dks;
+  const int lane = threadIdx.x % kLanes, group = threadIdx.x / kLanes;
+  const int per = kGroups / c.tokens, tok = group / per, g = group % per;
+  const Place at = place_of(lane, P.rot, INTER);
+  float w[16], acc[16];
+  {
+    Raw<T> x;
+    x.load(isq ? qw : kw, at);
 #pragma unroll
-  for (int i = 0; i < S::kVec; ++i) aq[i] = ak[i] = 0.f;
-  for (long long t0 = (long long)blockIdx.x * tokens; t0 < P.rows;
-       t0 += (long long)gridDim.x * tokens) {
-    const int nt = int(min((long long)tokens, P.rows - t0));
-    const int items = nt * heads;
+    for (int i = 0; i < 16; ++i) {
+      w[i] = x.get(i);
+      acc[i] = 0.f;
+    }
+  }
+  for (long long set = isq ? blockIdx.x : blockIdx.x - cq.blocks; set < c.sets; set += c.blocks) {
+    const long long t0 = set / c.chunks * c.tokens, r = t0 + tok;
+    const int h0 = int(set % c.chunks) * c.span, h1 = min(c.heads, h0 + c.span);
+    const int nt = int(min((long long)c.tokens, P.rows - t0));
+    const bool there = tok < nt;
+    auto fetch = [&](int base, Raw<T>& x, Raw<T>& y) {
+      const int h = base + g;
+      if (there && h < h1) {
+        x.load(src + r * ss + h * D, at);
+        y.load(gsrc + r * gs + h * D, at);
+      } else {
+        x.clear();  // adds nothing to the sums
+        y.clear();
+      }
+    };
+    Raw<T> cx, cg, nx, ng;
+    fetch(h0, cx, cg);
     __syncthreads();  // the previous tokens' angles are read
     fill_angles(cs, t0, nt, P.rot >> 1, inv_freq, pos);
     __syncthreads();
-    for (int base = 0; base < items; base += S::kSlots * kLoads) {
-      uint4 rx[kLoads], rg[kLoads];
-      int tok[kLoads], head[kLoads];
+    float2 ang[8];
+    my_angles(ang, cs, tok, lane, at.turned);
+    for (int base = h0; base < h1; base += per) {
+      fetch(base + per, nx, ng);
+      float x[16], y[16], sum = 0.f, tu = 0.f;
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        const int it = base + u * S::kSlots + slot;
-        tok[u] = it < items ? it / heads : -1;
-        head[u] = it - max(tok[u], 0) * heads;
-        rx[u] = rg[u] = make_uint4(0, 0, 0, 0);
-        if (tok[u] >= 0) {
-          const long long r = t0 + tok[u];
-          const bool isq = head[u] < P.hq;
-          const int h = (isq ? head[u] : head[u] - P.hq) * D + e0;
-          rx[u] = *reinterpret_cast<const uint4*>((isq ? q + r * P.qs : k + r * P.ks) + h);
-          rg[u] = *reinterpret_cast<const uint4*>((isq ? gq + r * P.qos : gk + r * P.kos) + h);
-        }
+      for (int i = 0; i < 16; ++i) {
+        x[i] = cx.get(i);
+        y[i] = cg.get(i);
+        sum += x[i] * x[i];
       }
+      const float mean = row_sum<kLanes>(sum) * (1.f / D);
+      // a row that is not there adds nothing (eps may be 0)
+      const float rr = there && base + g < h1 ? rsqrtf(mean + P.eps) : 0.f;
+      rotate<INTER>(y, ang, -1.f);
 #pragma unroll
-      for (int u = 0; u < kLoads; ++u) {
-        if (base + u * S::kSlots >= items) break;
-        const bool isq = head[u] < P.hq;
-        float x[S::kVec], g[S::kVec], ss = 0.f, tu = 0.f;
-        widen<T>(rx[u], x);
-        widen<T>(rg[u], g);
-#pragma unroll
-        for (int i = 0; i < S::kVec; ++i) ss += x[i] * x[i];
-        const float r = rsqrtf(row_sum<S::kVec, S::kLanes>(ss) * (1.f / D) + P.eps);
-        rotate(g, e0, P.rot, P.inter, cs[max(tok[u], 0)], -1.f);
-#pragma unroll
-        for (int i = 0; i < S::kVec; ++i) {
-          x[i] *= r;
-          const float gu = tok[u] >= 0 ? g[i] * x[i] : 0.f;
-          if (isq) aq[i] += gu; else ak[i] += gu;
-          g[i] *= isq ? wq[i] : wk[i];
-          tu += g[i] * x[i];
-        }
-        const float m = row_sum<S::kVec, S::kLanes>(tu) * (1.f / D);
-#pragma unroll
-        for (int i = 0; i < S::kVec; ++i) x[i] = r * (g[i] - x[i] * m);
-        if (tok[u] >= 0) {
-          const long long row = t0 + tok[u];
-          T* dst = isq ? dq + row * P.dqs + head[u] * D : dk + row * P.dks + (head[u] - P.hq) * D;
-          *reinterpret_cast<uint4*>(dst + e0) = narrow<T>(x);
-        }
+      for (int i = 0; i < 16; ++i) {
+        x[i] *= rr;
+        acc[i] += y[i] * x[i];
+        y[i] *= w[i];
+        tu += y[i] * x[i];
       }
+      const float m = row_sum<kLanes>(tu) * (1.f / D);
+#pragma unroll
+      for (int i = 0; i < 16; ++i) cx.set(i, rr * (y[i] - x[i] * m));
+      if (there && base + g < h1) cx.store(dst + r * ds + (base + g) * D, at);
+      cx = nx;
+      cg = ng;
     }
   }
 #pragma unroll
-  for (int which = 0; which < 2; ++which) {
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < S::kVec; ++i) sums[slot][e0 + i] = which ? ak[i] : aq[i];
-    __syncthreads();
-    if (threadIdx.x < D) {
-      float s = 0.f;
-      for (int r = 0; r < S::kSlots; ++r) s += sums[r][threadIdx.x];
-      part[((long long)blockIdx.x * 2 + which) * D + threadIdx.x] = s;
-    }
+  for (int i = 0; i < 16; ++i) sums[group][i < 8 ? at.a + i : at.b + i - 8] = acc[i];
+  __syncthreads();
+  if (threadIdx.x < D) {
+    float s = 0.f;
+    for (int x = 0; x < kGroups; ++x) s += sums[x][threadIdx.x];
+    part[(long long)blockIdx.x * D + threadIdx.x] = s;
   }
 }
 
-// dw[which][d] = sum over blocks of part[block][which][d], in a fixed order.
+// dw[d] = sum over blocks of part[block][d], in a fixed order: 32 columns of one weight
+// per block (blockIdx.x: query or key heads, y: columns).
 __global__ void __launch_bounds__(1024)
-norm_rope_weights_kernel(const float* part, int blocks, int D, float* dqw, float* dkw) {
-  __shared__ double sums[1024];
+norm_rope_weights_kernel(const float* part, int blocks_q, int blocks_k, int D, float* dqw,
+                         float* dkw) {
+  __shared__ double sums[32][32];
   float* dst = blockIdx.x ? dkw : dqw;
-  const int d = threadIdx.x % D, lane = threadIdx.x / D, lanes = 1024 / D;
+  const int c = threadIdx.x & 31, lane = threadIdx.x >> 5, d = blockIdx.y * 32 + c;
+  const int n = blockIdx.x ? blocks_k : blocks_q;
+  if (blockIdx.x) part += (long long)blocks_q * D;
   double s = 0.0;
-  for (int b = lane; b < blocks; b += lanes) s += part[((long long)b * 2 + blockIdx.x) * D + d];
-  sums[threadIdx.x] = s;
+#pragma unroll 8
+  for (int b = lane; b < n; b += 32) s += part[(long long)b * D + d];
+  sums[lane][c] = s;
   __syncthreads();
-  if (threadIdx.x < D && dst) {
-    for (int l = 1; l < lanes; ++l) s += sums[l * D + d];
+  if (lane == 0 && dst) {
+    for (int l = 1; l < 32; ++l) s += sums[l][c];
     dst[d] = float(s);
   }
 }
 
-// A block per token until every SM has several, then kTokens each.
-int tokens_per_block(long long rows) { return rows <= 148 * 8 ? 1 : kTokens; }
+// Few tokens: one at a time and a block per row group, so that every row is its own
+// thread group's; many: enough that a thread walks several heads of its token.
+Cut cut_of(long long rows, int heads, int D, int max_blocks) {
+  const int groups = kThreads / (D / 16);
+  Cut c{};
+  c.heads = heads;
+  if (heads == 0) return c;
+  c.tokens = rows <= 148 * 8 ? 1 : heads >= 32 ? 8 : 32;
+  c.span = c.tokens == 1 ? groups : heads;
+  c.chunks = (heads + c.span - 1) / c.span;
+  c.sets = (rows + c.tokens - 1) / c.tokens * c.chunks;
+  c.blocks = int(min(c.sets, (long long)max_blocks));
+  return c;
+}
 
 template <typename T, int D>
 cudaError_t forward(const NormRope& P, const void* q, const void* k, const void* qw,
                     const void* kw, const double* f, const int64_t* pos, void* qo, void* ko,
                     cudaStream_t s) {
-  const int tok = tokens_per_block(P.rows);
-  norm_rope_kernel<T, D><<<unsigned((P.rows + tok - 1) / tok), kThreads, 0, s>>>(
-      P, tok, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(qw),
+  const Cut cq = cut_of(P.rows, P.hq, D, 1 << 30), ck = cut_of(P.rows, P.hk, D, 1 << 30);
+  auto kern = P.inter ? norm_rope_kernel<T, D, true> : norm_rope_kernel<T, D, false>;
+  kern<<<unsigned(cq.blocks + ck.blocks), kThreads, 0, s>>>(
+      P, cq, ck, static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(qw),
       static_cast<const T*>(kw), f, pos, static_cast<T*>(qo), static_cast<T*>(ko));
   return cudaGetLastError();
 }
+
+// Blocks of the backward pass: each leaves one partial sum per weight.
+constexpr int kBackwardBlocks = 148 * 8;
 
 template <typename T, int D>
 cudaError_t backward(const NormRope& P, const void* gq, const void* gk, const void* q,
                      const void* k, const void* qw, const void* kw, const double* f,
                      const int64_t* pos, void* dq, void* dk, float* dqw, float* dkw, float* part,
                      cudaStream_t s) {
-  const int blocks = norm_rope_partials(P);
-  norm_rope_backward_kernel<T, D><<<blocks, kThreads, 0, s>>>(
-      P, tokens_per_block(P.rows), static_cast<const T*>(gq), static_cast<const T*>(gk),
-      static_cast<const T*>(q), static_cast<const T*>(k), static_cast<const T*>(qw),
-      static_cast<const T*>(kw), f, pos, static_cast<T*>(dq), static_cast<T*>(dk), part);
+  const Cut cq = cut_of(P.rows, P.hq, D, kBackwardBlocks);
+  const Cut ck = cut_of(P.rows, P.hk, D, kBackwardBlocks);
+  auto kern = P.inter ? norm_rope_backward_kernel<T, D, true>
+                      : norm_rope_backward_kernel<T, D, false>;
+  kern<<<cq.blocks + ck.blocks, kThreads, 0, s>>>(
+      P, cq, ck, static_cast<const T*>(gq), static_cast<const T*>(gk), static_cast<const T*>(q),
+      static_cast<const T*>(k), static_cast<const T*>(qw), static_cast<const T*>(kw), f, pos,
+      static_cast<T*>(dq), static_cast<T*>(dk), part);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  norm_rope_weights_kernel<<<2, 1024, 0, s>>>(part, blocks, D, dqw, P.hk ? dkw : nullptr);
+  norm_rope_weights_kernel<<<dim3(P.hk ? 2 : 1, D / 32), 1024, 0, s>>>(part, cq.blocks, ck.blocks,
+                                                                       D, dqw, dkw);
   return cudaGetLastError();
 }
 
 }  // namespace
 
 int norm_rope_partials(const NormRope& P) {
-  const int tok = tokens_per_block(P.rows);
-  return int(min((P.rows + tok - 1) / tok, 148LL * 6));
+  return cut_of(P.rows, P.hq, P.D, kBackwardBlocks).blocks +
+         cut_of(P.rows, P.hk, P.D, kBackwardBlocks).blocks;
 }
 
 cudaError_t launch_norm_rope(const NormRope& P, const void* q, const void* k, const void* qw,

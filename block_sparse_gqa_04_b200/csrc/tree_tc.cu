@@ -614,7 +614,7 @@ cudaError_t tree_tc(const Tree& A, const void* q, const void* k, const void* v, 
   tree_prep_kernel<<<A.mask_stride ? A.d.B : 1, 256, 0, s>>>(A.mask, A.mask_stride, A.d.Sq, A.bits,
                                                              status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  tree_tc_kernel<D><<<tree_ctas(), kThreads, smem_bytes<D>(), s>>>(
+  tree_tc_kernel<D><<<tree_ctas(A.d.f32), kThreads, smem_bytes<D>(), s>>>(
       mk, mv, A, static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(out), lse,
       status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
