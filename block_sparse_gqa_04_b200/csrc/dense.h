@@ -51,6 +51,7 @@ struct Tree {
   const int32_t* kv_lens;
   int rows;              // (node, head) rows of one work unit
   int groups;            // units per (sequence, key head)
+  bool q_boxes;          // tensor cores: 128 rows are the heads of whole nodes
   uint4* bits;           // tensor cores: the masks as bits, [masks, nodes + 1]
   float* part_o;         // [2 * CTAs, D, rows] unnormalised partial outputs
   float2* part_ml;       // [2 * CTAs, rows] base-2 running maximum and sum

@@ -539,16 +539,20 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
 }  // namespace
 
 // ---------------------------------------------------------------------------
-// Merge of the partial states of units that a share's border cut: a block per unit and
-// 8 of its columns, a thread per row (the partial outputs have rows innermost).
+// Merge of the partial states of units that a share's border cut: a thread per row (the
+// partial outputs have rows innermost) and 8 columns; a block of 128 threads holds
+// `rows` rows (a power of two) of one unit and as many groups of columns as fit.
 // ---------------------------------------------------------------------------
+constexpr int kJoinThreads = 128;
+
 template <typename T, int D>
-__global__ void __launch_bounds__(kTcTreeRows)
-tree_combine_kernel(Tree A, int ctas, T* __restrict__ out, float* __restrict__ lse) {
+__global__ void __launch_bounds__(kJoinThreads)
+tree_combine_kernel(Tree A, int ctas, int rows, T* __restrict__ out, float* __restrict__ lse) {
   const Dense& P = A.d;
-  const int nodes = P.Sq, per = P.Hkv * A.groups;
-  const int c0d = (blockIdx.x % (D / 8)) * 8, unit = (blockIdx.x / (D / 8)) % per;
-  const int b = blockIdx.x / (D / 8) / per, lane = threadIdx.x & 31;
+  const int nodes = P.Sq, per = P.Hkv * A.groups, blocks = max(1, D / 8 * rows / kJoinThreads);
+  const int c0d = (blockIdx.x % blocks * (kJoinThreads / rows) + threadIdx.x / rows) * 8;
+  const int unit = (blockIdx.x / blocks) % per;
+  const int b = blockIdx.x / blocks / per, lane = threadIdx.x & 31;
   const TreeSpan span = tree_span(A, ctas);
   long long before = 0;  // key tiles of the sequences before b
   for (int i = lane; i < b; i += 32) before += tree_seq(A, i).tiles;
@@ -558,8 +562,8 @@ tree_combine_kernel(Tree A, int ctas, T* __restrict__ out, float* __restrict__ l
   const long long t0 = before * per + (long long)unit * n;
   const int c0 = int(t0 / span.share), c1 = int((t0 + n - 1) / span.share);
   if (c0 == c1) return;
-  const int g = unit / A.groups, row0 = (unit % A.groups) * A.rows, r = threadIdx.x;
-  if (r >= min(A.rows, nodes * P.G - row0)) return;
+  const int g = unit / A.groups, row0 = (unit % A.groups) * A.rows, r = threadIdx.x % rows;
+  if (r >= min(A.rows, nodes * P.G - row0) || c0d >= D) return;
   // the unit's first piece lies in c0's slot 1, the others in their CTA's slot 0
   auto at = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * A.rows; };
   float m = -INFINITY;
@@ -651,15 +655,18 @@ cudaError_t tree(const Tree& A, const void* q, const void* k, const void* v, voi
 }  // namespace
 
 cudaError_t launch_tree_combine(const Tree& A, void* out, float* lse, cudaStream_t s) {
-  const long long blocks = (long long)A.d.B * A.d.Hkv * A.groups * (A.d.D / 8);
+  int rows = 8;
+  while (rows < std::min(A.rows, A.d.Sq * A.d.G)) rows *= 2;
+  const long long blocks = (long long)A.d.B * A.d.Hkv * A.groups *
+                           std::max(1, A.d.D / 8 * rows / kJoinThreads);
   const int ctas = tree_ctas(A.d.f32);
   if (A.d.f32) {
     auto kern = A.d.D == 128 ? tree_combine_kernel<float, 128> : tree_combine_kernel<float, 64>;
-    kern<<<unsigned(blocks), A.rows, 0, s>>>(A, ctas, static_cast<float*>(out), lse);
+    kern<<<unsigned(blocks), kJoinThreads, 0, s>>>(A, ctas, rows, static_cast<float*>(out), lse);
   } else {
     auto kern = A.d.D == 128 ? tree_combine_kernel<__nv_bfloat16, 128>
                              : tree_combine_kernel<__nv_bfloat16, 64>;
-    kern<<<unsigned(blocks), A.rows, 0, s>>>(A, ctas, static_cast<__nv_bfloat16*>(out), lse);
+    kern<<<unsigned(blocks), kJoinThreads, 0, s>>>(A, ctas, rows, static_cast<__nv_bfloat16*>(out), lse);
   }
   return cudaGetLastError();
 }

@@ -27,14 +27,15 @@ __device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int r1) {
   __syncwarp();
 }
 
-// Rows of `heads` heads of D: tiles of box_rows rows of one head, 64 dims at a time.
+// Rows of `heads` heads of D: tiles of box_rows rows of box_heads
+// heads, 64 dims at a time.
 inline cudaError_t encode_rows(CUtensorMap* map, const void* base, int D, int heads, long long rows,
-                               int box_rows = kDenseTile) {
+                               int box_rows = kDenseTile, int box_heads = 1) {
   auto enc = encode_fn();
   if (!enc) return cudaErrorNotSupported;
   cuuint64_t dims[3] = {cuuint64_t(D), cuuint64_t(heads), cuuint64_t(rows)};
   cuuint64_t strides[2] = {cuuint64_t(D) * 2, cuuint64_t(heads) * D * 2};
-  cuuint32_t box[3] = {64, 1, cuuint32_t(box_rows)}, estr[3] = {1, 1, 1};
+  cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)}, estr[3] = {1, 1, 1};
   return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box,
              estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,

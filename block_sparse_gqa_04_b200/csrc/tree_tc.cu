@@ -12,7 +12,7 @@
 // each with its own softmax warpgroup, running maximum and sum, and accumulator O, so that one chain's MMAs and copies run under the other's softmax;
 // the epilogue joins the two.  Scores, probabilities and the moving maximum are as in
 // the forward pass over whole prompts.  K and V tiles come through a ring of TMA
-// stages (160 KB in flight); Q rows are gathered by one warp, a piece ahead.
+// stages (160 KB); Q comes a piece ahead.
 //
 // Which drafted tokens a node sees comes as one bit mask per node, and which are seen
 // at all as one per sequence, formed by a small launch before.  V rows of unseen tokens
@@ -112,7 +112,8 @@ __device__ __forceinline__ uint32_t bits_at(const uint4& m, int pos) {
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1)
-tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
+tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
+               const __grid_constant__ CUtensorMap tmap_k,
                const __grid_constant__ CUtensorMap tmap_v, Tree A,
                const __nv_bfloat16* __restrict__ q, __nv_bfloat16* __restrict__ out,
                float* __restrict__ lse, int* __restrict__ status) {
@@ -175,7 +176,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
       TreeWalk w;
       w.begin(A, blockIdx.x, tree_span(A, gridDim.x));
       if (tc::elect_one()) {
-        tc::ArmedRing kv_armed;
+        tc::ArmedRing kv_armed, q_armed;
         int stage = 0;
         uint32_t phase = 0;
         for (int ii = 0; !failed; ++ii) {
@@ -191,30 +192,55 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                                   p.kt0, p.kt1 - p.kt0, p.len, p.slot};
           tc::mbar_arrive(&bars->i_full[slot]);
           if (!live) break;
+          // Q rows of (node, head) are heads of consecutive nodes: one box per half
+          if (A.q_boxes) {
+            const int qs = ii & 1;
+            if (!tc::mbar_wait(&bars->q_empty[qs], ((ii >> 1) & 1) ^ 1, abort)) {
+              failed = true;
+              break;
+            }
+            tc::mbar_arrive_expect_tx(&bars->q_full[qs], C::kTileBytes);
+            q_armed.note(qs, (ii >> 1) & 1);
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_load_3d(qbuf + qs * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[qs],
+                              64 * h, p.g * P.G, p.b * nodes + row0 / P.G);
+          }
+          // In the order of use, K0 K1 V0 K2 V1 K3 ..: a V tile that came with its K tile
+          // would hold a stage through the whole softmax.
           const int32_t* pages = P.table ? P.table + (long long)p.b * P.table_w : nullptr;
-          int page = pages ? pages[p.kt0] : 0;
-          for (int j = p.kt0; j < p.kt1 && !failed; ++j) {
-            int row = p.b * P.Skv + j * kDenseTile;
-            if (pages) {
-              const bool in = page >= 0 && page < P.pages;
-              if (!in) atomicOr(status, kStatusBadPage);
-              row = in ? page * kDenseTile : 0;
-              if (j + 1 < p.kt1) page = pages[j + 1];  // on its way during this tile's copies
-            }
+          const int n = p.kt1 - p.kt0;
+          int page = pages ? pages[p.kt0] : 0, next = 0;   // next: K tile whose row comes next
+          auto next_row = [&]() -> int {
+            const int t = p.kt0 + next++;
+            if (!pages) return p.b * P.Skv + t * kDenseTile;
+            const bool in = page >= 0 && page < P.pages;
+            if (!in) atomicOr(status, kStatusBadPage);
+            const int row = in ? page * kDenseTile : 0;
+            if (next < n) page = pages[t + 1];  // on its way during this tile's copies
+            return row;
+          };
+          auto copy = [&](const CUtensorMap* map, int row) {
+            if (!tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1, abort)) { failed = true; return; }
+            uint64_t* fb = &bars->kv_full[stage];
+            uint8_t* dst = kvbuf + stage * C::kTileBytes;
+            tc::mbar_arrive_expect_tx(fb, C::kTileBytes);
+            kv_armed.note(stage, phase);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              if (!tc::mbar_wait(&bars->kv_empty[stage], phase ^ 1, abort)) { failed = true; break; }
-              uint64_t* fb = &bars->kv_full[stage];
-              uint8_t* dst = kvbuf + stage * C::kTileBytes;
-              tc::mbar_arrive_expect_tx(fb, C::kTileBytes);
-              kv_armed.note(stage, phase);
-#pragma unroll
-              for (int h = 0; h < D / 64; ++h)
-                tc::tma_load_3d(dst + h * C::kHalf, x ? &tmap_v : &tmap_k, fb, 64 * h, p.g, row);
-              if (++stage == C::kStages) { stage = 0; phase ^= 1; }
-            }
+            for (int h = 0; h < D / 64; ++h)
+              tc::tma_load_3d(dst + h * C::kHalf, map, fb, 64 * h, p.g, row);
+            if (++stage == C::kStages) { stage = 0; phase ^= 1; }
+          };
+          int r0 = next_row(), r1 = 0;
+          copy(&tmap_k, r0);
+          if (n > 1 && !failed) copy(&tmap_k, r1 = next_row());
+          for (int x = 0; x < n && !failed; ++x) {
+            copy(&tmap_v, r0);
+            r0 = r1;
+            if (x + 2 < n && !failed) copy(&tmap_k, r1 = next_row());
           }
         }
+        if (!q_armed.drain(bars->q_full)) failed = true;
         if (!kv_armed.drain(bars->kv_full)) failed = true;
       }
     } else if (warp == 1) {
@@ -227,9 +253,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
         const uint32_t qd = uint32_t(tc::sdesc_sw128(tc::smem_addr(qbuf), 16, 1024));
         const uint32_t kd = uint32_t(tc::sdesc_sw128(tc::smem_addr(kvbuf), 16, 1024));
         const uint32_t vd = uint32_t(tc::sdesc_sw128(tc::smem_addr(kvbuf), C::kHalf, 1024));
-        int ii = 0, kx = 0, vx = 1;   // pieces; ring positions of the next K and V tile
+        int ii = 0, rx = 0;   // pieces; ring position of the next tile, in order of use
         uint32_t ppar = 0;
-        auto advance = [](int x) { return x + 2 >= C::kStages ? x + 2 - C::kStages : x + 2; };
+        auto advance = [&]() { rx = rx + 1 == C::kStages ? 0 : rx + 1; };
         auto fetch = [&](Item* it) -> bool {
           const int slot = ii % kItems;
           if (!tc::mbar_spin(&bars->i_full[slot], (ii / kItems) & 1, abort)) return false;
@@ -240,7 +266,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
         };
         // S of tile x of the piece whose Q stage is qs
         auto scores = [&](int x, int qs, bool last) {
-          const uint32_t a = qd + qs * kTile16, b = kd + kx * kTile16;
+          const uint32_t a = qd + qs * kTile16, b = kd + rx * kTile16;
           const uint32_t st = tmem + (x & 1) * 256;
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
@@ -248,9 +274,9 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
             tc::mma_ss_lo(st, a + off, b + off, kHi, C::kIdescS, kk > 0 ? 1u : 0u);
           }
           tc::mma_commit(&bars->s_full[x & 1]);
-          tc::mma_commit(&bars->kv_empty[kx]);
+          tc::mma_commit(&bars->kv_empty[rx]);
           if (last) tc::mma_commit(&bars->q_empty[qs]);
-          kx = advance(kx);
+          advance();
         };
         Item cur{};
         failed = !fetch(&cur);
@@ -267,7 +293,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
           int off = cur.len - cur.kt0 * 128;   // tile's row of drafted token 0
           for (int x = 0; x < n; ++x, off -= 128) {
             const int e = x & 1;
-            const uint32_t st = tmem + e * 256, v = vd + vx * kTile16;
+            const uint32_t st = tmem + e * 256, v = vd + rx * kTile16;
             if (x == n - 1 && !fetch(&cur)) { failed = true; break; }
             if (!tc::mbar_spin(&bars->p_full[e], (ppar >> e) & 1, abort)) { failed = true; break; }
             ppar ^= 1u << e;
@@ -284,8 +310,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
                 tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
                               kk > 0 ? 1u : uint32_t(x >= 2));
             }
-            tc::mma_commit(&bars->kv_empty[vx]);
-            vx = advance(vx);
+            tc::mma_commit(&bars->kv_empty[rx]);
+            advance();
             if (x + 2 >= n) tc::mma_commit(&bars->o_done[e]);
             if (x + 2 < n) {
               scores(x + 2, qs, x + 3 == n);
@@ -302,8 +328,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
       // One arrival per tile at p_full of its chain: V has landed, with the rows that no
       // node sees zeroed, K of the scores that follow too, the epilogue has read the
       // chain's previous O.
-      int ii = 0, kx = 0, vx = 1;
-      uint32_t kp = 0, vp = 0, un[2] = {0, 0}, on[2] = {0, 0};
+      int ii = 0, rx = 0;
+      uint32_t rp = 0, un[2] = {0, 0}, on[2] = {0, 0};
       auto fetch = [&](Item* it) -> bool {
         const int slot = ii % kItems;
         if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) return false;
@@ -313,16 +339,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
         ++ii;
         return true;
       };
-      auto landed = [&](int* x, uint32_t* ph) -> bool {
-        if (!warp_wait(&bars->kv_full[*x], *ph, abort)) return false;
-        *x += 2;
-        if (*x >= C::kStages) { *x -= C::kStages; *ph ^= 1; }
+      auto landed = [&]() -> bool {  // the next tile in the order of use
+        if (!warp_wait(&bars->kv_full[rx], rp, abort)) return false;
+        if (++rx == C::kStages) { rx = 0; rp ^= 1; }
         return true;
       };
       // Q of the piece just fetched, and its first K tiles
       auto start = [&](const Item& it) -> bool {
         return warp_wait(&bars->q_full[(ii - 1) & 1], ((ii - 1) >> 1) & 1, abort) &&
-               landed(&kx, &kp) && (it.n == 1 || landed(&kx, &kp));
+               landed() && (it.n == 1 || landed());
       };
       Item cur{}, nxt{};
       failed = !fetch(&cur) || (cur.live && !start(cur));
@@ -330,8 +355,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
       while (!failed && cur.live) {
         int off = cur.len - cur.kt0 * 128;
         for (int x = 0; x < cur.n; ++x, off -= 128) {
-          const int e = x & 1, vs = vx;
-          if (!landed(&vx, &vp)) { failed = true; break; }
+          const int e = x & 1, vs = rx;
+          if (!landed()) { failed = true; break; }
           if (off < 128) {
             uint8_t* v = kvbuf + vs * C::kTileBytes;
             const int rows = (min(128, off + nodes) + 15) & ~15;
@@ -353,7 +378,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
           // the arrival belongs to this tile: the chain's tile before is over
           if ((on[e] > 0 && !warp_wait(&bars->p_full[e], (on[e] & 1) ^ 1, abort)) ||
               (x < 2 && !warp_wait(&bars->o_empty[e], (un[e]++ & 1) ^ 1, abort)) ||
-              (x + 2 < cur.n && !landed(&kx, &kp)) ||
+              (x + 2 < cur.n && !landed()) ||
               (x == cur.n - 1 && (!fetch(&nxt) || (nxt.live && !start(nxt))))) {
             failed = true;
             break;
@@ -364,7 +389,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
         cur = nxt;
       }
     } else {
-      // ---------------- Q rows ----------------
+      // ---------------- Q rows, where a box does not fetch them ----------------
       constexpr int kChunks = D / 8;   // 16-byte chunks of a row
       for (int ii = 0; !failed; ++ii) {
         const int slot = ii % kItems, qs = ii & 1;
@@ -373,6 +398,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
         if (!it.live) break;
+        if (A.q_boxes) continue;  // the producer's
         if (!warp_wait(&bars->q_empty[qs], ((ii >> 1) & 1) ^ 1, abort)) { failed = true; break; }
         uint8_t* dst = qbuf + qs * C::kTileBytes;
         const int total = it.rows * kChunks;
@@ -601,11 +627,15 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_k,
 }
 
 template <int D>
-cudaError_t tree_tc(const Tree& A, const void* q, const void* k, const void* v, void* out,
+cudaError_t tree_tc(const Tree& A_, const void* q, const void* k, const void* v, void* out,
                     float* lse, int32_t* status, cudaStream_t s) {
   static std::atomic<uint64_t> done{0};
-  CUtensorMap mk, mv;
-  cudaError_t e = encode_rows(&mk, k, D, A.d.Hkv, A.d.rows_k);
+  CUtensorMap mq, mk, mv;
+  Tree A = A_;
+  A.q_boxes = 128 % A.d.G == 0;
+  cudaError_t e = encode_rows(&mq, q, D, A.d.Hq, A.d.rows_q, A.q_boxes ? 128 / A.d.G : 1,
+                              A.q_boxes ? A.d.G : 1);
+  if (e == cudaSuccess) e = encode_rows(&mk, k, D, A.d.Hkv, A.d.rows_k);
   if (e == cudaSuccess) e = encode_rows(&mv, v, D, A.d.Hkv, A.d.rows_k);
   if (e == cudaSuccess)
     e = prepare_kernel(&done, tree_tc_kernel<D>, smem_bytes<D>(), kRegsCtl + kRegsEpi + 2 * kRegsSoftmax,
@@ -615,7 +645,7 @@ cudaError_t tree_tc(const Tree& A, const void* q, const void* k, const void* v, 
                                                              status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   tree_tc_kernel<D><<<tree_ctas(A.d.f32), kThreads, smem_bytes<D>(), s>>>(
-      mk, mv, A, static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(out), lse,
+      mq, mk, mv, A, static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(out), lse,
       status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   return launch_tree_combine(A, out, lse, s);
