@@ -79,6 +79,10 @@ struct TreeSpan {
   long long share;  // of one CTA
 };
 
+__device__ __forceinline__ long long tree_share(long long total, int ctas) {
+  return (total + ctas - 1) / ctas;
+}
+
 // Called by whole warps.
 __device__ __forceinline__ TreeSpan tree_span(const Tree& T, int ctas) {
   const int lane = threadIdx.x & 31;
@@ -87,7 +91,7 @@ __device__ __forceinline__ TreeSpan tree_span(const Tree& T, int ctas) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(MSA_FULL_MASK, sum, o);
   const long long total = sum * T.d.Hkv * T.groups;
-  return TreeSpan{total, (total + ctas - 1) / ctas};
+  return TreeSpan{total, tree_share(total, ctas)};
 }
 
 // Walks the pieces of the share [at, end).

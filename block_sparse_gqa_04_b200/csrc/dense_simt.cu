@@ -553,31 +553,54 @@ tree_combine_kernel(Tree A, int ctas, int rows, T* __restrict__ out, float* __re
   const int c0d = (blockIdx.x % blocks * (kJoinThreads / rows) + threadIdx.x / rows) * 8;
   const int unit = (blockIdx.x / blocks) % per;
   const int b = blockIdx.x / blocks / per, lane = threadIdx.x & 31;
-  const TreeSpan span = tree_span(A, ctas);
-  long long before = 0;  // key tiles of the sequences before b
-  for (int i = lane; i < b; i += 32) before += tree_seq(A, i).tiles;
+  long long total = 0, before = 0;  // key tiles of all sequences, of those before b
+  for (int i = lane; i < P.B; i += 32) {
+    const int t = tree_seq(A, i).tiles;
+    total += t;
+    if (i < b) before += t;
+  }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(MSA_FULL_MASK, before, o);
+  for (int o = 16; o > 0; o >>= 1) {
+    total += __shfl_xor_sync(MSA_FULL_MASK, total, o);
+    before += __shfl_xor_sync(MSA_FULL_MASK, before, o);
+  }
+  const long long share = tree_share(total * per, ctas);
   const int n = tree_seq(A, b).tiles;
   const long long t0 = before * per + (long long)unit * n;
-  const int c0 = int(t0 / span.share), c1 = int((t0 + n - 1) / span.share);
+  const int c0 = int(t0 / share), c1 = int((t0 + n - 1) / share);
   if (c0 == c1) return;
   const int g = unit / A.groups, row0 = (unit % A.groups) * A.rows, r = threadIdx.x % rows;
   if (r >= min(A.rows, nodes * P.G - row0) || c0d >= D) return;
-  // the unit's first piece lies in c0's slot 1, the others in their CTA's slot 0
-  auto at = [&](int c) { return (long long)(2 * c + (c == c0 ? 1 : 0)) * A.rows; };
-  float m = -INFINITY;
-  for (int c = c0; c <= c1; ++c) m = fmaxf(m, A.part_ml[at(c) + r].x);
-  const float base = m == -INFINITY ? 0.f : m;
-  float o[8] = {}, l = 0.f;
-#pragma unroll 4
-  for (int c = c0; c <= c1; ++c) {
-    const float2 ml = A.part_ml[at(c) + r];
-    const float* x = A.part_o + at(c) * D + (long long)c0d * A.rows + r;
-    const float w = exp2f(ml.x - base);
-    l += w * ml.y;
+  // Four pieces' loads at a time: the join is a few round trips to L2 long.  The unit's
+  // first piece lies in c0's slot 1, the others in their CTA's slot 0.
+  float m = -INFINITY, o[8] = {}, l = 0.f;
+  for (int c = c0; c <= c1; c += 4) {
+    float2 ml[4];
+    float x[4][8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] += w * x[i * A.rows];
+    for (int u = 0; u < 4; ++u) {
+      const bool there = c + u <= c1;
+      const long long at = (long long)(2 * (there ? c + u : c) + (c + u == c0 ? 1 : 0)) * A.rows;
+      const float* src = A.part_o + at * D + (long long)c0d * A.rows + r;
+      ml[u] = there ? A.part_ml[at + r] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x[u][i] = there ? src[i * A.rows] : 0.f;
+    }
+    float top = m;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) top = fmaxf(top, ml[u].x);
+    const float base = top == -INFINITY ? 0.f : top, keep = exp2f(m - base);
+    m = top;
+    l *= keep;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[i] *= keep;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      const float w = exp2f(ml[u].x - base);
+      l += w * ml[u].y;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[i] += w * x[u][i];
+    }
   }
   const long long row = ((long long)b * nodes + (row0 + r) / P.G) * P.Hq + g * P.G + (row0 + r) % P.G;
   const float inv = l == 0.f ? 0.f : 1.f / l;
