@@ -28,8 +28,9 @@
 namespace msa {
 namespace {
 
-// warp 0 items and TMA, warp 1 MMA, warp 2 waits for it, warp 3 idle, warps 4-11 elementwise
-constexpr int kThreads = 384;
+// warp 0 items and TMA, warp 1 MMA, warp 2 waits for it, warp 3 idle, warps 4-19 elementwise
+constexpr int kWarpgroups = 4;  // elementwise; each takes 32 columns of a tile
+constexpr int kThreads = 128 + 128 * kWarpgroups;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItems = 2;
 
@@ -68,26 +69,27 @@ __device__ __forceinline__ void issue_nt(uint32_t d, uint32_t a, uint32_t b) {
   }
 }
 
-// G += A B over `groups` groups of 16 rows of B (MN-major tile); A in TMEM as bf16, its
-// first 64 columns of elements at a, the others 64 TMEM columns on.
+// G += A B over `groups` groups of 16 rows of B (MN-major tile); A in TMEM as bf16, 32
+// columns of elements in 16 TMEM columns at a, the next 32 at a + 32 and so on (each
+// warpgroup writes over what it has read itself).
 template <int D>
 __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint32_t b, int groups,
                                          uint32_t accumulate) {
   if (groups == 8) {
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
-      tc::mma_ts_lo(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * 128, kHi, Cfg<D>::kIdescG,
+      tc::mma_ts_lo(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * 128, kHi, Cfg<D>::kIdescG,
                     kk > 0 ? 1u : accumulate);
   } else {
 #pragma unroll 1
     for (int kk = 0; kk < groups; ++kk)
-      tc::mma_ts_lo(d, a + (kk >> 2) * 64 + (kk & 3) * 8, b + kk * 128, kHi, Cfg<D>::kIdescG,
+      tc::mma_ts_lo(d, a + (kk >> 1) * 32 + (kk & 1) * 8, b + kk * 128, kHi, Cfg<D>::kIdescG,
                     kk > 0 ? 1u : accumulate);
   }
 }
 
 // ---------------------------------------------------------------------------
-// -c lse and delta = sum_d dout out per (head, row), rows of a sequence padded to
+// -c lse and -delta = -sum_d dout out per (head, row), rows of a sequence padded to
 // groups of 16 (padding: -inf, so that P = 0, and 0): one warp per (16 rows, head).
 // ---------------------------------------------------------------------------
 template <int D>
@@ -131,7 +133,7 @@ dense_prep_kernel(Dense P, const __nv_bfloat16* __restrict__ dout,
     const bool there = i0 + lane < s.nq;
     const long long at = (long long)h * P.rows_pad + x0 + lane;
     nl[at] = there ? -kLog2e * lse[(long long)(s.q0 + i0 + lane) * P.Hq + h] : -INFINITY;
-    dl[at] = there ? mine : 0.f;
+    dl[at] = there ? -mine : 0.f;
   }
 }
 
@@ -226,14 +228,14 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
     tc::mbar_init(&bars->first_full, 1);
     tc::mbar_init(&bars->s_full, 1);
-    tc::mbar_init(&bars->p_full, 9);   // 8 elementwise warps and warp 2
+    tc::mbar_init(&bars->p_full, 4 * kWarpgroups + 1);   // elementwise warps and warp 2
     tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->ds_full, 9);
+    tc::mbar_init(&bars->ds_full, 4 * kWarpgroups + 1);
     tc::mbar_init(&bars->acc_full, 1);
-    tc::mbar_init(&bars->acc_empty, 8);
+    tc::mbar_init(&bars->acc_empty, 4 * kWarpgroups);
     for (int i = 0; i < kItems; ++i) {
       tc::mbar_init(&bars->i_full[i], 1);
-      tc::mbar_init(&bars->i_empty[i], 10);  // warps 1, 2 and 8 elementwise warps
+      tc::mbar_init(&bars->i_empty[i], 4 * kWarpgroups + 2);  // warps 1, 2, elementwise
     }
     tc::mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
@@ -412,11 +414,11 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       ++used;
     }
   } else if (warp >= 4) {
-    // ---------------- elementwise: P, dS, then the tile's dV (first warpgroup) or dK ----------------
-    const int half = (warp - 4) >> 2, quarter = warp & 3;
+    // ---------------- elementwise: P, dS, then the tile's dV (first half) or dK ----------------
+    const int wg = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
-    const uint32_t sa = ts + lanes + half * 64, pa = tp + lanes + half * 64;
+    const uint32_t sa = ts + lanes + wg * 32, pa = tp + lanes + wg * 32;
     const float sl2 = P.scale * kLog2e;
     const uint64_t sl2x2 = f2(sl2, sl2);
     int n = 0, used = 0;
@@ -428,76 +430,71 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (lane == 0) tc::mbar_arrive(&bars->i_empty[slot]);
       if (!it.live) break;
       const int tiles = it.nqt - it.qt0, steps = it.heads * tiles;
+      // first column of this warpgroup's that sees the thread's key, at the first tile
+      const int from0 = it.j0 + row - it.pos0 - it.qt0 * 128 - wg * 32;
+      int from = from0, left = tiles;
       for (int i = 0; i < steps; ++i, ++n) {
         const int s = n & 1;
         const uint32_t par = n & 1;
-        // first column of this half that sees the thread's key
-        const int from = it.j0 + row - it.pos0 - (it.qt0 + i % tiles) * 128 - half * 64;
         if (!warp_wait(&bars->q_full[s], (n >> 1) & 1, abort) ||
             !warp_wait(&bars->s_full, par, abort)) {
           failed = true;
           break;
         }
         tc::tc_fence_after();
-        uint32_t p[2][32];
-        tc::tmem_ld32(sa, p[0]);
-        tc::tmem_ld32(sa + 32, p[1]);
+        uint32_t p[32];
+        tc::tmem_ld32(sa, p);
         tc::tmem_ld_wait();
-        const float4* nl4 = reinterpret_cast<const float4*>(bars->nl[s] + half * 64);
+        const float4* nl4 = reinterpret_cast<const float4*>(bars->nl[s] + wg * 32);
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const float4 f = nl4[c * 8 + x / 4];
-            const uint64_t a = fma2(pair_of(&p[c][x]), sl2x2, f2(f.x, f.y));
-            const uint64_t b = fma2(pair_of(&p[c][x + 2]), sl2x2, f2(f.z, f.w));
-            p[c][x] = __float_as_uint(ex2_f32(lo_of(a)));
-            p[c][x + 1] = __float_as_uint(ex2_f32(hi_of(a)));
-            p[c][x + 2] = __float_as_uint(ex2_f32(lo_of(b)));
-            p[c][x + 3] = __float_as_uint(ex2_f32(hi_of(b)));
-          }
+        for (int x = 0; x < 32; x += 4) {
+          const float4 f = nl4[x / 4];
+          const uint64_t a = fma2(pair_of(&p[x]), sl2x2, f2(f.x, f.y));
+          const uint64_t b = fma2(pair_of(&p[x + 2]), sl2x2, f2(f.z, f.w));
+          p[x] = __float_as_uint(ex2_f32(lo_of(a)));
+          p[x + 1] = __float_as_uint(ex2_f32(hi_of(a)));
+          p[x + 2] = __float_as_uint(ex2_f32(lo_of(b)));
+          p[x + 3] = __float_as_uint(ex2_f32(hi_of(b)));
+        }
         if (__any_sync(MSA_FULL_MASK, from > 0)) {
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (c * 32 + x < from) p[c][x] = 0u;
-        }
-        {
-          uint32_t w[32];
-#pragma unroll
           for (int x = 0; x < 32; ++x)
-            w[x] = pack_bf16(__uint_as_float(p[x >> 4][(2 * x) & 31]),
-                             __uint_as_float(p[x >> 4][(2 * x + 1) & 31]));
-          tc::tmem_st32(sa, w);
+            if (x < from) p[x] = 0u;
         }
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x)
+          w[x] = pack_bf16(__uint_as_float(p[2 * x]), __uint_as_float(p[2 * x + 1]));
+        tmem_st8(sa, w);
+        tmem_st8(sa + 8, w + 8);
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->p_full);
         if (!warp_wait(&bars->dp_full, par, abort)) { failed = true; break; }
         tc::tc_fence_after();
-        const float4* dl4 = reinterpret_cast<const float4*>(bars->dl[s] + half * 64);
-        uint32_t w[32];
+        uint32_t d[32];
+        tc::tmem_ld32(pa, d);
+        tc::tmem_ld_wait();
+        const float4* dl4 = reinterpret_cast<const float4*>(bars->dl[s] + wg * 32);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t d[32];
-          tc::tmem_ld32(pa + c * 32, d);
-          tc::tmem_ld_wait();
-#pragma unroll
-          for (int x = 0; x < 32; x += 4) {
-            const float4 f = dl4[c * 8 + x / 4];
-            const uint64_t a = mul2(pair_of(&p[c][x]), add2(pair_of(&d[x]), f2(-f.x, -f.y)));
-            const uint64_t b = mul2(pair_of(&p[c][x + 2]), add2(pair_of(&d[x + 2]), f2(-f.z, -f.w)));
-            w[c * 16 + x / 2] = to_bf16x2(a);
-            w[c * 16 + x / 2 + 1] = to_bf16x2(b);
-          }
+        for (int x = 0; x < 32; x += 4) {
+          const float4 f = dl4[x / 4];  // -delta
+          w[x / 2] = to_bf16x2(mul2(pair_of(&p[x]), add2(pair_of(&d[x]), f2(f.x, f.y))));
+          w[x / 2 + 1] =
+              to_bf16x2(mul2(pair_of(&p[x + 2]), add2(pair_of(&d[x + 2]), f2(f.z, f.w))));
         }
-        tc::tmem_st32(pa, w);
+        tmem_st8(pa, w);
+        tmem_st8(pa + 8, w + 8);
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+        from -= 128;
+        if (--left == 0) {  // the next head
+          left = tiles;
+          from = from0;
+        }
       }
       if (failed) break;
       const bool any = steps > 0;
@@ -506,38 +503,37 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         tc::tc_fence_after();
         ++used;
       }
+      const int half = wg >> 1, col0 = (wg & 1) * (D / 2);
       const float scale = half ? P.scale : 1.f;
       const bool mine = it.j0 + row < it.nk;
-      const long long at = ((long long)(it.k0 + row) * P.Hkv + it.g) * D;
-      const uint32_t acc = (half ? tk : tv) + lanes;
+      const long long at = ((long long)(it.k0 + row) * P.Hkv + it.g) * D + col0;
+      const uint32_t acc = (half ? tk : tv) + lanes + col0;
       __nv_bfloat16* dst = half ? dk : dv;
       float* pdst = part + ((long long)(it.split * 2 + half) * P.rows_k * P.Hkv) * D;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        uint32_t o[32];
+      for (int c = 0; c < D / 2; c += 16) {
+        uint32_t o[16];
         __syncwarp();
         if (any) {
-          tc::tmem_ld32(acc + c * 32, o);
+          tc::tmem_ld16(acc + c, o);
           tc::tmem_ld_wait();
         } else {
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] = 0u;
+          for (int x = 0; x < 16; ++x) o[x] = 0u;
         }
         if (mine && PART) {
 #pragma unroll
-          for (int x = 0; x < 32; x += 4)
-            *reinterpret_cast<uint4*>(pdst + at + c * 32 + x) =
+          for (int x = 0; x < 16; x += 4)
+            *reinterpret_cast<uint4*>(pdst + at + c + x) =
                 make_uint4(o[x], o[x + 1], o[x + 2], o[x + 3]);
         } else if (mine) {
-          uint32_t w[16];
+          uint32_t w[8];
 #pragma unroll
-          for (int x = 0; x < 16; ++x)
+          for (int x = 0; x < 8; ++x)
             w[x] = pack_bf16(__uint_as_float(o[2 * x]) * scale,
                              __uint_as_float(o[2 * x + 1]) * scale);
-#pragma unroll
-          for (int x = 0; x < 16; x += 4)
-            *reinterpret_cast<uint4*>(dst + at + c * 32 + 2 * x) =
-                make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+          *reinterpret_cast<uint4*>(dst + at + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(dst + at + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
       if (any) {
@@ -573,10 +569,11 @@ struct RowBars {
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
   // first_full: Q, dO and the first K and V tiles are there; ds_full: dS written, and the
   // K and V tiles of the products after it are there
-  uint64_t first_full, s_full[2], dp_full, ds_full, acc_full, acc_empty;
+  uint64_t first_full, s_full[2], dp_full, ds_full, acc_full, acc_empty, r_full[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint64_t mma_done;
   RowItem item[kItems];
+  float rest[2][128];
   uint32_t tmem_base;
   int abort;
 };
@@ -585,6 +582,7 @@ template <int D>
 constexpr size_t row_smem() {
   return 1024 + size_t(7) * Cfg<D>::kTileBytes + sizeof(RowBars) + 64;
 }
+static_assert(kWarpgroups == 4, "sums of four warpgroups");
 static_assert(row_smem<128>() <= 232448 && row_smem<64>() <= 232448, "shared memory of a CTA");
 
 template <int D>
@@ -593,7 +591,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                    const __grid_constant__ CUtensorMap tmap_g,
                    const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, Dense P, int items,
-                   const float* __restrict__ nl, const float* __restrict__ dl,
+                   const float* __restrict__ nl, float* __restrict__ dl,
                    __nv_bfloat16* __restrict__ dq, int* __restrict__ next_item,
                    int* __restrict__ status) {
   using C = Cfg<D>;
@@ -620,15 +618,17 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       tc::mbar_init(&bars->v_empty[s], 1);
     }
     tc::mbar_init(&bars->first_full, 1);
+    tc::mbar_init(&bars->r_full[0], 8);   // warpgroups 2 and 3
+    tc::mbar_init(&bars->r_full[1], 4);   // warpgroup 1
     tc::mbar_init(&bars->s_full[0], 1);
     tc::mbar_init(&bars->s_full[1], 1);
     tc::mbar_init(&bars->dp_full, 1);
-    tc::mbar_init(&bars->ds_full, 9);   // 8 elementwise warps and warp 2
+    tc::mbar_init(&bars->ds_full, 4 * kWarpgroups + 1);   // elementwise warps and warp 2
     tc::mbar_init(&bars->acc_full, 1);
-    tc::mbar_init(&bars->acc_empty, 8);
+    tc::mbar_init(&bars->acc_empty, 4 * kWarpgroups);
     for (int i = 0; i < kItems; ++i) {
       tc::mbar_init(&bars->i_full[i], 1);
-      tc::mbar_init(&bars->i_empty[i], 10);
+      tc::mbar_init(&bars->i_empty[i], 4 * kWarpgroups + 2);
     }
     tc::mbar_init(&bars->mma_done, 1);
     bars->abort = 0;
@@ -748,10 +748,14 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int j = 0; j < it.n; ++j, ++n) {
           if (!tc::mbar_spin(&bars->ds_full, n & 1, abort)) { failed = true; break; }
           tc::tc_fence_after();
-          issue_ts<D>(tq, tp, kb + k0 * kTile16, j == it.n - 1 ? last : 8, j > 0);
+          // dP is read: the next one first, the elementwise warps want it soonest
+          if (j + 1 < it.n) products();
+          const uint32_t ds = tmem + uint32_t(j & 1) * 128, k = kb + k0 * kTile16;
+          const int groups = j == it.n - 1 ? last : 8;
+          issue_ts<D>(tq, ds, k, groups, j > 0);
+          issue_ts<D>(tq, ds + 16, k, groups, 1);
           tc::mma_commit(&bars->k_empty[k0]);
           k0 = k0 == 2 ? 0 : k0 + 1;
-          if (j + 1 < it.n) products();
           if (j + 2 < it.n) scores(j + 2);
         }
         if (failed) break;
@@ -804,11 +808,11 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
     }
   } else if (warp >= 4) {
-    // ---------------- elementwise, then half of the tile's dQ columns ----------------
-    const int half = (warp - 4) >> 2, quarter = warp & 3;
+    // ---------------- elementwise, then a share of the tile's dQ columns ----------------
+    const int wg = (warp - 4) >> 2, quarter = warp & 3;
     const int row = quarter * 32 + lane;
     const uint32_t lanes = uint32_t(quarter * 32) << 16;
-    const uint32_t pa = tp + lanes + half * 64;
+    const uint32_t pa = tp + lanes + wg * 32;
     const float sl2 = P.scale * kLog2e;
     const uint64_t sl2x2 = f2(sl2, sl2);
     long long n = 0;
@@ -822,81 +826,105 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       if (!it.live) break;
       const bool mine = row < it.rows;
       const long long at = (long long)it.head * P.rows_pad + it.pad0 + row;
-      const float nlse = mine ? nl[at] : -INFINITY, ndelta = mine ? -dl[at] : 0.f;
+      const float nlse = mine ? nl[at] : -INFINITY, ndelta = mine ? dl[at] : 0.f;
       const uint64_t nl2 = f2(nlse, nlse), nd2 = f2(ndelta, ndelta);
+      uint64_t rest = 0;  // sum of P (dP - delta) over this warpgroup's columns
       for (int j = 0; j < it.n; ++j, ++n) {
         const int b = j & 1;
-        const uint32_t sa = tmem + b * 128 + lanes + half * 64;
+        const uint32_t sa = tmem + b * 128 + lanes + wg * 32;
         if (!warp_wait(&bars->s_full[b], sn[b] & 1, abort)) { failed = true; break; }
         ++sn[b];
         tc::tc_fence_after();
-        uint32_t p[2][32];
-        tc::tmem_ld32(sa, p[0]);
-        tc::tmem_ld32(sa + 32, p[1]);
+        uint32_t p[32];
+        tc::tmem_ld32(sa, p);
         tc::tmem_ld_wait();
 #pragma unroll
-        for (int c = 0; c < 2; ++c)
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const uint64_t a = fma2(pair_of(&p[c][x]), sl2x2, nl2);
-            p[c][x] = __float_as_uint(ex2_f32(lo_of(a)));
-            p[c][x + 1] = __float_as_uint(ex2_f32(hi_of(a)));
-          }
+        for (int x = 0; x < 32; x += 2) {
+          const uint64_t a = fma2(pair_of(&p[x]), sl2x2, nl2);
+          p[x] = __float_as_uint(ex2_f32(lo_of(a)));
+          p[x + 1] = __float_as_uint(ex2_f32(hi_of(a)));
+        }
         if (!warp_wait(&bars->dp_full, uint32_t(n & 1), abort)) { failed = true; break; }
         tc::tc_fence_after();
-        const int lim = it.pos + row - j * 128 - half * 64;  // last visible column of this half
-        const bool cut = __any_sync(MSA_FULL_MASK, lim < 63);
-        uint32_t w[32];
+        uint32_t d[32];
+        tc::tmem_ld32(pa, d);
+        tc::tmem_ld_wait();
+        const int lim = it.pos + row - j * 128 - wg * 32;  // last visible column of these 32
+        const bool cut = __any_sync(MSA_FULL_MASK, lim < 31);
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          uint32_t d[32];
-          tc::tmem_ld32(pa + c * 32, d);
-          tc::tmem_ld_wait();
-#pragma unroll
-          for (int x = 0; x < 32; x += 2) {
-            const uint64_t y = mul2(pair_of(&p[c][x]), add2(pair_of(&d[x]), nd2));
-            d[x] = uint32_t(y);
-            d[x + 1] = uint32_t(y >> 32);
-          }
-          if (cut) {
-#pragma unroll
-            for (int x = 0; x < 32; ++x)
-              if (c * 32 + x > lim) d[x] = 0u;
-          }
-#pragma unroll
-          for (int x = 0; x < 32; x += 2)
-            w[c * 16 + x / 2] = pack_bf16(__uint_as_float(d[x]), __uint_as_float(d[x + 1]));
+        for (int x = 0; x < 32; x += 2) {
+          const uint64_t y = mul2(pair_of(&p[x]), add2(pair_of(&d[x]), nd2));
+          d[x] = uint32_t(y);
+          d[x + 1] = uint32_t(y >> 32);
         }
-        tc::tmem_st32(pa, w);
+        if (cut) {
+#pragma unroll
+          for (int x = 0; x < 32; ++x)
+            if (x > lim) d[x] = 0u;
+        }
+        // dS as the sum of two bf16 numbers, over the scores that made it
+        uint32_t hi[16], lo[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          const uint64_t y = pair_of(&d[2 * x]);
+          rest = add2(rest, y);
+          hi[x] = to_bf16x2(y);
+          lo[x] = to_bf16x2(add2(y, f2(-__uint_as_float(hi[x] << 16),
+                                       -__uint_as_float(hi[x] & 0xffff0000u))));
+        }
+        tmem_st8(sa, hi);
+        tmem_st8(sa + 8, hi + 8);
+        tmem_st8(sa + 16, lo);
+        tmem_st8(sa + 24, lo + 8);
         tc::tmem_st_wait();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->ds_full);
       }
-      if (failed || !warp_wait(&bars->acc_full, ii & 1, abort)) { failed = true; break; }
-      tc::tc_fence_after();
-      __nv_bfloat16* dst = dq + ((long long)(it.row0 + row) * P.Hq + it.head) * D + half * (D / 2);
-#pragma unroll 1
-      for (int c = 0; c < D / 64; ++c) {
-        uint32_t o[32];
+      if (failed) break;
+      // delta was formed from the rounded out: P sums to 1, so what is left of the sum
+      // of P (dP - delta) is what delta lacks; dk gets the better one
+      float r = lo_of(rest) + hi_of(rest);
+      if (wg >= 2) {
+        bars->rest[wg - 2][row] = r;
         __syncwarp();
-        tc::tmem_ld32(tq + lanes + half * (D / 2) + c * 32, o);
+        if (lane == 0) tc::mbar_arrive(&bars->r_full[0]);
+      }
+      if (!warp_wait(&bars->acc_full, ii & 1, abort)) { failed = true; break; }
+      tc::tc_fence_after();
+      __nv_bfloat16* dst = dq + ((long long)(it.row0 + row) * P.Hq + it.head) * D + wg * (D / 4);
+#pragma unroll 1
+      for (int c = 0; c < D / 4; c += 16) {
+        uint32_t o[16];
+        __syncwarp();
+        tc::tmem_ld16(tq + lanes + wg * (D / 4) + c, o);
         tc::tmem_ld_wait();
         if (mine) {
-          uint32_t w[16];
+          uint32_t w[8];
 #pragma unroll
-          for (int x = 0; x < 16; ++x)
+          for (int x = 0; x < 8; ++x)
             w[x] = pack_bf16(__uint_as_float(o[2 * x]) * P.scale,
                              __uint_as_float(o[2 * x + 1]) * P.scale);
-#pragma unroll
-          for (int x = 0; x < 16; x += 4)
-            *reinterpret_cast<uint4*>(dst + c * 32 + 2 * x) =
-                make_uint4(w[x], w[x + 1], w[x + 2], w[x + 3]);
+          *reinterpret_cast<uint4*>(dst + c) = make_uint4(w[0], w[1], w[2], w[3]);
+          *reinterpret_cast<uint4*>(dst + c + 8) = make_uint4(w[4], w[5], w[6], w[7]);
         }
       }
       tc::tc_fence_before();
       __syncwarp();
       if (lane == 0) tc::mbar_arrive(&bars->acc_empty);
+      // the four sums in a fixed order: 0 + 2, 1 + 3, both
+      if (wg < 2) {
+        if (!warp_wait(&bars->r_full[0], ii & 1, abort)) { failed = true; break; }
+        r += bars->rest[wg][row];
+        if (wg == 1) {
+          bars->rest[1][row] = r;
+          __syncwarp();
+          if (lane == 0) tc::mbar_arrive(&bars->r_full[1]);
+        } else {
+          if (!warp_wait(&bars->r_full[1], ii & 1, abort)) { failed = true; break; }
+          if (mine) dl[at] = ndelta - (r + bars->rest[1][row]);
+        }
+      }
     }
   }
   if (failed) {
@@ -938,6 +966,10 @@ cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* 
   dense_prep_kernel<D><<<unsigned((warps + 7) / 8), 256, 0, s>>>(
       P, static_cast<const bf16*>(dout), static_cast<const bf16*>(out), lse, W.nl, W.dl);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int qitems = P.qtiles * P.Hq;
+  dense_dq_tc_kernel<D><<<std::min(sm_count(), qitems), kThreads, row_smem<D>(), s>>>(
+      mq, mg, mk, mv, P, qitems, W.nl, W.dl, static_cast<bf16*>(dq), counters + 1, status);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int kitems = P.ktiles * P.Hkv * splits;
   dkv<<<std::min(sm_count(), kitems), kThreads, key_smem<D>(), s>>>(
       mq, mg, mk, mv, P, splits, kitems, W.nl, W.dl, static_cast<bf16*>(dk),
@@ -948,10 +980,7 @@ cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* 
                        static_cast<bf16*>(dv), s);
     if (e != cudaSuccess) return e;
   }
-  const int qitems = P.qtiles * P.Hq;
-  dense_dq_tc_kernel<D><<<std::min(sm_count(), qitems), kThreads, row_smem<D>(), s>>>(
-      mq, mg, mk, mv, P, qitems, W.nl, W.dl, static_cast<bf16*>(dq), counters + 1, status);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace
