@@ -151,7 +151,8 @@ struct KeyItem {
 
 struct KeyBars {
   uint64_t kv_full, kv_empty;
-  uint64_t q_full[2], q_empty[2], g_full[2], g_empty[2];  // Q (with lse, delta) and dO stages
+  uint64_t q_full[3], q_empty[3], g_full[2], g_empty[2];  // stages of Q and of dO
+  uint64_t nd_full[2];   // lse and delta; a slot is free with the Q stage of its step
   // first_full: the item's K, V and first Q, dO are there; p_full, ds_full: P and dS
   // written, and the next step's Q and dO are there
   uint64_t first_full, s_full, p_full, dp_full, ds_full, acc_full, acc_empty;
@@ -164,9 +165,11 @@ struct KeyBars {
   int abort;
 };
 
+// The dynamic part starts on a 1024-byte boundary, there is no room to align it by hand
+// (the kernel looks, and refuses to run otherwise).
 template <int D>
 constexpr size_t key_smem() {
-  return 1024 + size_t(6) * Cfg<D>::kTileBytes + sizeof(KeyBars) + 64;
+  return size_t(7) * Cfg<D>::kTileBytes + sizeof(KeyBars);
 }
 static_assert(key_smem<128>() <= 232448, "shared memory of a CTA");
 
@@ -206,13 +209,15 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     float* __restrict__ part, int* __restrict__ next_item,
                     int* __restrict__ status) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (tc::smem_addr(smem) & 1023) {
+    if (threadIdx.x == 0) atomicOr(status, tc::kStatusWaitTimeout);
+    return;
+  }
   uint8_t* kbuf = smem;
   uint8_t* vbuf = kbuf + C::kTileBytes;
-  uint8_t* qbuf = vbuf + C::kTileBytes;        // [2]
-  uint8_t* gbuf = qbuf + 2 * C::kTileBytes;    // [2]
+  uint8_t* qbuf = vbuf + C::kTileBytes;        // [3]
+  uint8_t* gbuf = qbuf + 3 * C::kTileBytes;    // [2]
   KeyBars* bars = reinterpret_cast<KeyBars*>(gbuf + 2 * C::kTileBytes);
   volatile int* abort = &bars->abort;
 
@@ -220,11 +225,14 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   if (threadIdx.x == 0) {
     tc::mbar_init(&bars->kv_full, 1);
     tc::mbar_init(&bars->kv_empty, 1);
-    for (int s = 0; s < 2; ++s) {
+    for (int s = 0; s < 3; ++s) {
       tc::mbar_init(&bars->q_full[s], 1);
       tc::mbar_init(&bars->q_empty[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
       tc::mbar_init(&bars->g_full[s], 1);
       tc::mbar_init(&bars->g_empty[s], 1);
+      tc::mbar_init(&bars->nd_full[s], 1);
     }
     tc::mbar_init(&bars->first_full, 1);
     tc::mbar_init(&bars->s_full, 1);
@@ -259,7 +267,9 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   if (warp == 0) {
     // ---------------- producer ----------------
     if (lane == 0) {
-      tc::ArmedRing kv_armed, q_armed, g_armed;
+      tc::ArmedRing kv_armed, q_armed, g_armed, nd_armed;
+      int qs = 0;
+      uint32_t qp = 0;
       int n = 0, used = 0;  // steps and items with steps so far
       int t = blockIdx.x;   // the first item is the CTA's own
       for (int ii = 0; !failed; ++ii) {
@@ -290,15 +300,13 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           for (int qt = it.qt0; qt < it.nqt; ++qt, ++n) {
             const int s = n & 1, par = (n >> 1) & 1, row = it.q0 + qt * 128;
             const long long at = (long long)hh * P.rows_pad + it.qp0 + qt * 128;
-            if (!tc::mbar_wait(&bars->q_empty[s], par ^ 1, abort)) { failed = true; break; }
-            tc::mbar_arrive_expect_tx(&bars->q_full[s], C::kTileBytes + 1024);
-            q_armed.note(s, par);
+            if (!tc::mbar_wait(&bars->q_empty[qs], qp ^ 1, abort)) { failed = true; break; }
+            tc::mbar_arrive_expect_tx(&bars->q_full[qs], C::kTileBytes);
+            q_armed.note(qs, qp);
 #pragma unroll
             for (int h = 0; h < D / 64; ++h)
-              tc::tma_load_3d(qbuf + s * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[s],
+              tc::tma_load_3d(qbuf + qs * C::kTileBytes + h * C::kHalf, &tmap_q, &bars->q_full[qs],
                               64 * h, hh, row);
-            tc::bulk_load(bars->nl[s], nl + at, 512, &bars->q_full[s]);
-            tc::bulk_load(bars->dl[s], dl + at, 512, &bars->q_full[s]);
             if (!tc::mbar_wait(&bars->g_empty[s], par ^ 1, abort)) { failed = true; break; }
             tc::mbar_arrive_expect_tx(&bars->g_full[s], C::kTileBytes);
             g_armed.note(s, par);
@@ -306,12 +314,23 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             for (int h = 0; h < D / 64; ++h)
               tc::tma_load_3d(gbuf + s * C::kTileBytes + h * C::kHalf, &tmap_g, &bars->g_full[s],
                               64 * h, hh, row);
+            // lse and delta: their slot was step n - 2's
+            if (n >= 2) {
+              const int x = qs == 2 ? 0 : qs + 1;  // (n - 2) % 3
+              const uint32_t xp = qs == 2 ? qp : qp ^ 1;
+              if (!tc::mbar_wait(&bars->q_empty[x], xp, abort)) { failed = true; break; }
+            }
+            tc::mbar_arrive_expect_tx(&bars->nd_full[s], 1024);
+            nd_armed.note(s, par);
+            tc::bulk_load(bars->nl[s], nl + at, 512, &bars->nd_full[s]);
+            tc::bulk_load(bars->dl[s], dl + at, 512, &bars->nd_full[s]);
+            if (++qs == 3) { qs = 0; qp ^= 1; }
           }
         }
         t = gridDim.x + atomicAdd(next_item, 1);  // late, so that no CTA holds two items
       }
       if (!(kv_armed.drain(&bars->kv_full) && q_armed.drain(bars->q_full) &&
-            g_armed.drain(bars->g_full)))
+            g_armed.drain(bars->g_full) && nd_armed.drain(bars->nd_full)))
         failed = true;
     }
   } else if (warp == 1) {
@@ -322,6 +341,7 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const uint32_t qb = mnmajor<D>(qbuf), gb = mnmajor<D>(gbuf);
       constexpr uint32_t kTile16 = C::kTileBytes / 16;
       uint32_t n = 0, used = 0;
+      int qs = 0;  // Q stage of this step
       for (int ii = 0; !failed; ++ii) {
         const int slot = ii % kItems;
         if (!tc::mbar_spin(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
@@ -333,14 +353,14 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         const int last = (min(128, it.nq - (it.nqt - 1) * 128) + 15) >> 4;
         if (!tc::mbar_spin(&bars->first_full, used & 1, abort)) { failed = true; break; }
         tc::tc_fence_after();
-        uint32_t off = (n & 1) * kTile16;  // of this step's stage
-        issue_nt<D>(ts, ka, qa + off);
+        uint32_t off = (n & 1) * kTile16;  // of this step's dO stage
+        issue_nt<D>(ts, ka, qa + qs * kTile16);
         tc::mma_commit(&bars->s_full);
         issue_nt<D>(tp, va, ga + off);
         tc::mma_commit(&bars->dp_full);
         int left = tiles;  // query tiles left of the head
         for (int i = 0; i < steps; ++i, ++n, off ^= kTile16) {
-          const int s = n & 1;
+          const int s = n & 1, next = qs == 2 ? 0 : qs + 1;
           const int groups = --left == 0 ? last : 8;
           if (left == 0) left = tiles;
           if (!tc::mbar_spin(&bars->p_full, n & 1, abort)) { failed = true; break; }
@@ -348,13 +368,14 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           issue_ts<D>(tv, ts, gb + off, groups, i > 0);
           tc::mma_commit(&bars->g_empty[s]);
           if (i + 1 < steps) {
-            issue_nt<D>(ts, ka, qa + (off ^ kTile16));
+            issue_nt<D>(ts, ka, qa + next * kTile16);
             tc::mma_commit(&bars->s_full);
           }
           if (!tc::mbar_spin(&bars->ds_full, n & 1, abort)) { failed = true; break; }
           tc::tc_fence_after();
-          issue_ts<D>(tk, tp, qb + off, groups, i > 0);
-          tc::mma_commit(&bars->q_empty[s]);
+          issue_ts<D>(tk, tp, qb + qs * kTile16, groups, i > 0);
+          tc::mma_commit(&bars->q_empty[qs]);
+          qs = next;
           if (i + 1 < steps) {
             issue_nt<D>(tp, va, ga + (off ^ kTile16));
             tc::mma_commit(&bars->dp_full);
@@ -369,7 +390,8 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
   } else if (warp == 2) {
     // ---------------- what else the products need ----------------
-    uint32_t n = 0, used = 0;
+    uint32_t n = 0, used = 0, qp = 0;
+    int qs = 0;
     for (int ii = 0; !failed; ++ii) {
       const int slot = ii % kItems;
       if (!warp_wait(&bars->i_full[slot], (ii / kItems) & 1, abort)) { failed = true; break; }
@@ -380,14 +402,21 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int tiles = it.nqt - it.qt0, steps = it.heads * tiles;
       if (steps <= 0) continue;
       const int rows = min(128, it.nq - (it.nqt - 1) * 128);  // of each head's last tile
-      // tile of step x has landed; rows behind the sequence are zero
-      auto landed = [&](uint64_t* full, uint8_t* buf, uint32_t x, bool tail) -> bool {
-        if (!warp_wait(&full[x & 1], (x >> 1) & 1, abort)) return false;
-        if (tail && (rows & 15)) zero_rows<D>(buf + (x & 1) * C::kTileBytes, rows, (rows + 15) & ~15);
+      // the next step's tile has landed; rows behind the sequence are zero
+      auto next_q = [&](bool tail) -> bool {
+        if (!warp_wait(&bars->q_full[qs], qp, abort)) return false;
+        if (tail && (rows & 15)) zero_rows<D>(qbuf + qs * C::kTileBytes, rows, (rows + 15) & ~15);
+        if (++qs == 3) { qs = 0; qp ^= 1; }
         return true;
       };
-      if (!warp_wait(&bars->kv_full, used & 1, abort) ||
-          !landed(bars->q_full, qbuf, n, tiles == 1) || !landed(bars->g_full, gbuf, n, tiles == 1)) {
+      auto next_g = [&](uint32_t x, bool tail) -> bool {
+        if (!warp_wait(&bars->g_full[x & 1], (x >> 1) & 1, abort)) return false;
+        if (tail && (rows & 15))
+          zero_rows<D>(gbuf + (x & 1) * C::kTileBytes, rows, (rows + 15) & ~15);
+        return true;
+      };
+      if (!warp_wait(&bars->kv_full, used & 1, abort) || !next_q(tiles == 1) ||
+          !next_g(n, tiles == 1)) {
         failed = true;
         break;
       }
@@ -399,13 +428,13 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // an arrival belongs to this step: the step before is over
         if ((n > 0 && !warp_wait(&bars->p_full, (n & 1) ^ 1, abort)) ||
             (i == 0 && !warp_wait(&bars->acc_empty, (used & 1) ^ 1, abort)) ||
-            (i + 1 < steps && !landed(bars->q_full, qbuf, n + 1, tail))) {
+            (i + 1 < steps && !next_q(tail))) {
           failed = true;
           break;
         }
         if (lane == 0) tc::mbar_arrive(&bars->p_full);
         if ((n > 0 && !warp_wait(&bars->ds_full, (n & 1) ^ 1, abort)) ||
-            (i + 1 < steps && !landed(bars->g_full, gbuf, n + 1, tail))) {
+            (i + 1 < steps && !next_g(n + 1, tail))) {
           failed = true;
           break;
         }
@@ -436,19 +465,23 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       for (int i = 0; i < steps; ++i, ++n) {
         const int s = n & 1;
         const uint32_t par = n & 1;
-        if (!warp_wait(&bars->q_full[s], (n >> 1) & 1, abort) ||
-            !warp_wait(&bars->s_full, par, abort)) {
-          failed = true;
-          break;
+        if (!warp_wait(&bars->nd_full[s], (n >> 1) & 1, abort)) { failed = true; break; }
+        // read before the wait for S: the MMAs' operands keep shared memory so busy that
+        // these reads, waited for one by one, took 650 cycles of a step (and delta's 400)
+        float4 col[8];
+        {
+          const float4* src = reinterpret_cast<const float4*>(bars->nl[s] + wg * 32);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) col[x] = src[x];
         }
+        if (!warp_wait(&bars->s_full, par, abort)) { failed = true; break; }
         tc::tc_fence_after();
         uint32_t p[32];
         tc::tmem_ld32(sa, p);
         tc::tmem_ld_wait();
-        const float4* nl4 = reinterpret_cast<const float4*>(bars->nl[s] + wg * 32);
 #pragma unroll
         for (int x = 0; x < 32; x += 4) {
-          const float4 f = nl4[x / 4];
+          const float4 f = col[x / 4];
           const uint64_t a = fma2(pair_of(&p[x]), sl2x2, f2(f.x, f.y));
           const uint64_t b = fma2(pair_of(&p[x + 2]), sl2x2, f2(f.z, f.w));
           p[x] = __float_as_uint(ex2_f32(lo_of(a)));
@@ -471,18 +504,30 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->p_full);
-        if (!warp_wait(&bars->dp_full, par, abort)) { failed = true; break; }
-        tc::tc_fence_after();
-        uint32_t d[32];
-        tc::tmem_ld32(pa, d);
-        tc::tmem_ld_wait();
-        const float4* dl4 = reinterpret_cast<const float4*>(bars->dl[s] + wg * 32);
+        {
+          const float4* src = reinterpret_cast<const float4*>(bars->dl[s] + wg * 32);
 #pragma unroll
-        for (int x = 0; x < 32; x += 4) {
-          const float4 f = dl4[x / 4];  // -delta
-          w[x / 2] = to_bf16x2(mul2(pair_of(&p[x]), add2(pair_of(&d[x]), f2(f.x, f.y))));
-          w[x / 2 + 1] =
-              to_bf16x2(mul2(pair_of(&p[x + 2]), add2(pair_of(&d[x + 2]), f2(f.z, f.w))));
+          for (int x = 0; x < 4; ++x) col[x] = src[x];
+          if (!warp_wait(&bars->dp_full, par, abort)) { failed = true; break; }
+          tc::tc_fence_after();
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t d[16];
+            tc::tmem_ld16(pa + h * 16, d);
+            tc::tmem_ld_wait();
+#pragma unroll
+            for (int x = 0; x < 16; x += 4) {
+              const float4 f = col[x / 4];  // -delta
+              const uint32_t* q2 = &p[h * 16 + x];
+              w[h * 8 + x / 2] = to_bf16x2(mul2(pair_of(q2), add2(pair_of(&d[x]), f2(f.x, f.y))));
+              w[h * 8 + x / 2 + 1] =
+                  to_bf16x2(mul2(pair_of(q2 + 2), add2(pair_of(&d[x + 2]), f2(f.z, f.w))));
+            }
+            if (h == 0) {
+#pragma unroll
+              for (int x = 0; x < 4; ++x) col[x] = src[4 + x];
+            }
+          }
         }
         tmem_st8(pa, w);
         tmem_st8(pa + 8, w + 8);
@@ -568,8 +613,8 @@ struct RowBars {
   uint64_t q_full, q_empty;
   uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2];
   // first_full: Q, dO and the first K and V tiles are there; ds_full: dS written, and the
-  // K and V tiles of the products after it are there
-  uint64_t first_full, s_full[2], dp_full, ds_full, acc_full, acc_empty, r_full[2];
+  // next V tile is there; kz_full: the K tile after the next is
+  uint64_t first_full, kz_full[2], s_full[2], dp_full, ds_full, acc_full, acc_empty, r_full[2];
   uint64_t i_full[kItems], i_empty[kItems];
   uint64_t mma_done;
   RowItem item[kItems];
@@ -618,6 +663,8 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       tc::mbar_init(&bars->v_empty[s], 1);
     }
     tc::mbar_init(&bars->first_full, 1);
+    tc::mbar_init(&bars->kz_full[0], 1);
+    tc::mbar_init(&bars->kz_full[1], 1);
     tc::mbar_init(&bars->r_full[0], 8);   // warpgroups 2 and 3
     tc::mbar_init(&bars->r_full[1], 4);   // warpgroup 1
     tc::mbar_init(&bars->s_full[0], 1);
@@ -720,7 +767,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const uint32_t qa = kmajor(qbuf), ga = kmajor(gbuf), ka = kmajor(kbuf), va = kmajor(vbuf);
       const uint32_t kb = mnmajor<D>(kbuf);
       constexpr uint32_t kTile16 = C::kTileBytes / 16;
-      uint32_t n = 0;
+      uint32_t n = 0, kz = 0;
       int k0 = 0, k2 = 0, vs = 0;  // K stages of dQ and of S, V stage of dP
       for (int ii = 0; !failed; ++ii) {
         const int slot = ii % kItems;
@@ -756,7 +803,12 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           issue_ts<D>(tq, ds + 16, k, groups, 1);
           tc::mma_commit(&bars->k_empty[k0]);
           k0 = k0 == 2 ? 0 : k0 + 1;
-          if (j + 2 < it.n) scores(j + 2);
+          if (j + 2 < it.n) {
+            if (!tc::mbar_spin(&bars->kz_full[kz & 1], (kz >> 1) & 1, abort)) { failed = true; break; }
+            ++kz;
+            tc::tc_fence_after();
+            scores(j + 2);
+          }
         }
         if (failed) break;
         tc::mma_commit(&bars->q_empty);
@@ -766,7 +818,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
     }
   } else if (warp == 2) {
     // ---------------- what else the products need ----------------
-    uint32_t n = 0;
+    uint32_t n = 0, kz = 0;
     int ks = 0, vs = 0;
     uint32_t kp = 0, vp = 0;
     for (int ii = 0; !failed; ++ii) {
@@ -800,11 +852,16 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         // the arrival belongs to this step: the step before is over
         if ((n > 0 && !warp_wait(&bars->ds_full, (n & 1) ^ 1, abort)) ||
             (j == 0 && !warp_wait(&bars->acc_empty, (ii & 1) ^ 1, abort)) ||
-            (j + 1 < it.n && !value_tile()) || (j + 2 < it.n && !key_tile(j + 2))) {
+            (j + 1 < it.n && !value_tile())) {
           failed = true;
           break;
         }
         if (lane == 0) tc::mbar_arrive(&bars->ds_full);
+        if (j + 2 < it.n) {
+          if (!key_tile(j + 2)) { failed = true; break; }
+          if (lane == 0) tc::mbar_arrive(&bars->kz_full[kz & 1]);
+          ++kz;
+        }
       }
     }
   } else if (warp >= 4) {
