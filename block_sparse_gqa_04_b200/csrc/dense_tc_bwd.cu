@@ -49,6 +49,23 @@ __device__ __forceinline__ uint64_t pair_of(const uint32_t* v) {
 __device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float(uint32_t(x)); }
 __device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float(uint32_t(x >> 32)); }
 
+// P of the pair of columns `pair`, POLY of every 8 pairs on the FMA pipe.  The dk, dv pass
+// waits for P on the exp2 unit's 1024 cycles a step: 3 of 8 take it from 0.88 to 0.83 ms
+// (2 x 4096 rows; 1 of 8 0.85, 4 of 8 0.84).  The dq pass does not gain (0.83 with none,
+// 0.84 with 3 of 8), nor does the forward pass (0.93 ms for 8192 rows with none, 0.95
+// with 1 of 8): there a warp alone on its scheduler pays for every instruction.
+template <int POLY>
+__device__ __forceinline__ void exp2_pair(uint32_t* p, uint64_t z, int pair) {
+  if ((pair * POLY) % 8 < POLY) {
+    const uint64_t y = exp2_poly(z);
+    p[0] = uint32_t(y);
+    p[1] = uint32_t(y >> 32);
+  } else {
+    p[0] = __float_as_uint(ex2_f32(lo_of(z)));
+    p[1] = __float_as_uint(ex2_f32(hi_of(z)));
+  }
+}
+
 // Low words of the tiles' descriptors, and the upper word that they share.
 constexpr uint32_t kHi = uint32_t(tc::kDescHi | (1024 >> 4));
 __device__ __forceinline__ uint32_t kmajor(const uint8_t* tile) {
@@ -484,10 +501,8 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           const float4 f = col[x / 4];
           const uint64_t a = fma2(pair_of(&p[x]), sl2x2, f2(f.x, f.y));
           const uint64_t b = fma2(pair_of(&p[x + 2]), sl2x2, f2(f.z, f.w));
-          p[x] = __float_as_uint(ex2_f32(lo_of(a)));
-          p[x + 1] = __float_as_uint(ex2_f32(hi_of(a)));
-          p[x + 2] = __float_as_uint(ex2_f32(lo_of(b)));
-          p[x + 3] = __float_as_uint(ex2_f32(hi_of(b)));
+          exp2_pair<3>(&p[x], a, x / 2);
+          exp2_pair<3>(&p[x + 2], b, x / 2 + 1);
         }
         if (__any_sync(MSA_FULL_MASK, from > 0)) {
 #pragma unroll
@@ -898,8 +913,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 #pragma unroll
         for (int x = 0; x < 32; x += 2) {
           const uint64_t a = fma2(pair_of(&p[x]), sl2x2, nl2);
-          p[x] = __float_as_uint(ex2_f32(lo_of(a)));
-          p[x + 1] = __float_as_uint(ex2_f32(hi_of(a)));
+          exp2_pair<0>(&p[x], a, x / 2);
         }
         if (!warp_wait(&bars->dp_full, uint32_t(n & 1), abort)) { failed = true; break; }
         tc::tc_fence_after();
