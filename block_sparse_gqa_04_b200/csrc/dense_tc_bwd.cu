@@ -478,6 +478,7 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const int tiles = it.nqt - it.qt0, steps = it.heads * tiles;
       // first column of this warpgroup's that sees the thread's key, at the first tile
       const int from0 = it.j0 + row - it.pos0 - it.qt0 * 128 - wg * 32;
+      const int rows = it.nq - (it.nqt - 1) * 128 - wg * 32;  // of the last tile, from here on
       int from = from0, left = tiles;
       for (int i = 0; i < steps; ++i, ++n) {
         const int s = n & 1;
@@ -504,10 +505,14 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           exp2_pair<3>(&p[x], a, x / 2);
           exp2_pair<3>(&p[x + 2], b, x / 2 + 1);
         }
-        if (__any_sync(MSA_FULL_MASK, from > 0)) {
+        // columns that do not see the key, and those behind the last row: P = 0, and dS
+        // too (the key and its value may hold anything)
+        const int to = left == 1 ? rows : 32;
+        const bool cut = to < 32 || __any_sync(MSA_FULL_MASK, from > 0);
+        if (cut) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            if (x < from) p[x] = 0u;
+            if (x < from || x >= to) p[x] = 0u;
         }
         uint32_t w[16];
 #pragma unroll
@@ -534,6 +539,11 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             for (int x = 0; x < 16; x += 4) {
               const float4 f = col[x / 4];  // -delta
               const uint32_t* q2 = &p[h * 16 + x];
+              if (cut) {
+#pragma unroll
+                for (int y = 0; y < 4; ++y)
+                  if (h * 16 + x + y < from || h * 16 + x + y >= to) d[x + y] = 0u;
+              }
               w[h * 8 + x / 2] = to_bf16x2(mul2(pair_of(q2), add2(pair_of(&d[x]), f2(f.x, f.y))));
               w[h * 8 + x / 2 + 1] =
                   to_bf16x2(mul2(pair_of(q2 + 2), add2(pair_of(&d[x + 2]), f2(f.z, f.w))));

@@ -216,3 +216,108 @@ def test_nothing_to_do():
     assert out.shape == q.shape and lse.shape == (2, 0, 4)
     dq, dk, dv = msa.dense_backward(q, q, k, k, out, lse)
     assert dq.numel() == 0 and not dk.any() and not dv.any()
+
+
+def test_rows_behind_32_bits_of_elements():
+    """2100 prompts of 128 rows x 64 heads x 128: q, out and dq hold more than 2^31
+    elements.  The last prompt's results equal those of a call on it alone, bit for bit
+    (whatever else runs, a prompt's sums have one order)."""
+    n, rows, hq, hkv, d = 2100, 128, 64, 4, 128
+    total = n * rows
+    cu = list(range(0, total + 1, rows))
+    q, dout = (torch.zeros((total, hq, d), dtype=BF16, device="cuda") for _ in range(2))
+    k, v = (torch.zeros((total, hkv, d), dtype=BF16, device="cuda") for _ in range(2))
+    assert q.numel() > 1 << 31
+    last = slice(total - rows, total)
+    for i, t in enumerate((q, dout, k, v)):
+        t[last] = randn((rows,) + t.shape[1:], BF16, 40 + i)
+    out, lse = msa.dense_attend_varlen(q, k, v, cu, cu, return_lse=True, check_device_status=True)
+    dq, dk, dv = msa.dense_backward_varlen(dout, q, k, v, out, lse, cu, cu)
+    one = [x[last].contiguous() for x in (q, k, v, dout)]
+    o1, l1 = msa.dense_attend_varlen(*one[:3], [0, rows], [0, rows], return_lse=True)
+    g1 = msa.dense_backward_varlen(one[3], *one[:3], o1, l1, [0, rows], [0, rows])
+    assert torch.equal(out[last], o1) and torch.equal(lse[last], l1)
+    assert torch.equal(dq[last], g1[0])
+    # dk and dv may be cut into other splits of the heads: the oracle's bounds
+    check_sequence(*one[:3], out[last], lse[last], 0, dout=one[3],
+                   grads=(dq[last], dk[last], dv[last]))
+    assert not out[:total - rows].any() and not dq[:total - rows].any()
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_two_streams_and_two_graphs_at_once(d):
+    """Calls that run at the same time, each with its workspace, and two graphs that share
+    one and are replayed in turn, give the bits of a call alone."""
+    lens = [257, 40, 600]
+    cu = np.cumsum([0] + lens).tolist()
+    q, k, v, dout = _inputs((cu[-1],), (cu[-1],), 8, 2, d, BF16, seed=31)
+
+    def step(ws=None):
+        o = msa.dense_attend_varlen(q, k, v, cu, cu, return_lse=True, workspace=ws)
+        return o + msa.dense_backward_varlen(dout, q, k, v, *o, cu, cu, workspace=ws)
+
+    want = step()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for _ in range(4):
+        for s in streams:
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(step())
+    torch.cuda.synchronize()
+    ws = torch.empty(1 << 25, dtype=torch.uint8, device="cuda")
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(step(ws))
+        graphs.append(g)
+    for g in graphs * 3:
+        g.replay()
+    torch.cuda.synchronize()
+    for o in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, o))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_gradients_where_hidden_rows_hold_anything(dtype):
+    """Keys that no row sees, and every key and value of them, may be NaN: dq does not
+    meet them, and their own gradients are zero."""
+    q, k, v, dout = _inputs((1, 70), (1, 300), 6, 2, 128, dtype, seed=23)
+    o = msa.dense_attend(q, k, v, q_pos0=55, return_lse=True)
+    want = msa.dense_backward(dout, q, k, v, *o, q_pos0=55)
+    k[:, 125:], v[:, 125:] = float("nan"), float("nan")
+    got = msa.dense_backward(dout, q, k, v, *o, q_pos0=55)
+    assert torch.equal(got[0], want[0])
+    for g, w in zip(got[1:], want[1:]):
+        assert torch.equal(g[:, :125], w[:, :125]) and not g[:, 125:].any()
+
+
+def test_attention_without_lse_and_into_a_given_output():
+    q, k, v, _ = _inputs((2, 200), (2, 200), 4, 4, 64, BF16, seed=29)
+    want, _ = msa.dense_attend(q, k, v, return_lse=True)
+    out = torch.full_like(q, 3.0)
+    assert msa.dense_attend(q, k, v, out=out) is out and torch.equal(out, want)
+
+
+def test_refusals_leave_everything_as_it_was():
+    q, k, v, dout = _inputs((1, 20), (1, 30), 4, 2, 64, BF16, seed=37)
+    out = torch.full_like(q, 5.0)
+    bad = [lambda: msa.dense_attend(q, k, v, q_pos0=11, out=out),        # behind the keys
+           lambda: msa.dense_attend(q, k, v, q_pos0=-1, out=out),
+           lambda: msa.dense_attend(q, k, v, softmax_scale=-1.0, out=out),
+           lambda: msa.dense_attend(q, k, v, workspace=torch.empty(64, dtype=torch.uint8,
+                                                                   device="cuda"), out=out),
+           lambda: msa.dense_attend(q[..., :32].contiguous(), k[..., :32].contiguous(),
+                                    v[..., :32].contiguous()),
+           lambda: msa.dense_attend_varlen(q[0], k[0], v[0], [0, 20], [0, 19], out=out[0]),
+           lambda: msa.dense_attend_varlen(q[0], k[0], v[0], [0, 30], [0, 30], out=out[0])]
+    for call in bad:
+        with pytest.raises((msa.MsaError, ValueError)):
+            call()
+    with pytest.raises(ValueError):
+        msa.dense_attend(q, k.cpu(), v)
+    with pytest.raises(ValueError):
+        msa.dense_attend(q.transpose(1, 2), k, v)
+    assert (out == 5).all()

@@ -173,3 +173,45 @@ def test_captured_and_replayed():
     want = msa.qk_norm_rope(q, k, w, w, f, pos)
     want += msa.qk_norm_rope_backward(*want, q, k, w, w, f, pos)
     assert all(torch.equal(a, b) for a, b in zip(out + grads, want))
+
+
+def test_rows_behind_32_bits_of_elements():
+    rows, hq, d = 300000, 64, 128
+    q = torch.zeros((rows, hq, d), dtype=BF16, device="cuda")
+    assert q.numel() > 1 << 31
+    q[-5:] = randn((5, hq, d), BF16, 1)
+    w, f = torch.ones(d, dtype=BF16, device="cuda"), _freqs(d)
+    pos = torch.arange(rows, device="cuda")
+    out, _ = msa.qk_norm_rope(q, None, w, None, f, pos)
+    want, _ = msa.qk_norm_rope(q[-5:], None, w, None, f, pos[-5:])
+    assert torch.equal(out[-5:], want) and not out[:-5].any()
+    del out
+    g = torch.zeros_like(q)
+    g[-5:] = randn((5, hq, d), BF16, 2)
+    dq, _, dw, _ = msa.qk_norm_rope_backward(g, None, q, None, w, None, f, pos)
+    want, _, dw1, _ = msa.qk_norm_rope_backward(g[-5:], None, q[-5:], None, w, None, f, pos[-5:])
+    assert torch.equal(dq[-5:], want) and not dq[:-5].any()
+    # the same 320 addends per weight, in another order
+    assert (dw - dw1).abs().max() <= 320 * 2.0 ** -23 * dw1.abs().max() + 1e-4
+
+
+def test_refusals():
+    q, k = randn((6, 4, 64), BF16, 1), randn((6, 2, 64), BF16, 2)
+    w, f = torch.ones(64, dtype=BF16, device="cuda"), _freqs(64)
+    pos = torch.arange(6, device="cuda")
+    buf = randn((6, 8, 64), BF16, 3)
+    bad = [lambda: msa.qk_norm_rope(q, k, w, None, f, pos),
+           lambda: msa.qk_norm_rope(q, k, w, w, f.float(), pos),
+           lambda: msa.qk_norm_rope(q, k, w, w, f, pos.int()),
+           lambda: msa.qk_norm_rope(q, k, w, w, f, pos[:5]),
+           lambda: msa.qk_norm_rope(q, k, w.float(), w, f, pos),
+           lambda: msa.qk_norm_rope(q, k[:5], w, w, f, pos),
+           lambda: msa.qk_norm_rope(q.transpose(0, 1), k, w, w, f, pos),
+           lambda: msa.qk_norm_rope(q, k, w, w, f[:12], pos),                  # rotary 24
+           lambda: msa.qk_norm_rope(q, k, w, w, f, pos, eps=-1.0),
+           lambda: msa.qk_norm_rope(q, k, w, w, f, pos, out=(buf[:, :4], buf[:, 3:5])),
+           lambda: msa.qk_norm_rope(buf[:, :4], k, w, w, f, pos, out=(buf[:, 1:5], k)),
+           lambda: msa.qk_norm_rope(q.cpu(), k, w, w, f, pos)]
+    for call in bad:
+        with pytest.raises((ValueError, msa.MsaError)):
+            call()

@@ -49,6 +49,8 @@ CASES = {
     "only_drafts": (2, 7, [0, 0], 8, 2, 64),
     "long": (1, 4, [6000], 8, 1, 128),
     "five_heads": (1, 30, [260], 5, 1, 64),
+    "whole_tile_of_heads": (2, 3, [300, 5], 128, 1, 64),
+    "64_heads": (1, 5, [1000], 64, 1, 128),
 }
 
 
@@ -196,3 +198,60 @@ def test_captured_and_replayed_with_growing_lengths():
             g.replay()
             want = msa.tree_attend(q, k, v, mask, lens, return_lse=True)
             assert all(torch.equal(a, b_) for a, b_ in zip(got, want))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_cache_rows_behind_32_bits_of_elements(dtype):
+    """The last sequence's rows lie more than 2^31 elements into the cache."""
+    b, cap, hq, hkv, d = 5, 1 << 20, 16, 4, 128
+    lens = [3, 0, 50, 1, 700]
+    k, v = (torch.empty((b, cap, hkv, d), dtype=dtype, device="cuda") for _ in range(2))
+    assert k[:4].numel() >= 1 << 31
+    for i, n in enumerate(lens):
+        k[i, :n + 2], v[i, :n + 2] = randn((n + 2, hkv, d), dtype, i), randn((n + 2, hkv, d), dtype, 9 + i)
+    q = randn((b, 2, hq, d), dtype, 77)
+    mask = np.tril(np.ones((2, 2), bool))
+    out, lse = msa.tree_attend(q, k, v, torch.from_numpy(mask).cuda(),
+                               torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                               return_lse=True, check_device_status=True)
+    _check(q, k, v, mask, lens, out, lse)
+
+
+def test_two_streams_at_once():
+    q = randn((3, 4, 16, 128), BF16, 1)
+    k, v = randn((3, 3000, 2, 128), BF16, 2), randn((3, 3000, 2, 128), BF16, 3)
+    mask = torch.ones((4, 4), dtype=torch.bool, device="cuda").tril()
+    lens = torch.tensor([2990, 100, 1500], dtype=torch.int32, device="cuda")
+    want = msa.tree_attend(q, k, v, mask, lens, return_lse=True)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(5):
+        for s in (torch.cuda.Stream(), torch.cuda.Stream()):
+            s.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(s):
+                got.append(msa.tree_attend(q, k, v, mask, lens, return_lse=True))
+    torch.cuda.synchronize()
+    for o in got:
+        assert all(torch.equal(a, b) for a, b in zip(want, o))
+
+
+def test_nothing_drafted_and_refusals():
+    k = randn((2, 50, 2, 64), BF16, 2)
+    lens = torch.tensor([1, 2], dtype=torch.int32, device="cuda")
+    q = torch.empty((2, 0, 4, 64), dtype=BF16, device="cuda")
+    none = torch.empty((0, 0), dtype=torch.bool, device="cuda")
+    assert msa.tree_attend(q, k, k, none, lens).shape == q.shape
+    q, one = randn((2, 1, 4, 64), BF16, 1), torch.ones((1, 1), dtype=torch.bool, device="cuda")
+    for bad in (lambda: msa.tree_attend(q, k, k, one, lens.long()),
+                lambda: msa.tree_attend(q, k, k, one.int(), lens),
+                lambda: msa.tree_attend(q, k, k, one[0], lens),
+                lambda: msa.tree_attend(q, k, k, one, lens.cpu()),
+                lambda: msa.tree_attend(q, k, k[:1], one, lens),
+                lambda: msa.tree_attend(q, k, k, one, lens, kv_len=50),
+                lambda: msa.tree_attend(q, k, k, one, lens, out=q.float()),
+                lambda: msa.tree_attend(q.repeat(1, 129, 1, 1), k.repeat(1, 4, 1, 1),
+                                        k.repeat(1, 4, 1, 1),
+                                        torch.ones((129, 129), dtype=torch.bool, device="cuda"),
+                                        lens)):
+        with pytest.raises((ValueError, msa.MsaError)):
+            bad()
