@@ -57,9 +57,12 @@ struct Tree {
   float2* part_ml;       // [2 * CTAs, rows] base-2 running maximum and sum
 };
 
-// Records of a packed batch into device memory, as kernel parameters: nothing is
-// read from host memory after the launch.
-cudaError_t launch_put_records(const SeqRec* host, SeqRec* dst, int n, cudaStream_t s);
+// Head of a workspace: the status word, then work counters of the tensor-core kernels.
+constexpr int kHeadWords = 4;
+// Zeroes the head and brings a packed batch's n records (or none) into device memory, as
+// kernel parameters: nothing is read from host memory after the launch.
+cudaError_t launch_dense_begin(int32_t* head, const SeqRec* host, SeqRec* dst, int n,
+                               cudaStream_t s);
 // Flags a block table's entries outside the pool (no launch without a table).
 cudaError_t launch_dense_check_table(const Dense& P, int32_t* status, cudaStream_t s);
 
@@ -75,11 +78,11 @@ struct DenseBwdSpace {
   float *nl, *dl, *part;
 };
 int dense_bwd_splits(const Dense& P);
-// counters: two zeroed words.
+// Zeroes the head words itself.
 cudaError_t launch_dense_bwd_tc(const Dense& P, const void* dout, const void* q, const void* k,
                                 const void* v, const void* out, const float* lse,
                                 const DenseBwdSpace& W, void* dq, void* dk, void* dv,
-                                int32_t* counters, int32_t* status, cudaStream_t s);
+                                int32_t* head, cudaStream_t s);
 // fp32 on the CUDA cores (nl unused).
 cudaError_t launch_dense_bwd_simt(const Dense& P, const void* dout, const void* q, const void* k,
                                   const void* v, const void* out, const float* lse,

@@ -7,7 +7,7 @@
 #include <new>
 
 #include "../../include/msa.h"
-#include "dense.h"
+#include "dense_common.cuh"
 #include "internal.h"
 
 using msa::Dense;
@@ -17,8 +17,7 @@ using msa::Tree;
 namespace {
 
 constexpr size_t kAlign = 256;
-// Status word, then the work counters of the tensor-core kernels; zeroed by each call.
-constexpr size_t kHeadBytes = 4 * sizeof(int32_t);
+constexpr size_t kHeadBytes = msa::kHeadWords * sizeof(int32_t);
 constexpr int kMaxSeqs = 1 << 20;
 constexpr int kMaxNodes = 128;
 
@@ -180,14 +179,13 @@ struct Records {
   ~Records() { delete[] r; }
 };
 
-// Clears the status word and the counters and puts the records in place.
+// Clears the head of the workspace and puts the records in place.
 msa_status_t begin(Dense* P, const Records& R, const DenseLayout& L, void* ws, cudaStream_t s) {
-  cudaError_t e = cudaMemsetAsync(ws, 0, kHeadBytes, s);
-  if (e == cudaSuccess && R.r) {
-    P->seqs = at<SeqRec>(ws, L.recs);
-    e = msa::launch_put_records(R.r, at<SeqRec>(ws, L.recs), P->B, s);
-  }
-  if (e == cudaSuccess) e = msa::launch_dense_check_table(*P, at<int32_t>(ws, L.status), s);
+  int32_t* head = at<int32_t>(ws, L.status);
+  if (R.r) P->seqs = at<SeqRec>(ws, L.recs);
+  cudaError_t e = msa::launch_dense_begin(head, R.r, R.r ? at<SeqRec>(ws, L.recs) : nullptr,
+                                          R.r ? P->B : 0, s);
+  if (e == cudaSuccess) e = msa::launch_dense_check_table(*P, head, s);
   return msa::status_of(e);
 }
 
@@ -295,14 +293,16 @@ msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlen
   const DenseLayout L = dense_layout(P, R.r != nullptr, true);
   if ((st = check_ws(ws, ws_bytes, L.total)) != MSA_OK) return st;
   cudaStream_t s = (cudaStream_t)stream;
-  if ((st = begin(&P, R, L, ws, s)) != MSA_OK) return st;
+  // without records the gradients' first kernel clears the head
+  const bool own_begin = !P.f32 && !R.r && P.rows_q > 0;
+  if (!own_begin && (st = begin(&P, R, L, ws, s)) != MSA_OK) return st;
   int32_t* head = at<int32_t>(ws, L.status);
   const msa::DenseBwdSpace W{at<float>(ws, L.nl), at<float>(ws, L.delta), at<float>(ws, L.part)};
   if (P.f32)
     return msa::status_of(
         msa::launch_dense_bwd_simt(P, dout, q, k, v, out, lse, W, dq, dk, dv, s));
   return msa::status_of(
-      msa::launch_dense_bwd_tc(P, dout, q, k, v, out, lse, W, dq, dk, dv, head + 1, head, s));
+      msa::launch_dense_bwd_tc(P, dout, q, k, v, out, lse, W, dq, dk, dv, head, s));
 }
 
 size_t msa_tree_workspace_size(const msa_problem_t* p) {
@@ -408,7 +408,10 @@ struct Chunk {
   SeqRec r[kChunkRecs];
 };
 
-__global__ void put_records_kernel(const __grid_constant__ Chunk c, SeqRec* dst, int n) {
+__global__ void dense_begin_kernel(const __grid_constant__ Chunk c, SeqRec* dst, int n,
+                                   int32_t* head) {
+  tc::griddep_launch();
+  if (head && threadIdx.x < kHeadWords) head[threadIdx.x] = 0;
   if (int(threadIdx.x) < n) dst[threadIdx.x] = c.r[threadIdx.x];
 }
 
@@ -420,13 +423,14 @@ __global__ void dense_check_table_kernel(const int32_t* table, long long n, int 
 
 }  // namespace
 
-cudaError_t launch_put_records(const SeqRec* host, SeqRec* dst, int n, cudaStream_t s) {
-  for (int i = 0; i < n; i += kChunkRecs) {
+cudaError_t launch_dense_begin(int32_t* head, const SeqRec* host, SeqRec* dst, int n,
+                               cudaStream_t s) {
+  for (int i = 0; i == 0 || i < n; i += kChunkRecs) {
     Chunk c;
     const int m = std::min(kChunkRecs, n - i);
     std::copy(host + i, host + i + m, c.r);
     std::fill(c.r + m, c.r + kChunkRecs, SeqRec{});
-    put_records_kernel<<<1, 128, 0, s>>>(c, dst + i, m);
+    dense_begin_kernel<<<1, 128, 0, s>>>(c, dst + i, m, i == 0 ? head : nullptr);
     const cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }

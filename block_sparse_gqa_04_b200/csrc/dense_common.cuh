@@ -4,6 +4,7 @@
 
 #include "common.cuh"
 #include "dense.h"
+#include "tc_common.cuh"
 
 namespace msa {
 
@@ -153,5 +154,23 @@ struct TreeWalk {
     return true;
   }
 };
+
+// Launches a kernel whose set-up may run while its predecessor in the stream finishes
+// (the kernel calls griddep_wait()).
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*kern)(P...), dim3 grid, int threads, size_t smem,
+                                cudaStream_t s, A&&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
 
 }  // namespace msa

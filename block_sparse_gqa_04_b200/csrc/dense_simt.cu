@@ -416,6 +416,7 @@ template <typename T>
 __global__ void __launch_bounds__(256)
 dense_dkv_sum_kernel(const float* __restrict__ part, int splits, long long n, float scale,
                      T* __restrict__ dk, T* __restrict__ dv) {
+  tc::griddep_wait();
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;
   if (i >= n) return;
   const int which = blockIdx.y;
@@ -568,6 +569,7 @@ tree_combine_kernel(Tree A, int ctas, int rows, T* __restrict__ out, float* __re
   const int n = tree_seq(A, b).tiles;
   const long long t0 = before * per + (long long)unit * n;
   const int c0 = int(t0 / share), c1 = int((t0 + n - 1) / share);
+  tc::griddep_wait();  // the partial states are written
   if (c0 == c1) return;
   const int g = unit / A.groups, row0 = (unit % A.groups) * A.rows, r = threadIdx.x % rows;
   if (r >= min(A.rows, nodes * P.G - row0) || c0d >= D) return;
@@ -685,13 +687,14 @@ cudaError_t launch_tree_combine(const Tree& A, void* out, float* lse, cudaStream
   const int ctas = tree_ctas(A.d.f32);
   if (A.d.f32) {
     auto kern = A.d.D == 128 ? tree_combine_kernel<float, 128> : tree_combine_kernel<float, 64>;
-    kern<<<unsigned(blocks), kJoinThreads, 0, s>>>(A, ctas, rows, static_cast<float*>(out), lse);
+    return launch_after(kern, unsigned(blocks), kJoinThreads, 0, s, A, ctas, rows,
+                        static_cast<float*>(out), lse);
   } else {
     auto kern = A.d.D == 128 ? tree_combine_kernel<__nv_bfloat16, 128>
                              : tree_combine_kernel<__nv_bfloat16, 64>;
-    kern<<<unsigned(blocks), kJoinThreads, 0, s>>>(A, ctas, rows, static_cast<__nv_bfloat16*>(out), lse);
+    return launch_after(kern, unsigned(blocks), kJoinThreads, 0, s, A, ctas, rows,
+                        static_cast<__nv_bfloat16*>(out), lse);
   }
-  return cudaGetLastError();
 }
 
 // bf16 problems run on the tensor cores: only fp32 comes here.
@@ -727,9 +730,8 @@ int dense_bwd_splits(const Dense& P) {
 template <typename T>
 cudaError_t launch_dkv_sum(const float* part, int splits, long long n, float scale, T* dk, T* dv,
                            cudaStream_t s) {
-  dense_dkv_sum_kernel<<<dim3(unsigned((n / 4 + 255) / 256), 2), 256, 0, s>>>(part, splits, n,
-                                                                              scale, dk, dv);
-  return cudaGetLastError();
+  return launch_after(dense_dkv_sum_kernel<T>, dim3(unsigned((n / 4 + 255) / 256), 2), 256, 0, s,
+                      part, splits, n, scale, dk, dv);
 }
 template cudaError_t launch_dkv_sum(const float*, int, long long, float, float*, float*,
                                     cudaStream_t);

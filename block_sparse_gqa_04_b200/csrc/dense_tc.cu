@@ -168,6 +168,7 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  tc::griddep_wait();  // the records and the counter are written
   bool failed = false;
 
   if (warp < 4) {
@@ -673,9 +674,9 @@ cudaError_t fwd_tc(const Dense& P, const void* q, const void* k, const void* v, 
     e = prepare_kernel(&done, dense_fwd_tc_kernel<D>, smem_bytes<D>(),
                        kRegsCtl + kRegsEpi + 2 * kRegsSoftmax, kThreads);
   if (e != cudaSuccess) return e;
-  dense_fwd_tc_kernel<D><<<std::min(sm_count(), P.pairs), kThreads, smem_bytes<D>(), s>>>(
-      mq, mk, mv, mo, P, static_cast<__nv_bfloat16*>(out), lse, counter, status);
-  return cudaGetLastError();
+  return launch_after(dense_fwd_tc_kernel<D>, std::min(sm_count(), P.pairs), kThreads,
+                      smem_bytes<D>(), s, mq, mk, mv, mo, P, static_cast<__nv_bfloat16*>(out), lse,
+                      counter, status);
 }
 
 }  // namespace

@@ -113,7 +113,10 @@ template <int D>
 __global__ void __launch_bounds__(256)
 dense_prep_kernel(Dense P, const __nv_bfloat16* __restrict__ dout,
                   const __nv_bfloat16* __restrict__ out, const float* __restrict__ lse,
-                  float* __restrict__ nl, float* __restrict__ dl) {
+                  float* __restrict__ nl, float* __restrict__ dl, int* __restrict__ head) {
+  tc::griddep_wait();  // the records are in place
+  tc::griddep_launch();
+  if (blockIdx.x == 0 && threadIdx.x < kHeadWords) head[threadIdx.x] = 0;
   constexpr int kLanes = D / 8, kRowsAtOnce = 32 / kLanes;
   const long long w = (long long)blockIdx.x * 8 + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -228,6 +231,7 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
   if (tc::smem_addr(smem) & 1023) {
+    tc::griddep_wait();
     if (threadIdx.x == 0) atomicOr(status, tc::kStatusWaitTimeout);
     return;
   }
@@ -277,6 +281,8 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  tc::griddep_wait();    // the dq pass has completed delta
+  tc::griddep_launch();
   // S^T | dP^T | dV | dK
   const uint32_t ts = tmem, tp = tmem + 128, tv = tmem + 256, tk = tmem + 256 + D;
   bool failed = false;
@@ -717,6 +723,8 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  tc::griddep_wait();    // lse and delta are in place
+  tc::griddep_launch();
   // S of even and of odd key tiles | dP | dQ
   const uint32_t tp = tmem + 256, tq = tmem + 384;
   bool failed = false;
@@ -1023,7 +1031,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
 template <int D>
 cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* k, const void* v,
                    const void* out, const float* lse, const DenseBwdSpace& W, void* dq, void* dk,
-                   void* dv, int32_t* counters, int32_t* status, cudaStream_t s) {
+                   void* dv, int32_t* head, cudaStream_t s) {
   using bf16 = __nv_bfloat16;
   cudaError_t e = cudaSuccess;
   const int splits = dense_bwd_splits(P);
@@ -1044,18 +1052,25 @@ cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* 
     e = prepare_kernel(&done[2], dense_dq_tc_kernel<D>, row_smem<D>(), 0, kThreads);
   if (e != cudaSuccess) return e;
   const long long warps = P.rows_pad / 16 * P.Hq;
-  dense_prep_kernel<D><<<unsigned((warps + 7) / 8), 256, 0, s>>>(
-      P, static_cast<const bf16*>(dout), static_cast<const bf16*>(out), lse, W.nl, W.dl);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (P.seqs) {
+    e = launch_after(dense_prep_kernel<D>, unsigned((warps + 7) / 8), 256, 0, s, P,
+                     static_cast<const bf16*>(dout), static_cast<const bf16*>(out), lse, W.nl, W.dl,
+                     head);
+  } else {  // nothing of this call ran before: an ordinary launch
+    dense_prep_kernel<D><<<unsigned((warps + 7) / 8), 256, 0, s>>>(
+        P, static_cast<const bf16*>(dout), static_cast<const bf16*>(out), lse, W.nl, W.dl, head);
+    e = cudaGetLastError();
+  }
+  if (e != cudaSuccess) return e;
   const int qitems = P.qtiles * P.Hq;
-  dense_dq_tc_kernel<D><<<std::min(sm_count(), qitems), kThreads, row_smem<D>(), s>>>(
-      mq, mg, mk, mv, P, qitems, W.nl, W.dl, static_cast<bf16*>(dq), counters + 1, status);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_after(dense_dq_tc_kernel<D>, std::min(sm_count(), qitems), kThreads, row_smem<D>(), s,
+                   mq, mg, mk, mv, P, qitems, W.nl, W.dl, static_cast<bf16*>(dq), head + 2, head);
+  if (e != cudaSuccess) return e;
   const int kitems = P.ktiles * P.Hkv * splits;
-  dkv<<<std::min(sm_count(), kitems), kThreads, key_smem<D>(), s>>>(
-      mq, mg, mk, mv, P, splits, kitems, W.nl, W.dl, static_cast<bf16*>(dk),
-      static_cast<bf16*>(dv), W.part, counters, status);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_after(dkv, std::min(sm_count(), kitems), kThreads, key_smem<D>(), s, mq, mg, mk, mv, P,
+                   splits, kitems, W.nl, W.dl, static_cast<bf16*>(dk), static_cast<bf16*>(dv),
+                   W.part, head + 1, head);
+  if (e != cudaSuccess) return e;
   if (splits > 1) {
     e = launch_dkv_sum(W.part, splits, kelems, P.scale, static_cast<bf16*>(dk),
                        static_cast<bf16*>(dv), s);
@@ -1069,9 +1084,9 @@ cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* 
 cudaError_t launch_dense_bwd_tc(const Dense& P, const void* dout, const void* q, const void* k,
                                 const void* v, const void* out, const float* lse,
                                 const DenseBwdSpace& W, void* dq, void* dk, void* dv,
-                                int32_t* counters, int32_t* status, cudaStream_t s) {
+                                int32_t* head, cudaStream_t s) {
   return (P.D == 128 ? bwd_tc<128> : bwd_tc<64>)(P, dout, q, k, v, out, lse, W, dq, dk, dv,
-                                                 counters, status, s);
+                                                 head, s);
 }
 
 }  // namespace msa

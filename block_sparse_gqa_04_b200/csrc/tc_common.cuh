@@ -219,6 +219,17 @@ __device__ __forceinline__ void tma_load_4d_hint(void* dst, const CUtensorMap* m
       : "memory");
 }
 
+// Programmatic dependent launch: a kernel launched with launch_after() starts while its
+// predecessor in the stream still runs; griddep_wait() returns once that has completed and
+// its writes are visible.  Every thread block passes it before it exits, so that a kernel
+// never completes before its predecessor.  griddep_launch() lets the successor start.
+__device__ __forceinline__ void griddep_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void griddep_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // One lane of a converged warp.  The compiler knows that exactly one thread runs what
 // this guards and keeps MMA and TMA operands in uniform registers there.
 __device__ __forceinline__ bool elect_one() {

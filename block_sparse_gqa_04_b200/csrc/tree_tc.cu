@@ -77,6 +77,7 @@ __global__ void __launch_bounds__(256)
 tree_prep_kernel(const uint8_t* __restrict__ mask, long long stride, int nodes,
                  uint4* __restrict__ bits, int32_t* __restrict__ status) {
   __shared__ uint32_t any[4];
+  tc::griddep_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
   if (threadIdx.x < 4) any[threadIdx.x] = 0;
@@ -127,6 +128,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   const int nodes = P.Sq;
 
   if (tc::smem_addr(smem) & 1023) {
+    tc::griddep_wait();
     if (threadIdx.x == 0) atomicOr(status, tc::kStatusWaitTimeout);
     return;
   }
@@ -164,6 +166,8 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
   __syncthreads();
   tc::tc_fence_after();
   const uint32_t tmem = bars->tmem_base;
+  tc::griddep_wait();    // the masks' bits are in place, the status word is clear
+  tc::griddep_launch();
   bool failed = false;
 
   if (warp < 4) {
@@ -644,10 +648,10 @@ cudaError_t tree_tc(const Tree& A_, const void* q, const void* k, const void* v,
   tree_prep_kernel<<<A.mask_stride ? A.d.B : 1, 256, 0, s>>>(A.mask, A.mask_stride, A.d.Sq, A.bits,
                                                              status);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  tree_tc_kernel<D><<<tree_ctas(A.d.f32), kThreads, smem_bytes<D>(), s>>>(
-      mq, mk, mv, A, static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(out), lse,
-      status);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_after(tree_tc_kernel<D>, tree_ctas(A.d.f32), kThreads, smem_bytes<D>(), s, mq, mk, mv,
+                   A, static_cast<const __nv_bfloat16*>(q), static_cast<__nv_bfloat16*>(out), lse,
+                   status);
+  if (e != cudaSuccess) return e;
   return launch_tree_combine(A, out, lse, s);
 }
 
