@@ -761,6 +761,23 @@ def _plan(op, B, Sq, Skv, Hq, Hkv, D, dtype, q_pos0, scale, pages):
     return p, n
 
 
+@functools.lru_cache(maxsize=64)
+def _packed_plan(op, cu_q, cu_k, Hq, Hkv, D, dtype, scale):
+    """(Problem, cu_q, cu_k as ctypes arrays, workspace bytes, rows of q, rows of k) of a
+    packed call; cu_q and cu_k are tuples."""
+    p, cq, ck = varlen_problem(list(cu_q), list(cu_k), Hq, Hkv, D, 32, dtype=dtype,
+                               softmax_scale=scale)
+    n = load().msa_dense_workspace_size(ctypes.byref(p), cq, ck, int(op == "backward"))
+    return p, cq, ck, n, cq[len(cq) - 1], ck[len(ck) - 1]
+
+
+def _numbers(cu, name):
+    """Prefix sums as a tuple of ints."""
+    if isinstance(cu, torch.Tensor) and cu.is_cuda:
+        raise ValueError(f"{name} is read on the host: pass a CPU tensor or a list")
+    return tuple(cu.tolist() if hasattr(cu, "tolist") else cu)
+
+
 def _with_table(p, block_table):
     if block_table is None:
         return p
@@ -793,12 +810,12 @@ def _dense_setup(op, q, k, v, cu_q, cu_k, q_pos0, softmax_scale, block_table=Non
     _want("v", v, kshape, dt)
     dev = _one_device(q, k, v, block_table)
     if packed:
-        p, cq, ck = varlen_problem(cu_q, cu_k, Hq, Hkv, D, 32, dtype=dt,
-                                   softmax_scale=softmax_scale)
-        if cq[len(cq) - 1] != qs[0] or ck[len(ck) - 1] != ks[0]:
-            raise ValueError(f"the prefix sums end at {cq[len(cq) - 1]} / {ck[len(ck) - 1]}, "
-                             f"the tensors hold {qs[0]} / {ks[0]} rows")
-        n = load().msa_dense_workspace_size(ctypes.byref(p), cq, ck, int(op == "backward"))
+        p, cq, ck, n, rows_q, rows_k = _packed_plan(
+            op, _numbers(cu_q, "cu_seqlens_q"), _numbers(cu_k, "cu_seqlens_k"), Hq, Hkv, D, dt,
+            float(softmax_scale))
+        if rows_q != qs[0] or rows_k != ks[0]:
+            raise ValueError(f"the prefix sums end at {rows_q} / {rows_k}, the tensors hold "
+                             f"{qs[0]} / {ks[0]} rows")
         return p, cq, ck, n, dev
     pages = _paged(block_table, kv_len, qs[0], ks[0], 128).get("num_pages", 0)
     p, n = _plan(op, qs[0], qs[1], int(kv_len) if pages else ks[1], Hq, Hkv, D, dt, int(q_pos0),
@@ -998,29 +1015,57 @@ def _check_overlap(name, dst, stride, *others):
             raise ValueError(f"{name} overlaps another tensor of the call")
 
 
+@functools.lru_cache(maxsize=512)
+def _norm_plan(qs, qst, ks, kst, dtype, half, eps, interleaved):
+    """NormRope of these shapes and strides with contiguous outputs, or what is wrong."""
+    esz = 4 if dtype == torch.float32 else 2
+    if len(qs) < 3 or (ks is not None and (len(ks) != len(qs) or ks[:-2] != qs[:-2]
+                                           or ks[-1] != qs[-1])):
+        return "q and k are [.., heads, D] with the same leading sizes and D"
+    (Hq, D), Hk = qs[-2:], 0 if ks is None else ks[-2]
+    steps = _rows_of(qs, qst, esz), 0 if ks is None else _rows_of(ks, kst, esz)
+    if None in steps:
+        return (f"q and k need contiguous heads and evenly spaced rows on 16-byte boundaries: "
+                f"shapes {tuple(qs)}, {ks and tuple(ks)}, strides {qst}, {kst}")
+    rows = 1
+    for n in qs[:-2]:
+        rows *= n
+    return NormRope(rows, Hq, Hk, D, 2 * half, interleaved,
+                    MSA_F32 if dtype == torch.float32 else MSA_BF16, eps, 0, *steps,
+                    Hq * D, Hk * D, Hq * D, Hk * D)
+
+
 def _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
-    """(NormRope with the strides of q and k, device index), all checked."""
+    """(NormRope with the strides of q and k, device index), all checked.  The NormRope is
+    shared between calls: callers change a copy."""
     _main_dtype(q)
     dt, qs = q.dtype, q.shape
-    lead, (Hq, D) = qs[:-2], qs[-2:]
-    if len(qs) < 3 or (k is not None and (k.dim() != len(qs) or k.shape[-1] != D)):
-        raise ValueError("q and k are [.., heads, D] with the same leading sizes and D")
     if (k is None) != (k_weight is None):
         raise ValueError("k and k_weight come together")
     dev = _one_device(q, k, q_weight, k_weight, inv_freq, positions)
-    _want("q_weight", q_weight, (D,), dt)
-    Hk = kstep = 0
+    if k is None:
+        p = _norm_plan(qs, q.stride(), None, None, dt, inv_freq.numel(), float(eps),
+                       bool(interleaved))
+    else:
+        if k.dtype != dt:
+            raise ValueError(f"q is {dt} and k {k.dtype}")
+        p = _norm_plan(qs, q.stride(), k.shape, k.stride(), dt, inv_freq.numel(), float(eps),
+                       bool(interleaved))
+    if isinstance(p, str):
+        raise ValueError(p)
+    D = qs[-1:]
+    _want("q_weight", q_weight, D, dt)
     if k is not None:
-        _want("k_weight", k_weight, (D,), dt)
-        Hk, kstep = k.shape[-2], _row_stride("k", k, lead, dt)
+        _want("k_weight", k_weight, D, dt)
     if inv_freq.dim() != 1:
         raise ValueError("inv_freq must be a vector")
     _want("inv_freq", inv_freq, inv_freq.shape, torch.float64)
-    _want("positions", positions, lead, torch.int64)
-    p = NormRope(positions.numel(), Hq, Hk, D, 2 * inv_freq.numel(), interleaved,
-                 MSA_F32 if dt == torch.float32 else MSA_BF16, eps, 0,
-                 _row_stride("q", q, lead, dt), kstep, Hq * D, Hk * D, Hq * D, Hk * D)
+    _want("positions", positions, qs[:-2], torch.int64)
     return p, dev
+
+
+def _contiguous_like(t):
+    return torch.empty_like(t, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps: float = 1e-6,
@@ -1035,9 +1080,10 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps: float = 
     or out=(q_out, k_out), which may be q and k themselves."""
     p, dev = _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
     if out is None:
-        qo = q.new_empty(q.shape)
-        ko = None if k is None else k.new_empty(k.shape)
+        qo = _contiguous_like(q)
+        ko = None if k is None else _contiguous_like(k)
     else:
+        p = NormRope.from_buffer_copy(p)
         qo, ko = out
         if qo.shape != q.shape or (ko is None) != (k is None) or (
                 k is not None and ko.shape != k.shape):
@@ -1069,12 +1115,15 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, po
             k is not None and dk_out.shape != k.shape):
         raise ValueError("dq_out and dk_out must be shaped like q and k")
     _one_device(q, dq_out, dk_out)
+    p = NormRope.from_buffer_copy(p)
     p.q_out_stride = _row_stride("dq_out", dq_out, lead, q.dtype)
-    dq, dqw = q.new_empty(q.shape), q.new_empty((D,), dtype=torch.float32)
-    dk = dkw = None
-    if k is not None:
+    dq, dk, dkw = _contiguous_like(q), None, None
+    if k is None:
+        dqw = q.new_empty((D,), dtype=torch.float32)
+    else:
         p.k_out_stride = _row_stride("dk_out", dk_out, lead, q.dtype)
-        dk, dkw = k.new_empty(k.shape), k.new_empty((D,), dtype=torch.float32)
+        dk = _contiguous_like(k)
+        dqw, dkw = q.new_empty((2, D), dtype=torch.float32).unbind()
     lib = load()
     wp, wn, workspace = _new_ws(lib.msa_norm_rope_workspace_size(ctypes.byref(p)), workspace, q,
                                 where)
