@@ -36,6 +36,7 @@ constexpr int kThreads = 512;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kItems = 3;     // items in flight
 constexpr float kSlack = 8.f;
+constexpr int kFirst = 6;   // groups of 16 keys of P that P V starts on (1-2 % over 4)
 // 96 + 64 + 2 x 176 = 512 = 4 x 128: the registers the CTA is launched with
 constexpr int kRegsCtl = 96, kRegsEpi = 64, kRegsSoftmax = 176;
 
@@ -323,13 +324,13 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
               if (!tc::mbar_spin(&bars->p_half[e], par, abort)) { failed = true; break; }
               tc::tc_fence_after();
 #pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
+              for (int kk = 0; kk < kFirst; ++kk)
                 tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
                               kk > 0 ? 1u : uint32_t(j));
               if (!tc::mbar_spin(&bars->p_full[e], par, abort)) { failed = true; break; }
               tc::tc_fence_after();
 #pragma unroll
-              for (int kk = 4; kk < 8; ++kk)
+              for (int kk = kFirst; kk < 8; ++kk)
                 tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO, 1u);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
@@ -354,14 +355,14 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
               const int nkt = e ? nkt1 : nkt0;
               const int left = !end ? nkt - j - 1 : cur.live ? (e ? cur.nkt[1] : cur.nkt[0]) : 0;
               if (j < nkt) {
-                // keys 0-63 run while the softmax finishes keys 64-127
+                // the first keys' products run while the softmax finishes the others
                 const int groups = (min(128, (e ? seen1 : seen0) - j * 128) + 15) >> 4;
                 const uint32_t v = vd + ps * 2 * kTile16;
                 if (!tc::mbar_spin(&bars->p_half[e], (ppar >> e) & 1, abort)) { failed = true; break; }
                 tc::tc_fence_after();
-                if (groups >= 4) {
+                if (groups >= kFirst) {
 #pragma unroll
-                  for (int kk = 0; kk < 4; ++kk)
+                  for (int kk = 0; kk < kFirst; ++kk)
                     tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO,
                                   kk > 0 ? 1u : uint32_t(j));
                 } else {
@@ -375,11 +376,11 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                 tc::tc_fence_after();
                 if (groups == 8) {
 #pragma unroll
-                  for (int kk = 4; kk < 8; ++kk)
+                  for (int kk = kFirst; kk < 8; ++kk)
                     tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO, 1u);
                 } else {
 #pragma unroll 1
-                  for (int kk = 4; kk < groups; ++kk)
+                  for (int kk = kFirst; kk < groups; ++kk)
                     tc::mma_ts_lo(st + 128, st + kk * 8, v + kk * 128, kHi, C::kIdescO, 1u);
                 }
                 if (j == nkt - 1) tc::mma_commit(&bars->o_done[e]);
@@ -541,11 +542,11 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
             }
             tmem_st8(st + q4 * 16 + x8 * 8, pw);
           }
-          if (q4 & 1) {
+          if (q4 == kFirst / 2 - 1 || q4 == 3) {
             tc::tmem_st_wait();
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(q4 == 1 ? &bars->p_half[e] : &bars->p_full[e]);
+            if (lane == 0) tc::mbar_arrive(q4 < 3 ? &bars->p_half[e] : &bars->p_full[e]);
           }
         }
         const uint64_t lsx = add2(lsum[0], lsum[1]);
