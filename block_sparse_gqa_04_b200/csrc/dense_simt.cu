@@ -32,26 +32,26 @@ struct Smem {
   static constexpr int kPFloats = kRows * kPPitch;
 };
 
-// Rows 0 .. N-1 of `src` (row r at src + r * stride elements) into an fp32 tile; rows
-// from `valid` on are zero.
-template <typename T, int D, int N>
-__device__ __forceinline__ void load_tile(float* dst, const T* src, long long stride, int valid) {
-  constexpr int vec = 16 / int(sizeof(T)), lanes = D / vec;
+// Rows 0 .. N-1 of `src` (row r at src + r * stride elements) on their way into a tile;
+// rows from `valid` on become zero.  One group of copies: tile_wait() waits for all but
+// the latest `left` groups of the thread.
+template <int D, int N>
+__device__ __forceinline__ void load_tile(float* dst, const float* src, long long stride,
+                                          int valid) {
 #pragma unroll 8
-  for (int i = threadIdx.x; i < N * lanes; i += kThreads) {
-    const int r = i / lanes, c = (i % lanes) * vec;
-    float x[vec];
-    if (r < valid) {
-      load_vec<T, vec>(src + r * stride + c, x);
-    } else {
-#pragma unroll
-      for (int e = 0; e < vec; ++e) x[e] = 0.f;
-    }
-#pragma unroll
-    for (int e = 0; e < vec; e += 4)
-      *reinterpret_cast<float4*>(dst + r * Smem<D>::kPitch + c + e) =
-          make_float4(x[e], x[e + 1], x[e + 2], x[e + 3]);
+  for (int i = threadIdx.x; i < N * (D / 4); i += kThreads) {
+    const int r = i / (D / 4), c = (i % (D / 4)) * 4, bytes = r < valid ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                     tc::smem_addr(dst + r * Smem<D>::kPitch + c)),
+                 "l"(src + (r < valid ? r * stride : 0) + c), "r"(bytes)
+                 : "memory");
   }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+template <int LEFT>
+__device__ __forceinline__ void tile_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+  __syncthreads();
 }
 
 // acc[i][j] += A[row ty + 8 i] . B[row tx + 16 j] over D columns.
@@ -189,19 +189,24 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
   const int rows = min(kRows, s.nq - i0), g = h / P.G;
   const int b = P.seqs ? 0 : s.q0 / P.Sq;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  load_tile<T, D, kRows>(Qs, q + ((long long)(s.q0 + i0) * P.Hq + h) * D, (long long)P.Hq * D,
-                         rows);
+  load_tile<D, kRows>(Qs, q + ((long long)(s.q0 + i0) * P.Hq + h) * D, (long long)P.Hq * D, rows);
   Running<D> R;
   R.clear();
   const float sl2 = P.scale * kLog2e;
   const int seen = min(s.nk, s.pos0 + i0 + rows);  // keys that the block's last row sees
-  for (int j0 = 0; j0 < seen; j0 += kTile) {
+  auto load = [&](float* dst, const T* src, int j0) {
+    if (j0 >= seen) {  // keeps the count of groups
+      asm volatile("cp.async.commit_group;" ::: "memory");
+      return;
+    }
     const long long row = tile_row(P, b, s.k0, j0 / kDenseTile) + (j0 % kDenseTile);
-    const int valid = min(kTile, s.nk - j0);
-    __syncthreads();  // the previous tile's P and V are read
-    load_tile<T, D, kTile>(Ks, k + (row * P.Hkv + g) * D, (long long)P.Hkv * D, valid);
-    load_tile<T, D, kTile>(Vs, v + (row * P.Hkv + g) * D, (long long)P.Hkv * D, valid);
-    __syncthreads();
+    load_tile<D, kTile>(dst, src + (row * P.Hkv + g) * D, (long long)P.Hkv * D,
+                        min(kTile, s.nk - j0));
+  };
+  load(Ks, k, 0);
+  load(Vs, v, 0);
+  for (int j0 = 0; j0 < seen; j0 += kTile) {
+    tile_wait<1>();  // K is there (and the previous P is read)
     float sc[4][4] = {};
     product_nt<D>(Qs, Ks, ty, tx, sc);
 #pragma unroll
@@ -212,8 +217,12 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
         sc[i][j] = sees ? sc[i][j] * sl2 : -INFINITY;
       }
     R.step(sc, Ps, ty, tx);
-    __syncthreads();
+    __syncthreads();  // K is read, P written
+    load(Ks, k, j0 + kTile);
+    tile_wait<1>();   // V is there
     product_nn<D>(Ps, Vs, ty, tx, R.o);
+    __syncthreads();  // V is read
+    load(Vs, v, j0 + kTile);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -282,43 +291,65 @@ dense_dkv_simt_kernel(Dense P, int splits, const T* __restrict__ dout, const T* 
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const long long kst = (long long)P.Hkv * D, qst = (long long)P.Hq * D;
   const long long kat = ((long long)(s.k0 + j0) * P.Hkv + g) * D;
-  load_tile<T, D, kRows>(Ks, k + kat, kst, keys);
-  load_tile<T, D, kRows>(Vs, v + kat, kst, keys);
+  load_tile<D, kRows>(Ks, k + kat, kst, keys);
+  load_tile<D, kRows>(Vs, v + kat, kst, keys);
   float ak[4][D / 16] = {}, av[4][D / 16] = {};
   // the first query row that sees key j0 sits at position j0
   const int i_first = max(0, j0 - s.pos0) / kTile * kTile;
   const int per = (P.G + splits - 1) / splits;
   const int h0 = g * P.G + split * per, h1 = min(h0 + per, (g + 1) * P.G);
-  for (int h = h0; h < h1; ++h) {
-    for (int i0 = i_first; i0 < s.nq; i0 += kTile) {
-      const int rows = min(kTile, s.nq - i0);
-      const long long at = (long long)(s.q0 + i0) * P.Hq + h;
-      __syncthreads();
-      load_tile<T, D, kTile>(Qs, q + at * D, qst, rows);
-      load_tile<T, D, kTile>(Gs, dout + at * D, qst, rows);
-      if (threadIdx.x < kTile) {
-        const bool ok = int(threadIdx.x) < rows;
-        lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] * kLog2e : 0.f;
-        delta_s[threadIdx.x] = ok ? delta[at + (long long)threadIdx.x * P.Hq] : 0.f;
-      }
-      __syncthreads();
-      float sc[4][4] = {}, dp[4][4] = {};
-      product_nt<D>(Ks, Qs, ty, tx, sc);
-      product_nt<D>(Vs, Gs, ty, tx, dp);
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int key = ty + 8 * i, c = tx + 16 * j;
-          const bool sees = c < rows && j0 + key <= s.pos0 + i0 + c;
-          const float p = sees ? exp2f(sc[i][j] * (P.scale * kLog2e) - lse_s[c]) : 0.f;
-          Ps[key * Smem<D>::kPPitch + c] = p;
-          Ss[key * Smem<D>::kPPitch + c] = sees ? p * (dp[i][j] - delta_s[c]) : 0.f;
-        }
-      __syncthreads();
-      product_nn<D>(Ps, Gs, ty, tx, av);
-      product_nn<D>(Ss, Qs, ty, tx, ak);
+  const int tiles = max(0, (s.nq - i_first + kTile - 1) / kTile), steps = max(0, h1 - h0) * tiles;
+  // step x: query tile x % tiles of head h0 + x / tiles
+  auto place = [&](int x) {
+    return (long long)(s.q0 + i_first + x % tiles * kTile) * P.Hq + h0 + x / tiles;
+  };
+  auto load = [&](float* dst, const T* src, int x) {
+    if (x < steps)
+      load_tile<D, kTile>(dst, src + place(x) * D, qst,
+                          min(kTile, s.nq - i_first - x % tiles * kTile));
+    else
+      asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float lse_r = 0.f, delta_r = 0.f;  // of the thread's query row in the coming step
+  auto stats = [&](int x) {
+    if (x >= steps || threadIdx.x >= kTile) return;
+    const bool ok = int(threadIdx.x) < s.nq - i_first - x % tiles * kTile;
+    const long long at = place(x) + (long long)threadIdx.x * P.Hq;
+    lse_r = ok ? lse[at] * kLog2e : 0.f;
+    delta_r = ok ? delta[at] : 0.f;
+  };
+  load(Gs, dout, 0);
+  load(Qs, q, 0);
+  stats(0);
+  for (int x = 0; x < steps; ++x) {
+    const int i0 = i_first + x % tiles * kTile, rows = min(kTile, s.nq - i0);
+    if (threadIdx.x < kTile) {
+      lse_s[threadIdx.x] = lse_r;
+      delta_s[threadIdx.x] = delta_r;
     }
+    tile_wait<1>();  // dO is there
+    stats(x + 1);
+    float sc[4][4] = {}, dp[4][4] = {};
+    product_nt<D>(Vs, Gs, ty, tx, dp);
+    tile_wait<0>();  // Q is there
+    product_nt<D>(Ks, Qs, ty, tx, sc);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int key = ty + 8 * i, c = tx + 16 * j;
+        const bool sees = c < rows && j0 + key <= s.pos0 + i0 + c;
+        const float p = sees ? exp2f(sc[i][j] * (P.scale * kLog2e) - lse_s[c]) : 0.f;
+        Ps[key * Smem<D>::kPPitch + c] = p;
+        Ss[key * Smem<D>::kPPitch + c] = sees ? p * (dp[i][j] - delta_s[c]) : 0.f;
+      }
+    __syncthreads();
+    product_nn<D>(Ps, Gs, ty, tx, av);
+    __syncthreads();  // dO is read
+    load(Gs, dout, x + 1);
+    product_nn<D>(Ss, Qs, ty, tx, ak);
+    __syncthreads();  // Q is read
+    load(Qs, q, x + 1);
   }
   const long long all = P.rows_k * P.Hkv * D;
   float* pv = part + (long long)split * 2 * all;
@@ -370,8 +401,8 @@ dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ 
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   const long long kst = (long long)P.Hkv * D, qst = (long long)P.Hq * D;
   const long long at = (long long)(s.q0 + i0) * P.Hq + h;
-  load_tile<T, D, kRows>(Qs, q + at * D, qst, rows);
-  load_tile<T, D, kRows>(Gs, dout + at * D, qst, rows);
+  load_tile<D, kRows>(Qs, q + at * D, qst, rows);
+  load_tile<D, kRows>(Gs, dout + at * D, qst, rows);
   if (threadIdx.x < kRows) {
     const bool ok = int(threadIdx.x) < rows;
     lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] * kLog2e : 0.f;
@@ -379,17 +410,23 @@ dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ 
   }
   float aq[4][D / 16] = {};
   const int seen = min(s.nk, s.pos0 + i0 + rows);
+  // rows behind what is seen are zero: they must not meet a weight of zero as NaN
+  auto load = [&](float* dst, const T* src, int j0) {
+    if (j0 < seen)
+      load_tile<D, kTile>(dst, src + ((long long)(s.k0 + j0) * P.Hkv + g) * D, kst,
+                          min(kTile, seen - j0));
+    else
+      asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  load(Vs, v, 0);
+  load(Ks, k, 0);
   for (int j0 = 0; j0 < seen; j0 += kTile) {
-    // rows behind what is seen are zero: they must not meet a weight of zero as NaN
-    const int keys = min(kTile, seen - j0);
-    const long long kat = ((long long)(s.k0 + j0) * P.Hkv + g) * D;
-    __syncthreads();
-    load_tile<T, D, kTile>(Ks, k + kat, kst, keys);
-    load_tile<T, D, kTile>(Vs, v + kat, kst, keys);
-    __syncthreads();
     float sc[4][4] = {}, dp[4][4] = {};
-    product_nt<D>(Qs, Ks, ty, tx, sc);
+    tile_wait<1>();  // V is there
     product_nt<D>(Gs, Vs, ty, tx, dp);
+    tile_wait<0>();  // K is there, V read
+    load(Vs, v, j0 + kTile);
+    product_nt<D>(Qs, Ks, ty, tx, sc);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -401,6 +438,8 @@ dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ 
       }
     __syncthreads();
     product_nn<D>(Ss, Ks, ty, tx, aq);
+    __syncthreads();  // K is read
+    load(Ks, k, j0 + kTile);
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -486,15 +525,15 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
       const int valid = min(kTile, total - j0);
       const bool drafts = j0 + kTile > p.len;  // the tile reaches the drafted tokens
       __syncthreads();
-      load_tile<T, D, kTile>(Ks, k + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
-      load_tile<T, D, kTile>(Vs, v + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
+      load_tile<D, kTile>(Ks, k + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
+      load_tile<D, kTile>(Vs, v + (row * P.Hkv + p.g) * D, (long long)P.Hkv * D, valid);
       if (drafts && threadIdx.x < kTile) {
         const int j = j0 + int(threadIdx.x) - p.len;
         bool any = j < 0;
         for (int i = 0; i < nodes && j >= 0 && j < nodes; ++i) any |= mask[i * nodes + j] != 0;
         seen_s[threadIdx.x] = any;
       }
-      __syncthreads();
+      tile_wait<0>();
       if (drafts) {  // a row that no node sees must not reach the products
         for (int i = threadIdx.x; i < kTile * D; i += kThreads)
           if (!seen_s[i / D]) Vs[i / D * Smem<D>::kPitch + i % D] = 0.f;
