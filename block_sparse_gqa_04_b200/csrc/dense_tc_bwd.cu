@@ -9,18 +9,33 @@
 //           MN-major operands of the last two, so nothing is stored twice.
 //   dq:     a CTA owns 128 query rows of a head and walks the keys they see, with the
 //           rows as lanes: S = Q K^T, dP = dO V^T, dS as above, dQ += dS K.
-// The two passes take 4 + 3 products of 128 x 128 x D per pair of tiles where a single
-// pass would take 5; in exchange no gradient leaves the chip before it is finished.
+// The two passes take 4 + 4 products of 128 x 128 x D per pair of tiles where a single
+// pass would take 5; in exchange no gradient leaves the chip before it is finished (the
+// single pass would add 64 KB of dQ per pair of tiles to memory, 4.4 GB for 2 x 4096 rows
+// x 64 heads, in an order that changes).
 //
-// One thread issues all MMAs in an order that keeps the pipe fed while the eight
-// elementwise warps (two warpgroups, half of the columns each) work on the other half
-// of a step: dK, dV pass ... dV(i) S(i+1) | dK(i) dP(i+1) | ..., dq pass ... dQ(i)
-// dP(i+1) S(i+2) ...: P(i+1) is computed during the products between the first pair of
-// bars, dS(i+1) during the next.
+// Roundings.  P and dS meet the MMAs as bf16.  For dq, where nothing but dS is rounded
+// before the result, dS is the sum of two bf16 numbers (the fourth product): its error
+// falls from 0.0025 to 0.0019, of which a bf16 result's own rounding is 0.0017.  delta =
+// sum_d dout out is formed from the rounded out; since P sums to 1, the dq pass knows
+// exactly what delta lacks, sum_j P (dP - delta), and leaves delta completed for dk.
+//
+// One thread issues all MMAs in an order that keeps the pipe fed while the sixteen
+// elementwise warps (four warpgroups, a quarter of the columns each) work on the other
+// half of a step: dK, dV pass ... dV(i) S(i+1) | dK(i) dP(i+1) | ..., dq pass ... dP(i+1)
+// dQ(i) S(i+2) ... with dS over the scores that made it, so that dP is free at once.  A
+// second warp gathers every other condition of the products into the barrier that the
+// elementwise warps complete, so that the issuing thread waits for one thing at a time.
+//
+// What bounds them (2 x 4096 rows x 64 heads x 128: dk, dv 0.85 ms, dq 0.83 ms; the tensor
+// pipe 69 and 67 % busy): a dk, dv step has 2048 cycles of MMA and takes ~2870, the chain
+// dV, S, P (its exponentials) and the barriers between them; a dq step has 2048 and takes
+// ~2900, of which the elementwise warps are busy 2500.
 //
 // Rows behind the end of a sequence come in with its last tiles.  Query rows there have
-// lse = inf, hence P = 0; the products that sum over rows stop at whole groups of 16,
-// and the rest of the last group is zeroed in shared memory before use.
+// lse = inf, hence P = 0 (and are masked: a key may hold anything); the products that sum
+// over rows stop at whole groups of 16, and the rest of the last group is zeroed in shared
+// memory before use.
 #include <algorithm>
 
 #include "dense_tc.cuh"
@@ -38,7 +53,6 @@ template <int D>
 struct Cfg {
   static constexpr int kTileBytes = 128 * D * 2;
   static constexpr int kHalf = 128 * 64 * 2;
-  static constexpr int kStages = 2;                     // dkv: of Q and of dO
   static constexpr uint32_t kIdescS = tc::idesc_bf16_f32(128, 128, 0, 0);
   static constexpr uint32_t kIdescG = tc::idesc_bf16_f32(128, D, 0, 1);
 };

@@ -17,6 +17,8 @@
 // once per block and token, in fp64 (positions x frequencies reach 10^6 turns, where fp32
 // keeps no fraction), reduced to a quarter turn before the fp32 sine and cosine.  Blocks
 // take query heads or key heads, so that a thread needs one set of weights and sums.
+// 32768 tokens x 68 heads x 128: 0.212 ms, 5.4 TB/s; gradients of 8191 tokens 82 us, 5.2
+// TB/s, and 6 us for the sum of the blocks' weight gradients.
 #include "common.cuh"
 #include "dense.h"
 
@@ -293,7 +295,9 @@ norm_rope_weights_kernel(const float* part, int blocks_q, int blocks_k, int D, f
 }
 
 // Few tokens: one at a time and a block per row group, so that every row is its own
-// thread group's; many: enough that a thread walks several heads of its token.
+// thread group's (32 tokens x 68 heads 2.9 us, against 3.8 with four tokens a block); many:
+// enough that a thread walks several heads of its token with the next row's load in flight
+// (32768 tokens 0.212 ms, against 0.288 with four tokens and loads in batches).
 Cut cut_of(long long rows, int heads, int D, int max_blocks) {
   const int groups = kThreads / (D / 16);
   Cut c{};
