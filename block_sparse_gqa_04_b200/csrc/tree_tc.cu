@@ -463,23 +463,27 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (!warp_wait(&bars->s_full[e], on & 1, abort)) { failed = true; break; }
         if (work) {
           tc::tc_fence_after();
-          uint32_t v[4][32];
-#pragma unroll
-          for (int q4 = 0; q4 < 4; ++q4) tc::tmem_ld32(st + q4 * 32, v[q4]);
-          tc::tmem_ld_wait();
+          // 32 columns at a time, each read twice: a loop over the whole row at once is
+          // 700 instructions that every launch fetches anew, 4000 cycles and more of a
+          // piece's first tiles
           const int off = it.len - (it.kt0 + j) * 128;
-          if (off < 128) {
-#pragma unroll
-            for (int q4 = 0; q4 < 4; ++q4) {
+          auto chunk = [&](int q4, uint32_t (&v)[32]) {
+            tc::tmem_ld32(st + q4 * 32, v);
+            tc::tmem_ld_wait();
+            if (off < 128) {
               const uint32_t w = bits_at(seen, q4 * 32 - off);
 #pragma unroll
               for (int x = 0; x < 32; ++x)
-                if (!((w >> x) & 1u)) v[q4][x] = __float_as_uint(-INFINITY);
+                if (!((w >> x) & 1u)) v[x] = __float_as_uint(-INFINITY);
             }
+          };
+          float top = -INFINITY;
+#pragma unroll 1
+          for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t v[32];
+            chunk(q4, v);
+            top = max32(v, top);
           }
-          float top = max32(v[0], -INFINITY);
-          top = fmaxf(fmaxf(top, max32(v[1], -INFINITY)), fmaxf(max32(v[2], -INFINITY),
-                                                               max32(v[3], -INFINITY)));
           const bool grow = j == e || (top - m) * sl2 > kSlack;
           float keep = 1.f;
           if (grow) {
@@ -490,22 +494,21 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
           }
           const uint64_t nmsx2 = f2(-ms, -ms);
           uint64_t lsum[2] = {0, 0};
-#pragma unroll
+          // P of columns 32 q4 .. goes over columns 16 q4 .., which have been read
+#pragma unroll 1
           for (int q4 = 0; q4 < 4; ++q4) {
+            uint32_t v[32], pw[16];
+            chunk(q4, v);
 #pragma unroll
-            for (int x8 = 0; x8 < 2; ++x8) {
-              uint32_t pw[8];
-#pragma unroll
-              for (int x = 0; x < 16; x += 2) {
-                const uint32_t* s2 = v[q4] + x8 * 16 + x;
-                const uint64_t z = fma2((uint64_t(s2[1]) << 32) | s2[0], sl2x2, nmsx2);
-                const float pa = ex2_f32(__uint_as_float(uint32_t(z)));
-                const float pb = ex2_f32(__uint_as_float(uint32_t(z >> 32)));
-                lsum[(x >> 1) & 1] = add2(lsum[(x >> 1) & 1], f2(pa, pb));
-                pw[x >> 1] = pack_bf16(pa, pb);
-              }
-              tmem_st8(st + q4 * 16 + x8 * 8, pw);
+            for (int x = 0; x < 32; x += 2) {
+              const uint64_t z = fma2((uint64_t(v[x + 1]) << 32) | v[x], sl2x2, nmsx2);
+              const float pa = ex2_f32(__uint_as_float(uint32_t(z)));
+              const float pb = ex2_f32(__uint_as_float(uint32_t(z >> 32)));
+              lsum[(x >> 1) & 1] = add2(lsum[(x >> 1) & 1], f2(pa, pb));
+              pw[x >> 1] = pack_bf16(pa, pb);
             }
+            tmem_st8(st + q4 * 16, pw);
+            tmem_st8(st + q4 * 16 + 8, pw + 8);
           }
           if (j > e && __any_sync(MSA_FULL_MASK, grow)) {
             // the previous P V was issued before this S: O is there
