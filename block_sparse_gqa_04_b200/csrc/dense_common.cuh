@@ -101,20 +101,27 @@ struct TreeWalk {
   int b;
   TreeSeq s;
 
-  // Called by whole warps.
-  __device__ __forceinline__ void begin(const Tree& T, int cta, const TreeSpan& sp) {
-    at = min(sp.share * cta, sp.total);
-    end = min(at + sp.share, sp.total);
+  // Called by whole warps.  Up to 32 sequences take one read of their lengths.
+  __device__ __forceinline__ void begin(const Tree& T, int cta, int ctas) {
     const int lane = threadIdx.x & 31, per = T.d.Hkv * T.groups;
-    first = 0;
+    const bool few = T.d.B <= 32;
+    long long total = few ? 0 : tree_span(T, ctas).total;
+    at = end = first = 0;
     b = 0;
     // the sequence that holds tile `at`: 32 sequences at a time
-    for (int base = 0; at < end; base += 32) {
+    for (int base = 0;; base += 32) {
       long long mine = base + lane < T.d.B ? (long long)tree_seq(T, base + lane).tiles * per : 0;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const long long up = __shfl_up_sync(MSA_FULL_MASK, mine, o);
         if (lane >= o) mine += up;
+      }
+      if (base == 0) {
+        if (few) total = __shfl_sync(MSA_FULL_MASK, mine, 31);
+        const long long share = tree_share(total, ctas);
+        at = min(share * cta, total);
+        end = min(at + share, total);
+        if (at >= end) break;
       }
       const unsigned past = __ballot_sync(MSA_FULL_MASK, first + mine > at);
       if (past) {
@@ -145,8 +152,10 @@ struct TreeWalk {
       first += (long long)s.tiles * per;
       s = tree_seq(T, ++b);
     }
-    const int unit = int((at - first) / s.tiles);
-    const int kt0 = int((at - first) % s.tiles);
+    const long long into = at - first;
+    const bool narrow = into < (1LL << 32);  // a 64-bit division takes hundreds of cycles
+    const int unit = narrow ? int(unsigned(into) / unsigned(s.tiles)) : int(into / s.tiles);
+    const int kt0 = int(into - (long long)unit * s.tiles);
     const int n = int(min((long long)(s.tiles - kt0), end - at));
     *p = Piece{b, unit / T.groups, unit % T.groups, kt0, kt0 + n, s.len,
                kt0 > 0 ? 0 : (n < s.tiles ? 1 : -1)};

@@ -499,9 +499,8 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
   if (blockIdx.x == 0)
     for (int b = threadIdx.x; b < P.B; b += kThreads)
       if (A.kv_lens[b] < 0 || A.kv_lens[b] > P.Skv - nodes) atomicOr(status, kStatusBadLength);
-  const TreeSpan span = tree_span(A, gridDim.x);
   TreeWalk w;
-  w.begin(A, blockIdx.x, span);
+  w.begin(A, blockIdx.x, gridDim.x);
   TreeWalk::Piece p;
   while (w.next(A, &p)) {
     const uint8_t* mask = A.mask + p.b * A.mask_stride;

@@ -184,7 +184,7 @@ tree_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int b = lane; b < P.B; b += 32)
           if (A.kv_lens[b] < 0 || A.kv_lens[b] > P.Skv - nodes) atomicOr(status, kStatusBadLength);
       TreeWalk w;
-      w.begin(A, blockIdx.x, tree_span(A, gridDim.x));
+      w.begin(A, blockIdx.x, gridDim.x);
       if (tc::elect_one()) {
         tc::ArmedRing kv_armed, q_armed;
         int stage = 0;
