@@ -27,7 +27,7 @@
 // second warp gathers every other condition of the products into the barrier that the
 // elementwise warps complete, so that the issuing thread waits for one thing at a time.
 //
-// What bounds them (2 x 4096 rows x 64 heads x 128: dk, dv 0.85 ms, dq 0.83 ms; the tensor
+// What bounds them (2 x 4096 rows x 64 heads x 128: dk, dv 0.87 ms, dq 0.86 ms; the tensor
 // pipe 69 and 67 % busy): a dk, dv step has 2048 cycles of MMA and takes ~2870, the chain
 // dV, S, P (its exponentials) and the barriers between them; a dq step has 2048 and takes
 // ~2900, of which the elementwise warps are busy 2500.
@@ -66,7 +66,7 @@ __device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float(uint
 // P of the pair of columns `pair`, POLY of every 8 pairs on the FMA pipe.  The dk, dv pass
 // waits for P on the exp2 unit's 1024 cycles a step: 3 of 8 take it from 0.88 to 0.83 ms
 // (2 x 4096 rows; 1 of 8 0.85, 4 of 8 0.84).  The dq pass does not gain (0.83 with none,
-// 0.84 with 3 of 8), nor does the forward pass (0.93 ms for 8192 rows with none, 0.95
+// 0.84 with 3 of 8; before it summed P), nor does the forward pass (0.93 ms for 8192 rows with none, 0.95
 // with 1 of 8): there a warp alone on its scheduler pays for every instruction.
 template <int POLY>
 __device__ __forceinline__ void exp2_pair(uint32_t* p, uint64_t z, int pair) {
@@ -663,14 +663,15 @@ struct RowBars {
   uint64_t i_full[kItems], i_empty[kItems];
   uint64_t mma_done;
   RowItem item[kItems];
-  float rest[2][128];
+  float2 rest[2][128];
   uint32_t tmem_base;
   int abort;
 };
 
+// Aligned by its declaration, as above.
 template <int D>
 constexpr size_t row_smem() {
-  return 1024 + size_t(7) * Cfg<D>::kTileBytes + sizeof(RowBars) + 64;
+  return size_t(7) * Cfg<D>::kTileBytes + sizeof(RowBars);
 }
 static_assert(kWarpgroups == 4, "sums of four warpgroups");
 static_assert(row_smem<128>() <= 232448 && row_smem<64>() <= 232448, "shared memory of a CTA");
@@ -685,9 +686,12 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                    __nv_bfloat16* __restrict__ dq, int* __restrict__ next_item,
                    int* __restrict__ status) {
   using C = Cfg<D>;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = reinterpret_cast<uint8_t*>(
-      (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if (tc::smem_addr(smem) & 1023) {
+    tc::griddep_wait();
+    if (threadIdx.x == 0) atomicOr(status, tc::kStatusWaitTimeout);
+    return;
+  }
   uint8_t* qbuf = smem;
   uint8_t* gbuf = qbuf + C::kTileBytes;
   uint8_t* kbuf = gbuf + C::kTileBytes;      // [3]
@@ -932,7 +936,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       const long long at = (long long)it.head * P.rows_pad + it.pad0 + row;
       const float nlse = mine ? nl[at] : -INFINITY, ndelta = mine ? dl[at] : 0.f;
       const uint64_t nl2 = f2(nlse, nlse), nd2 = f2(ndelta, ndelta);
-      uint64_t rest = 0;  // sum of P (dP - delta) over this warpgroup's columns
+      uint64_t rest = 0, mass = 0;  // sums of P (dP - delta) and of P over these columns
       for (int j = 0; j < it.n; ++j, ++n) {
         const int b = j & 1;
         const uint32_t sa = tmem + b * 128 + lanes + wg * 32;
@@ -963,7 +967,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         if (cut) {
 #pragma unroll
           for (int x = 0; x < 32; ++x)
-            if (x > lim) d[x] = 0u;
+            if (x > lim) d[x] = p[x] = 0u;
         }
         // dS as the sum of two bf16 numbers, over the scores that made it
         uint32_t hi[16], lo[16];
@@ -971,6 +975,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         for (int x = 0; x < 16; ++x) {
           const uint64_t y = pair_of(&d[2 * x]);
           rest = add2(rest, y);
+          mass = add2(mass, pair_of(&p[2 * x]));
           hi[x] = to_bf16x2(y);
           lo[x] = to_bf16x2(add2(y, f2(-__uint_as_float(hi[x] << 16),
                                        -__uint_as_float(hi[x] & 0xffff0000u))));
@@ -986,10 +991,11 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       if (failed) break;
       // delta was formed from the rounded out: P sums to 1, so what is left of the sum
-      // of P (dP - delta) is what delta lacks; dk gets the better one
-      float r = lo_of(rest) + hi_of(rest);
+      // of P (dP - delta) is what delta lacks; dk gets the better one.  (Not where P does
+      // not sum to 1: lse and out may be those of more keys than this call's.)
+      float r = lo_of(rest) + hi_of(rest), sum = lo_of(mass) + hi_of(mass);
       if (wg >= 2) {
-        bars->rest[wg - 2][row] = r;
+        bars->rest[wg - 2][row] = make_float2(r, sum);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->r_full[0]);
       }
@@ -1018,14 +1024,16 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // the four sums in a fixed order: 0 + 2, 1 + 3, both
       if (wg < 2) {
         if (!warp_wait(&bars->r_full[0], ii & 1, abort)) { failed = true; break; }
-        r += bars->rest[wg][row];
+        r += bars->rest[wg][row].x;
+        sum += bars->rest[wg][row].y;
         if (wg == 1) {
-          bars->rest[1][row] = r;
+          bars->rest[1][row] = make_float2(r, sum);
           __syncwarp();
           if (lane == 0) tc::mbar_arrive(&bars->r_full[1]);
         } else {
           if (!warp_wait(&bars->r_full[1], ii & 1, abort)) { failed = true; break; }
-          if (mine) dl[at] = ndelta - (r + bars->rest[1][row]);
+          const float2 other = bars->rest[1][row];
+          if (mine && fabsf(sum + other.y - 1.f) < 1e-3f) dl[at] = ndelta - (r + other.x);
         }
       }
     }

@@ -5,7 +5,8 @@ import pytest
 import torch
 
 from block_sparse_gqa_04_b200 import msa
-from tests.dense_util import check_sequence, randn
+from oracle import dense_oracle as D_
+from tests.dense_util import U, check_grads, check_sequence, randn, weight_error
 
 pytestmark = pytest.mark.gpu
 
@@ -321,3 +322,26 @@ def test_refusals_leave_everything_as_it_was():
     with pytest.raises(ValueError):
         msa.dense_attend(q.transpose(1, 2), k, v)
     assert (out == 5).all()
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_gradients_of_keys_in_two_parts(dtype):
+    """Out and lse of all keys, dk and dv part by part (the first keys, then the rest, as
+    ranks that hold a part of the keys each have them): a part's P does not sum to 1."""
+    n, m, hq, hkv, d = 96, 256, 4, 2, 128
+    q, k, v, dout = _inputs((1, n), (1, m + n), hq, hkv, d, dtype, seed=43)
+    out, lse = msa.dense_attend(q, k, v, q_pos0=m, return_lse=True)
+    dq, dk, dv = msa.dense_backward(dout, q, k, v, out, lse, q_pos0=m)
+    # behind the first part keys of zeros, whose gradients are not looked at
+    a = [x[:, :m].contiguous() for x in (k, v)]
+    b = [x[:, m:].contiguous() for x in (k, v)]
+    pad = [torch.cat((x, torch.zeros_like(x[:, :n])), 1) for x in a]
+    first = msa.dense_backward(dout, q, *pad, out, lse, q_pos0=m)
+    rest = msa.dense_backward(dout, q, *b, out, lse)
+    r = D_.dense_attend(q[0], k[0], v[0], m, dout=dout[0])
+    f, u = weight_error(q[0], k[0]), U[dtype]
+    parts = torch.cat((first[1][:, :m], rest[1]), 1), torch.cat((first[2][:, :m], rest[2]), 1)
+    # every key's gradient within the bounds of the whole call's (delta, of the rounded out,
+    # is not completed for a part: the dk_p term)
+    check_grads(dq[0], parts[0][0], parts[1][0], r, f, dtype)
+    check_grads(dq[0], dk[0], dv[0], r, f, dtype)
