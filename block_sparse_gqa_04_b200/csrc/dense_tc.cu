@@ -272,10 +272,10 @@ dense_fwd_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // ---------------- MMA issuer ----------------
       // In the fixed order P V of tile 0, its next S, P V of tile 1, its next S (the next
       // item's first S at an item's end): the two tiles stay half a step apart, each in
-      // its softmax while the other's products run.  The pipe queues one instruction
-      // only, so whatever this thread waits for or does between them shows: it waits for
-      // one barrier per pair of products, which warp 2 completes once all else that they
-      // need is there.
+      // its softmax while the other's products run.  The pipe queues few instructions, so
+      // whatever this thread waits for or does between them shows: it waits for P alone
+      // (its first keys, then the others), to whose first barrier warp 2 adds its arrival
+      // once all else that the products need is there.
       if (tc::elect_one()) {
         int ii = 0, ps = 0;                  // items, stage
         uint32_t pp = 0, qpar = 0, ppar = 0; // parities: stage; per query tile Q and P (bit e)
