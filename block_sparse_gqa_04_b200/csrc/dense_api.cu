@@ -69,7 +69,8 @@ msa_status_t check_sizes(const Dense& P, long long qtiles, long long ktiles, lon
 msa_status_t resolve_batched(const msa_problem_t* p, Dense* P) {
   msa_status_t st = resolve_heads(p, P);
   if (st != MSA_OK) return st;
-  if (p->q_len < 0 || p->kv_len < 1 || p->q_pos0 < 0 || p->q_pos0 + p->q_len > p->kv_len)
+  if (p->q_len < 0 || p->kv_len < 1 || p->q_pos0 < 0 ||
+      p->q_pos0 > (int64_t)p->kv_len - p->q_len)
     return MSA_ERR_INVALID_ARG;
   P->Sq = p->q_len;
   P->Skv = p->kv_len;

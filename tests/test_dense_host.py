@@ -80,6 +80,16 @@ def test_positions_behind_the_keys_are_refused(lib):
     assert _tree(lib, p) == WORKSPACE                                 # ignores q_pos0
 
 
+@pytest.mark.parametrize("q_pos0", [2**63 - 1, 2**63 - 64, 2**32, 2**31])
+def test_positions_behind_every_integer_are_refused(lib, q_pos0):
+    """q_pos0 + q_len is not formed: it may pass 64 bits."""
+    p = _problem()
+    p.q_pos0 = q_pos0
+    assert _attend(lib, p) == INVALID
+    assert _backward(lib, p) == INVALID
+    assert lib.msa_dense_workspace_size(ctypes.byref(p), None, None, 0) == 0
+
+
 @pytest.mark.parametrize("cq,ck,code", [
     ([0, 3, 9], None, INVALID), (None, [0, 3, 9], INVALID),
     ([1, 3, 9], [0, 3, 9], INVALID), ([0, 3, 9], [1, 3, 9], INVALID),
