@@ -20,6 +20,9 @@ constexpr size_t kAlign = 256;
 constexpr size_t kHeadBytes = msa::kHeadWords * sizeof(int32_t);
 constexpr int kMaxSeqs = 1 << 20;
 constexpr int kMaxNodes = 128;
+// Tokens of a sequence: the idle warps of the tensor-core kernels wait for a row of key
+// tiles, 65536 of them about 0.1 s, and a bounded wait gives up after a second or so.
+constexpr int kMaxTokens = 1 << 23;
 
 size_t align_up(size_t x) { return (x + kAlign - 1) / kAlign * kAlign; }
 
@@ -72,6 +75,7 @@ msa_status_t resolve_batched(const msa_problem_t* p, Dense* P) {
   if (p->q_len < 0 || p->kv_len < 1 || p->q_pos0 < 0 ||
       p->q_pos0 > (int64_t)p->kv_len - p->q_len)
     return MSA_ERR_INVALID_ARG;
+  if (p->kv_len > kMaxTokens) return MSA_ERR_UNSUPPORTED;
   P->Sq = p->q_len;
   P->Skv = p->kv_len;
   P->pos0 = int(p->q_pos0);
@@ -100,6 +104,7 @@ msa_status_t resolve_packed(const msa_problem_t* p, const int32_t* cu_q, const i
   for (int b = 0; b < p->batch; ++b) {
     const long long nq = (long long)cu_q[b + 1] - cu_q[b], nk = (long long)cu_k[b + 1] - cu_k[b];
     if (nq < 0 || nk < 0 || nq > nk) return MSA_ERR_INVALID_ARG;
+    if (nk > kMaxTokens) return MSA_ERR_UNSUPPORTED;
     pad += (nq + 15) / 16 * 16;
     qt += tiles(nq);
     kt += tiles(nk);

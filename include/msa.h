@@ -271,7 +271,7 @@ msa_status_t msa_index_kl(const msa_problem_t* p, const void* q, const void* k,
  * Used fields of p: batch, q_len, kv_len, num_q_heads, num_kv_heads, head_dim (64
  * or 128), dtype, q_pos0, softmax_scale, num_pages and block_table; the others are
  * ignored, except that qk_dtype must be 0.  num_q_heads is any multiple of
- * num_kv_heads.
+ * num_kv_heads.  A sequence holds at most 2^23 tokens (MSA_ERR_UNSUPPORTED).
  * cu_seqlens_q_opt, cu_seqlens_k_opt: both NULL for the batched layout above; both
  * given for a packed batch with the layout and rules of msa_forward_varlen (host
  * arrays, read before the call returns; q_len, kv_len and q_pos0 ignored; num_pages

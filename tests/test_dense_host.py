@@ -104,6 +104,20 @@ def test_prefix_sums(lib, cq, ck, code):
     assert (size > 0) == (code == WORKSPACE)
 
 
+def test_longest_sequence(lib):
+    """2^23 tokens of a sequence: key tiles times 128 stay below 2^31 and a warp that waits
+    for a whole row of key tiles stays within its bounded wait."""
+    n = 1 << 23
+    for kv_len, code in ((n, WORKSPACE), (n + 1, UNSUPPORTED), (2**31 - 1, UNSUPPORTED)):
+        p = _problem(num_pages=9, kv_len=kv_len, q_pos0=0)
+        p.block_table = FAKE
+        assert _attend(lib, p) == code
+        assert _tree(lib, p) == code
+        assert (lib.msa_tree_workspace_size(ctypes.byref(p)) > 0) == (code == WORKSPACE)
+        assert _backward(lib, _problem(batch=1, kv_len=kv_len, q_pos0=0)) == code
+        assert _attend(lib, _problem(), [0, 5, 7], [0, 10, min(kv_len + 10, 2**31 - 1)]) == code
+
+
 def test_pages(lib):
     p = _problem(num_pages=9)
     p.block_table = FAKE
