@@ -197,6 +197,7 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
   R.clear();
   const float sl2 = P.scale * kLog2e;
   const int seen = min(s.nk, s.pos0 + i0 + rows);  // keys that the block's last row sees
+  // rows behind what is seen are zero: a value there must not meet a weight of zero as NaN
   auto load = [&](float* dst, const T* src, int j0) {
     if (j0 >= seen) {  // keeps the count of groups
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -204,7 +205,7 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
     }
     const long long row = tile_row(P, b, s.k0, j0 / kDenseTile) + (j0 % kDenseTile);
     load_tile<D, kTile>(dst, src + (row * P.Hkv + g) * D, (long long)P.Hkv * D,
-                        min(kTile, s.nk - j0));
+                        min(kTile, seen - j0));
   };
   load(Ks, k, 0);
   load(Vs, v, 0);

@@ -276,8 +276,9 @@ msa_status_t msa_index_kl(const msa_problem_t* p, const void* q, const void* k,
  * given for a packed batch with the layout and rules of msa_forward_varlen (host
  * arrays, read before the call returns; q_len, kv_len and q_pos0 ignored; num_pages
  * 0; 0 <= n_q <= n_k per sequence).  No sequence reads another's rows: whatever
- * they hold, infinities and NaN included, does not reach it.  Inside a sequence
- * hidden tokens are weighted by zero, so their v must be finite.
+ * they hold, infinities and NaN included, does not reach it.  Nor do tokens that no
+ * row sees (a cache's unwritten rows); a token that some rows see is weighted by zero
+ * in the others, so its v must be finite.
  * lse_opt [batch, q_len, num_q_heads] (packed: [total_q, num_q_heads]) or NULL.
  * Workspace: msa_dense_workspace_size(.., 0) bytes.  bf16 problems run on the tensor
  * cores and round the unnormalised probabilities to bf16 for the product with v

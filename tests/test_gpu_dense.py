@@ -118,6 +118,17 @@ def test_infinite_keys_of_hidden_tokens(dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+@pytest.mark.parametrize("sq,pos0,skv", [(40, 100, 200), (1, 0, 512), (129, 3, 133), (70, 58, 128)])
+def test_tokens_that_no_row_sees_may_hold_anything(sq, pos0, skv, dtype):
+    """A cache's rows behind the last query row: not written yet."""
+    q, k, v, _ = _inputs((2, sq), (2, skv), 6, 2, 64, dtype, seed=11)
+    want = msa.dense_attend(q, k, v, q_pos0=pos0, return_lse=True)
+    k[:, pos0 + sq:], v[:, pos0 + sq:] = float("nan"), float("nan")
+    got = msa.dense_attend(q, k, v, q_pos0=pos0, return_lse=True)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
 @pytest.mark.parametrize("kv_len", [128, 200, 515])
 def test_paged(kv_len, dtype):
     b, sq, hq, hkv, d = 2, 70, 8, 2, 128
