@@ -185,6 +185,12 @@ struct Records {
   ~Records() { delete[] r; }
 };
 
+// A call without rows: it reports no error, whatever the workspace held.
+msa_status_t nothing_to_do(void* ws, size_t have, cudaStream_t s) {
+  if (check_ws(ws, have, sizeof(int32_t)) != MSA_OK) return MSA_OK;
+  return msa::status_of(cudaMemsetAsync(ws, 0, sizeof(int32_t), s));
+}
+
 // Clears the head of the workspace and puts the records in place.
 msa_status_t begin(Dense* P, const Records& R, const DenseLayout& L, void* ws, cudaStream_t s) {
   int32_t* head = at<int32_t>(ws, L.status);
@@ -270,7 +276,7 @@ msa_status_t msa_dense_attend(const msa_problem_t* p, const int32_t* cu_seqlens_
   if (!R.make(p, cu_seqlens_q_opt, cu_seqlens_k_opt)) return MSA_ERR_TOO_LARGE;
   msa_status_t st = resolve_dense(p, cu_seqlens_q_opt, cu_seqlens_k_opt, &P, R.r);
   if (st != MSA_OK) return st;
-  if (P.rows_q == 0) return MSA_OK;
+  if (P.rows_q == 0) return nothing_to_do(ws, ws_bytes, (cudaStream_t)stream);
   if (!pointers_ok(q, k, v, out) || (lse_opt && !aligned16(lse_opt))) return MSA_ERR_INVALID_ARG;
   const DenseLayout L = dense_layout(P, R.r != nullptr, false);
   if ((st = check_ws(ws, ws_bytes, L.total)) != MSA_OK) return st;
@@ -293,7 +299,7 @@ msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlen
   msa_status_t st = resolve_dense(p, cu_seqlens_q_opt, cu_seqlens_k_opt, &P, R.r);
   if (st != MSA_OK) return st;
   if (P.table) return MSA_ERR_UNSUPPORTED;
-  if (P.rows_k == 0) return MSA_OK;
+  if (P.rows_k == 0) return nothing_to_do(ws, ws_bytes, (cudaStream_t)stream);
   if (!pointers_ok(k, v, dk, dv)) return MSA_ERR_INVALID_ARG;
   if (P.rows_q > 0 && !pointers_ok(dout, q, out, lse, dq)) return MSA_ERR_INVALID_ARG;
   const DenseLayout L = dense_layout(P, R.r != nullptr, true);
@@ -324,7 +330,7 @@ msa_status_t msa_tree_attend(const msa_problem_t* p, const void* q, const void* 
   Tree T{};
   msa_status_t st = resolve_tree(p, &T);
   if (st != MSA_OK) return st;
-  if (T.d.rows_q == 0) return MSA_OK;
+  if (T.d.rows_q == 0) return nothing_to_do(ws, ws_bytes, (cudaStream_t)stream);
   if (!pointers_ok(q, k, v, out) || (lse_opt && !aligned16(lse_opt)) || !tree_mask || !kv_lens ||
       (reinterpret_cast<uintptr_t>(kv_lens) & 3u) != 0)
     return MSA_ERR_INVALID_ARG;

@@ -230,6 +230,27 @@ def test_nothing_to_do():
     assert dq.numel() == 0 and not dk.any() and not dv.any()
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=["bf16", "f32"])
+def test_nothing_to_do_reports_no_error(dtype):
+    """Whatever the workspace held before."""
+    ws = torch.full((1 << 25,), 255, dtype=torch.uint8, device="cuda")
+    how = dict(workspace=ws, check_device_status=True)
+    q = torch.empty((2, 0, 4, 64), dtype=dtype, device="cuda")
+    k = randn((2, 9, 2, 64), dtype, 0)
+    out, lse = msa.dense_attend(q, k, k, return_lse=True, **how)
+    ws.fill_(255)
+    msa.dense_backward(q, q, k, k, out, lse, **how)
+    ws.fill_(255)
+    out, lse = msa.dense_attend_varlen(q[0], k[0], k[0], [0, 0, 0], [0, 4, 9], return_lse=True, **how)
+    ws.fill_(255)
+    msa.dense_backward_varlen(q[0], q[0], k[0], k[0], out, lse, [0, 0, 0], [0, 4, 9], **how)
+    ws.fill_(255)
+    msa.dense_backward_varlen(q[0], q[0], k[0, :0], k[0, :0], out, lse, [0, 0], [0, 0], **how)
+    ws.fill_(255)
+    msa.tree_attend(q, k, k, torch.ones((0, 0), dtype=torch.bool, device="cuda"),
+                    torch.tensor([3, 9], dtype=torch.int32, device="cuda"), **how)
+
+
 def test_rows_behind_32_bits_of_elements():
     """2100 prompts of 128 rows x 64 heads x 128: q, out and dq hold more than 2^31
     elements.  The last prompt's results equal those of a call on it alone, bit for bit
