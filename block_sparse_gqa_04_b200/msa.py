@@ -710,6 +710,17 @@ def _want(name, t, shape, dtype):
                          f"{t.dtype} {tuple(t.shape)}")
 
 
+def _given_out(out, q, *others):
+    """out is like q and shares no memory with q or the others (all contiguous)."""
+    _want("out", out, q.shape, q.dtype)
+    _one_device(q, out)
+    a = out.data_ptr()
+    for t in (q,) + others:
+        b = t.data_ptr()
+        if a < b + t.nbytes and b < a + out.nbytes:
+            raise ValueError("out overlaps an input of the call")
+
+
 def _main_dtype(t):
     if t.dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"expected bf16 or fp32 tensors, got {t.dtype}")
@@ -830,8 +841,7 @@ def _dense_forward(where, q, k, v, cu_q, cu_k, q_pos0, softmax_scale, return_lse
     if out is None:
         out = torch.empty_like(q)
     else:
-        _want("out", out, q.shape, q.dtype)
-        _one_device(q, out)
+        _given_out(out, q, k, v)
     lse = q.new_empty(q.shape[:-1], dtype=torch.float32) if return_lse else None
     wp, wn, workspace = _new_ws(n, workspace, q, where)
     _run(where, dev, load().msa_dense_attend, ctypes.byref(p), cq, ck, q.data_ptr(), k.data_ptr(),
@@ -927,7 +937,7 @@ def tree_attend(q, k, v, tree_mask, kv_lens, *, softmax_scale: float = 0.0,
     _want("v", v, kshape, dt)
     _want("kv_lens", kv_lens, (B,), torch.int32)
     _want("tree_mask", tree_mask, (B, n, n) if each else (n, n), torch.bool)
-    dev = _one_device(q, k, v, kv_lens, tree_mask, block_table, out)
+    dev = _one_device(q, k, v, kv_lens, tree_mask, block_table)
     pages = _paged(block_table, kv_len, B, ks[0], 128).get("num_pages", 0)
     p, nbytes = _plan("tree", B, n, int(kv_len) if pages else ks[1], Hq, Hkv, D, dt, 0,
                       float(softmax_scale), pages)
@@ -935,7 +945,7 @@ def tree_attend(q, k, v, tree_mask, kv_lens, *, softmax_scale: float = 0.0,
     if out is None:
         out = torch.empty_like(q)
     else:
-        _want("out", out, qs, dt)
+        _given_out(out, q, k, v)
     lse = q.new_empty((B, n, Hq), dtype=torch.float32) if return_lse else None
     wp, wn, workspace = _new_ws(nbytes, workspace, q, where)
     _run(where, dev, load().msa_tree_attend, ctypes.byref(p), q.data_ptr(), k.data_ptr(),

@@ -280,9 +280,10 @@ msa_status_t msa_index_kl(const msa_problem_t* p, const void* q, const void* k,
  * row sees (a cache's unwritten rows); a token that some rows see is weighted by zero
  * in the others, so its v must be finite.
  * lse_opt [batch, q_len, num_q_heads] (packed: [total_q, num_q_heads]) or NULL.
- * Workspace: msa_dense_workspace_size(.., 0) bytes.  bf16 problems run on the tensor
- * cores and round the unnormalised probabilities to bf16 for the product with v
- * (sums in fp32); fp32 problems run in fp32 on the CUDA cores. */
+ * out overlaps no input (nor does any output of the operators below, except where the
+ * norm and rotation allow it).  Workspace: msa_dense_workspace_size(.., 0) bytes.  bf16
+ * problems run on the tensor cores and round the unnormalised probabilities to bf16 for
+ * the product with v (sums in fp32); fp32 problems run in fp32 on the CUDA cores. */
 msa_status_t msa_dense_attend(const msa_problem_t* p, const int32_t* cu_seqlens_q_opt,
                               const int32_t* cu_seqlens_k_opt, const void* q, const void* k,
                               const void* v, void* out, float* lse_opt, void* ws,
@@ -298,8 +299,9 @@ msa_status_t msa_dense_attend(const msa_problem_t* p, const int32_t* cu_seqlens_
  * bits.  bf16 problems round P and dS to bf16 for the products (dS as two bf16 numbers
  * for dq); delta is completed by what the rounding of out took from it (where P sums to
  * 1: out and lse may also be those of more keys than this call's, as where ranks hold a
- * part of the keys each).  Tokens that no row sees may hold anything.  dout, out, dq [.., num_q_heads, head_dim].  num_pages must be 0
- * (MSA_ERR_UNSUPPORTED).  Workspace: msa_dense_workspace_size(.., 1) bytes. */
+ * part of the keys each).  Tokens that no row sees may hold anything.
+ * dout, out, dq [.., num_q_heads, head_dim].  num_pages must be 0 (MSA_ERR_UNSUPPORTED).
+ * Workspace: msa_dense_workspace_size(.., 1) bytes. */
 msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlens_q_opt,
                                 const int32_t* cu_seqlens_k_opt, const void* dout, const void* q,
                                 const void* k, const void* v, const void* out, const float* lse,

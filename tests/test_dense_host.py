@@ -221,6 +221,19 @@ def test_python_checks_come_before_the_library():
             bad()
 
 
+def test_an_output_shares_no_memory_with_the_inputs(monkeypatch):
+    monkeypatch.setattr(msa, "_one_device", lambda *t: 0)                 # CPU tensors here
+    buf = torch.zeros(4, 6, 8, 64)
+    q, k, v = buf[0:1], torch.zeros(1, 6, 2, 64), torch.zeros(1, 6, 2, 64)
+    msa._given_out(buf[1:2], q, k, v)                                     # next to it
+    msa._given_out(torch.zeros_like(q), q, k, v)
+    late = buf.view(-1)[64:64 + q.numel()].view(q.shape)                  # a head later
+    cache = buf[2:].view(1, -1, 2, 64)
+    for out, k_ in ((q, k), (late, k), (buf[3:], cache)):
+        with pytest.raises(ValueError, match="overlaps"):
+            msa._given_out(out, q, k_, v)
+
+
 def test_overlap_and_stride_checks_of_norm_rope():
     buf = torch.zeros(6, 1536)
     q, k = buf[:, :1024].unflatten(1, (8, 128)), buf[:, 1024:1280].unflatten(1, (2, 128))
