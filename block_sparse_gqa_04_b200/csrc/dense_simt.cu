@@ -11,12 +11,14 @@
 // columns of O.  The products are register-tiled from shared memory: 64 FMAs per 8
 // 16-byte loads, which bound them (4 cycles of shared memory each against 64 cycles of the
 // FMA pipe for four warps).  A tile is copied while the other operand's product runs.  32
-// rows rather than 64 give small problems twice the blocks and half the longest one.
-// Training step of 1024 rows x 8 heads x 64: 0.31 ms; attention of 1500 rows x 32 heads x
-// 128: 0.56 ms, 33 TFLOP/s.
+// rows rather than 64 give small problems twice the blocks and half the longest one; 8 or 2
+// rows to a thread instead of 4 (64 or 256 threads) take 1.0 to 1.5 times as long, for want
+// of warps or for more loads.  Training step of 1024 rows x 8 heads x 64: 0.28 ms; attention
+// of 1500 rows x 32 heads x 128: 0.49 ms, 38 TFLOP/s.
 #include <algorithm>
 
 #include "dense_common.cuh"
+#include "tc_warp.cuh"
 
 namespace msa {
 namespace {
@@ -24,6 +26,8 @@ namespace {
 constexpr int kThreads = 128;
 constexpr int kRows = 32;    // rows of a block
 constexpr int kTile = 64;    // columns at a time
+constexpr int kTy = kThreads / 16;   // threads along the rows
+constexpr int kR = kRows / kTy;      // rows of a thread, kTy apart
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
@@ -57,54 +61,65 @@ __device__ __forceinline__ void tile_wait() {
   __syncthreads();
 }
 
-// acc[i][j] += A[row ty + 8 i] . B[row tx + 16 j] over D columns.
+// acc[i][j] = A[row ty + kTy i] . B[row tx + 16 j] over D columns.  Two FMAs to an
+// instruction, here and below (neighbouring columns lie side by side in both operands), and
+// 16 passes unrolled: against scalar FMAs, 4 and 2 passes unrolled, the attention of 4000
+// rows x 8 heads x 64 went from 518 to 458 us and its gradients from 1.69 to 1.66 ms, that of
+// 1500 rows x 32 heads x 128 from 560 to 491 us and from 2.31 to 1.96 ms (32 passes: 2.15).
 template <int D>
 __device__ __forceinline__ void product_nt(const float* A, const float* B, int ty, int tx,
-                                           float (&acc)[4][4]) {
+                                           float (&acc)[kR][4]) {
   constexpr int P = Smem<D>::kPitch;
-#pragma unroll 4
+  uint64_t sum[kR][4] = {};  // of even and of odd columns
+#pragma unroll 16
   for (int d = 0; d < D; d += 4) {
-    float4 a[4], b[4];
+    ulonglong2 a[kR], b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      a[i] = *reinterpret_cast<const float4*>(A + (ty + 8 * i) * P + d);
-      b[i] = *reinterpret_cast<const float4*>(B + (tx + 16 * i) * P + d);
-    }
+    for (int i = 0; i < kR; ++i)
+      a[i] = *reinterpret_cast<const ulonglong2*>(A + (ty + kTy * i) * P + d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const ulonglong2*>(B + (tx + 16 * j) * P + d);
+#pragma unroll
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
-        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
-        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
-        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+        sum[i][j] = fma2(a[i].x, b[j].x, sum[i][j]);
+        sum[i][j] = fma2(a[i].y, b[j].y, sum[i][j]);
       }
   }
+#pragma unroll
+  for (int i = 0; i < kR; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      acc[i][j] = __uint_as_float(uint32_t(sum[i][j])) + __uint_as_float(uint32_t(sum[i][j] >> 32));
 }
 
-// acc[i][c] += sum_k W[row ty + 8 i][k] * B[k][col], W [32][kPPitch], columns
-// tx * 4 + 64 * (c / 4) + c % 4 (D = 64: 4 columns, 128: 8).
+// acc[i][c] += sum_k W[row ty + kTy i][k] * B[k][col], W [32][kPPitch], columns
+// tx * 4 + 64 * (c / 4) + c % 4 (D = 64: 4 columns, 128: 8), two to an accumulator.
 template <int D>
 __device__ __forceinline__ void product_nn(const float* W, const float* B, int ty, int tx,
-                                           float (&acc)[4][D / 16]) {
+                                           uint64_t (&acc)[kR][D / 32]) {
   constexpr int P = Smem<D>::kPitch, PP = Smem<D>::kPPitch;
-#pragma unroll 2
-  for (int k = 0; k < kTile; k += 4) {
-    float4 w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty + 8 * i) * PP + k);
+  for (int k = 0; k < kTile; k += 4) {
+    float4 w[kR];
+#pragma unroll
+    for (int i = 0; i < kR; ++i) w[i] = *reinterpret_cast<const float4*>(W + (ty + kTy * i) * PP + k);
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
+      uint64_t x[kR];
 #pragma unroll
-      for (int c = 0; c < D / 16; c += 4) {
-        const float4 b = *reinterpret_cast<const float4*>(B + (k + kk) * P + tx * 4 + c * 16);
+      for (int i = 0; i < kR; ++i) {
+        const float y = reinterpret_cast<const float*>(&w[i])[kk];
+        x[i] = f2(y, y);
+      }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = reinterpret_cast<const float*>(&w[i])[kk];
-          acc[i][c] = fmaf(x, b.x, acc[i][c]);
-          acc[i][c + 1] = fmaf(x, b.y, acc[i][c + 1]);
-          acc[i][c + 2] = fmaf(x, b.z, acc[i][c + 2]);
-          acc[i][c + 3] = fmaf(x, b.w, acc[i][c + 3]);
+      for (int c = 0; c < D / 32; c += 2) {
+        const ulonglong2 b = *reinterpret_cast<const ulonglong2*>(B + (k + kk) * P + tx * 4 + c * 32);
+#pragma unroll
+        for (int i = 0; i < kR; ++i) {
+          acc[i][c] = fma2(x[i], b.x, acc[i][c]);
+          acc[i][c + 1] = fma2(x[i], b.y, acc[i][c + 1]);
         }
       }
     }
@@ -125,20 +140,21 @@ __device__ __forceinline__ float sum16(float v) {
 // Running softmax of a thread's 4 rows (each shared by the 16 threads of a row).
 template <int D>
 struct Running {
-  float m[4], l[4], o[4][D / 16];
+  float m[kR], l[kR];
+  uint64_t o[kR][D / 32];
   __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[i][c] = 0.f;
+      for (int c = 0; c < D / 32; ++c) o[i][c] = 0;
     }
   }
   // Scores (already scaled to base 2, -inf where hidden) of one key tile: P into Ps.
-  __device__ __forceinline__ void step(float (&s)[4][4], float* Ps, int ty, int tx) {
+  __device__ __forceinline__ void step(float (&s)[kR][4], float* Ps, int ty, int tx) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < kR; ++i) {
       float mx = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
       mx = fmaxf(m[i], max16(mx));
       const float base = mx == -INFINITY ? 0.f : mx;  // a row that has seen nothing yet
@@ -149,19 +165,23 @@ struct Running {
       for (int j = 0; j < 4; ++j) {
         const float p = exp2f(s[i][j] - base);
         sum += p;
-        Ps[(ty + 8 * i) * Smem<D>::kPPitch + tx + 16 * j] = p;
+        Ps[(ty + kTy * i) * Smem<D>::kPPitch + tx + 16 * j] = p;
       }
       l[i] = l[i] * keep + sum16(sum);
 #pragma unroll
-      for (int c = 0; c < D / 16; ++c) o[i][c] *= keep;
+      for (int c = 0; c < D / 32; ++c) o[i][c] = mul2(o[i][c], f2(keep, keep));
     }
   }
 };
 
+__device__ __forceinline__ float part_of(const uint64_t* x, int e) {  // e: a constant
+  return __uint_as_float(uint32_t(x[e >> 1] >> (e & 1 ? 32 : 0)));
+}
+
 template <typename T>
-__device__ __forceinline__ void store4(T* dst, const float* x, float scale) {
+__device__ __forceinline__ void store4(T* dst, const uint64_t* x, float scale) {
 #pragma unroll
-  for (int e = 0; e < 4; ++e) dst[e] = from_f32<T>(x[e] * scale);
+  for (int e = 0; e < 4; ++e) dst[e] = from_f32<T>(part_of(x, e) * scale);
 }
 
 template <int D>
@@ -211,13 +231,13 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
   load(Vs, v, 0);
   for (int j0 = 0; j0 < seen; j0 += kTile) {
     tile_wait<1>();  // K is there (and the previous P is read)
-    float sc[4][4] = {};
+    float sc[kR][4] = {};
     product_nt<D>(Qs, Ks, ty, tx, sc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const bool sees = j0 + tx + 16 * j <= s.pos0 + i0 + ty + 8 * i;
+        const bool sees = j0 + tx + 16 * j <= s.pos0 + i0 + ty + kTy * i;
         sc[i][j] = sees ? sc[i][j] * sl2 : -INFINITY;
       }
     R.step(sc, Ps, ty, tx);
@@ -229,13 +249,13 @@ dense_fwd_simt_kernel(Dense P, const T* __restrict__ q, const T* __restrict__ k,
     load(Vs, v, j0 + kTile);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty + 8 * i;
+  for (int i = 0; i < kR; ++i) {
+    const int r = ty + kTy * i;
     if (r >= rows) continue;
     const long long at = (long long)(s.q0 + i0 + r) * P.Hq + h;
     const float inv = 1.f / R.l[i];
 #pragma unroll
-    for (int c = 0; c < D / 16; c += 4) store4(out + at * D + tx * 4 + c * 16, &R.o[i][c], inv);
+    for (int c = 0; c < D / 16; c += 4) store4(out + at * D + tx * 4 + c * 16, &R.o[i][c / 2], inv);
     if (lse && tx == 0) lse[at] = (R.m[i] + log2f(R.l[i])) * kLn2;
   }
 }
@@ -297,7 +317,7 @@ dense_dkv_simt_kernel(Dense P, int splits, const T* __restrict__ dout, const T* 
   const long long kat = ((long long)(s.k0 + j0) * P.Hkv + g) * D;
   load_tile<D, kRows>(Ks, k + kat, kst, keys);
   load_tile<D, kRows>(Vs, v + kat, kst, keys);
-  float ak[4][D / 16] = {}, av[4][D / 16] = {};
+  uint64_t ak[kR][D / 32] = {}, av[kR][D / 32] = {};
   // the first query row that sees key j0 sits at position j0
   const int i_first = max(0, j0 - s.pos0) / kTile * kTile;
   const int per = (P.G + splits - 1) / splits;
@@ -333,15 +353,15 @@ dense_dkv_simt_kernel(Dense P, int splits, const T* __restrict__ dout, const T* 
     }
     tile_wait<1>();  // dO is there
     stats(x + 1);
-    float sc[4][4] = {}, dp[4][4] = {};
+    float sc[kR][4] = {}, dp[kR][4] = {};
     product_nt<D>(Vs, Gs, ty, tx, dp);
     tile_wait<0>();  // Q is there
     product_nt<D>(Ks, Qs, ty, tx, sc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int key = ty + 8 * i, c = tx + 16 * j;
+        const int key = ty + kTy * i, c = tx + 16 * j;
         const bool sees = c < rows && j0 + key <= s.pos0 + i0 + c;
         const float p = sees ? exp2f(sc[i][j] * (P.scale * kLog2e) - lse_s[c]) : 0.f;
         Ps[key * Smem<D>::kPPitch + c] = p;
@@ -358,18 +378,18 @@ dense_dkv_simt_kernel(Dense P, int splits, const T* __restrict__ dout, const T* 
   const long long all = P.rows_k * P.Hkv * D;
   float* pv = part + (long long)split * 2 * all;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty + 8 * i;
+  for (int i = 0; i < kR; ++i) {
+    const int r = ty + kTy * i;
     if (r >= keys) continue;
     const long long at = kat + r * kst + tx * 4;
 #pragma unroll
     for (int c = 0; c < D / 16; c += 4) {
       if (splits > 1) {
-        store4(pv + at + c * 16, &av[i][c], 1.f);
-        store4(pv + all + at + c * 16, &ak[i][c], 1.f);
+        store4(pv + at + c * 16, &av[i][c / 2], 1.f);
+        store4(pv + all + at + c * 16, &ak[i][c / 2], 1.f);
       } else {
-        store4(dk + at + c * 16, &ak[i][c], P.scale);
-        store4(dv + at + c * 16, &av[i][c], 1.f);
+        store4(dk + at + c * 16, &ak[i][c / 2], P.scale);
+        store4(dv + at + c * 16, &av[i][c / 2], 1.f);
       }
     }
   }
@@ -412,7 +432,7 @@ dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ 
     lse_s[threadIdx.x] = ok ? lse[at + (long long)threadIdx.x * P.Hq] * kLog2e : 0.f;
     delta_s[threadIdx.x] = ok ? delta[at + (long long)threadIdx.x * P.Hq] : 0.f;
   }
-  float aq[4][D / 16] = {};
+  uint64_t aq[kR][D / 32] = {};
   const int seen = min(s.nk, s.pos0 + i0 + rows);
   // rows behind what is seen are zero: they must not meet a weight of zero as NaN
   auto load = [&](float* dst, const T* src, int j0) {
@@ -425,17 +445,17 @@ dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ 
   load(Vs, v, 0);
   load(Ks, k, 0);
   for (int j0 = 0; j0 < seen; j0 += kTile) {
-    float sc[4][4] = {}, dp[4][4] = {};
+    float sc[kR][4] = {}, dp[kR][4] = {};
     tile_wait<1>();  // V is there
     product_nt<D>(Gs, Vs, ty, tx, dp);
     tile_wait<0>();  // K is there, V read
     load(Vs, v, j0 + kTile);
     product_nt<D>(Qs, Ks, ty, tx, sc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < kR; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int r = ty + 8 * i, c = tx + 16 * j;
+        const int r = ty + kTy * i, c = tx + 16 * j;
         const bool sees = r < rows && j0 + c <= s.pos0 + i0 + r;
         const float p = sees ? exp2f(sc[i][j] * (P.scale * kLog2e) - lse_s[r]) : 0.f;
         Ss[r * Smem<D>::kPPitch + c] = sees ? p * (dp[i][j] - delta_s[r]) : 0.f;
@@ -446,12 +466,12 @@ dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ 
     load(Ks, k, j0 + kTile);
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int r = ty + 8 * i;
+  for (int i = 0; i < kR; ++i) {
+    const int r = ty + kTy * i;
     if (r >= rows) continue;
 #pragma unroll
     for (int c = 0; c < D / 16; c += 4)
-      store4(dq + (at + (long long)r * P.Hq) * D + tx * 4 + c * 16, &aq[i][c], P.scale);
+      store4(dq + (at + (long long)r * P.Hq) * D + tx * 4 + c * 16, &aq[i][c / 2], P.scale);
   }
 }
 
@@ -541,11 +561,11 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
         for (int i = threadIdx.x; i < kTile * D; i += kThreads)
           if (!seen_s[i / D]) Vs[i / D * Smem<D>::kPitch + i % D] = 0.f;
       }
-      float sc[4][4] = {};
+      float sc[kR][4] = {};
       product_nt<D>(Qs, Ks, ty, tx, sc);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int node = min((row0 + ty + 8 * i) / P.G, nodes - 1);
+      for (int i = 0; i < kR; ++i) {
+        const int node = min((row0 + ty + kTy * i) / P.G, nodes - 1);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int draft = j0 + tx + 16 * j - p.len;
@@ -558,14 +578,14 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
       product_nn<D>(Ps, Vs, ty, tx, R.o);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int r = ty + 8 * i;
+    for (int i = 0; i < kR; ++i) {
+      const int r = ty + kTy * i;
       if (r >= rows) continue;
       if (p.slot >= 0) {
         const long long at = (long long)(blockIdx.x * 2 + p.slot) * A.rows;
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
-          A.part_o[at * D + (tx * 4 + (c / 4) * 64 + c % 4) * A.rows + r] = R.o[i][c];
+          A.part_o[at * D + (tx * 4 + (c / 4) * 64 + c % 4) * A.rows + r] = part_of(R.o[i], c);
         if (tx == 0) A.part_ml[at + r] = make_float2(R.m[i], R.l[i]);
         continue;
       }
@@ -573,7 +593,7 @@ tree_simt_kernel(Tree A, const T* __restrict__ q, const T* __restrict__ k,
                            (row0 + r) % P.G;
       const float inv = R.l[i] == 0.f ? 0.f : 1.f / R.l[i];
 #pragma unroll
-      for (int c = 0; c < D / 16; c += 4) store4(out + at * D + tx * 4 + c * 16, &R.o[i][c], inv);
+      for (int c = 0; c < D / 16; c += 4) store4(out + at * D + tx * 4 + c * 16, &R.o[i][c / 2], inv);
       if (lse && tx == 0) lse[at] = R.l[i] == 0.f ? -INFINITY : (R.m[i] + log2f(R.l[i])) * kLn2;
     }
   }
@@ -691,7 +711,7 @@ cudaError_t bwd(const Dense& P, const void* dout, const void* q, const void* k, 
   const T *k_ = static_cast<const T*>(k), *v_ = static_cast<const T*>(v);
   T *dk_ = static_cast<T*>(dk), *dv_ = static_cast<T*>(dv);
   if (n > 0)
-    dense_delta_kernel<T, D><<<unsigned((n + 3) / 4), kThreads, 0, s>>>(
+    dense_delta_kernel<T, D><<<unsigned((n + kThreads / 32 - 1) / (kThreads / 32)), kThreads, 0, s>>>(
         g_, static_cast<const T*>(out), W.dl, n);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int splits = dense_bwd_splits(P);
