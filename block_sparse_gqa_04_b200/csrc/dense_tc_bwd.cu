@@ -994,13 +994,15 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       // of P (dP - delta) is what delta lacks; dk gets the better one.  (Not where P does
       // not sum to 1: lse and out may be those of more keys than this call's.)
       float r = lo_of(rest) + hi_of(rest), sum = lo_of(mass) + hi_of(mass);
+      if (!warp_wait(&bars->acc_full, ii & 1, abort)) { failed = true; break; }
+      tc::tc_fence_after();
+      // Not before acc_full: it takes every warp's last dS of this item, so the previous
+      // item's sums have been read.  (In an item of one key tile nothing else orders them.)
       if (wg >= 2) {
         bars->rest[wg - 2][row] = make_float2(r, sum);
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(&bars->r_full[0]);
       }
-      if (!warp_wait(&bars->acc_full, ii & 1, abort)) { failed = true; break; }
-      tc::tc_fence_after();
       __nv_bfloat16* dst = dq + ((long long)(it.row0 + row) * P.Hq + it.head) * D + wg * (D / 4);
 #pragma unroll 1
       for (int c = 0; c < D / 4; c += 16) {
