@@ -81,26 +81,36 @@ __device__ __forceinline__ float ex2_f32(float x) {
   return y;
 }
 
+// The larger of two values, NaN if either is (fmaxf takes the other).
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+  return y;
+}
+
 // 2^x of two values on the FMA pipe, for part of a tile's exponentials where the exp2
 // unit (16 values per SM and cycle) is what everything waits for.  x = n + f, n the
 // nearest integer, found by adding 1.5 x 2^23; 2^f on [-1/2, 1/2] by a quartic, the minimax
-// fit of the relative error by Remez exchange (3e-6, against 2^-9 of a bf16 rounding); n
-// goes into the exponent by an integer add.  Below 2^-126 the result stays 2^-126.
+// fit of the relative error by Remez exchange (3e-6, against 2^-9 of a bf16 rounding);
+// times 2^n, made of n's bits by an integer add.  (Added to the quartic's exponent instead,
+// n's bits would turn a NaN into a number.)  For x up to 127; below -126 it is taken as
+// -126.
 __device__ __forceinline__ uint64_t exp2_poly(uint64_t x) {
   constexpr float c[5] = {0.9999992847442627f, 0.6931217908859253f, 0.240247443318367f,
                           0.05591785907745361f, 0.009570102207362652f};
   constexpr float kMagic = 12582912.f;
-  x = f2(fmaxf(__uint_as_float(uint32_t(x)), -126.f),
-         fmaxf(__uint_as_float(uint32_t(x >> 32)), -126.f));
+  constexpr uint32_t kOne = 0x3f800000u;  // 1.f
+  x = f2(max_nan(__uint_as_float(uint32_t(x)), -126.f),
+         max_nan(__uint_as_float(uint32_t(x >> 32)), -126.f));
   const uint64_t t = add2(x, f2(kMagic, kMagic));
   const uint64_t n = add2(t, f2(-kMagic, -kMagic));
   const uint64_t f = fma2(n, f2(-1.f, -1.f), x);
   uint64_t p = f2(c[4], c[4]);
 #pragma unroll
   for (int i = 3; i >= 0; --i) p = fma2(p, f, f2(c[i], c[i]));
-  const uint32_t lo = uint32_t(p) + (uint32_t(t) << 23);
-  const uint32_t hi = uint32_t(p >> 32) + (uint32_t(t >> 32) << 23);
-  return (uint64_t(hi) << 32) | lo;
+  const uint32_t lo = (uint32_t(t) << 23) + kOne;
+  const uint32_t hi = (uint32_t(t >> 32) << 23) + kOne;
+  return mul2(p, (uint64_t(hi) << 32) | lo);
 }
 
 inline PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
