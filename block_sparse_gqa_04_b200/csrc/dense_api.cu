@@ -250,6 +250,12 @@ msa_status_t resolve_norm(const msa_norm_rope_t* p, msa::NormRope* P) {
   return MSA_OK;
 }
 
+// An output that starts on the other heads' input or output (it may lie on its own input).
+bool crossed(const msa::NormRope& P, const void* q_in, const void* k_in, const void* q_out,
+             const void* k_out) {
+  return P.hk && (q_out == k_in || k_out == q_in || q_out == k_out);
+}
+
 // A row stride holds the heads and keeps rows on 16-byte boundaries.
 bool stride_ok(const msa::NormRope& P, long long stride, int heads) {
   return stride >= (long long)heads * P.D && stride % (P.f32 ? 4 : 8) == 0 &&
@@ -374,6 +380,7 @@ msa_status_t msa_qk_norm_rope(const msa_norm_rope_t* p, const void* q, const voi
   if (P.rot && (!inv_freq || !positions || (reinterpret_cast<uintptr_t>(inv_freq) & 7u) ||
                 (reinterpret_cast<uintptr_t>(positions) & 7u)))
     return MSA_ERR_INVALID_ARG;
+  if (crossed(P, q, k, q_out, k_out)) return MSA_ERR_INVALID_ARG;
   return msa::status_of(msa::launch_norm_rope(P, q, k, q_weight, k_weight, inv_freq, positions,
                                               q_out, k_out, (cudaStream_t)stream));
 }
@@ -404,6 +411,7 @@ msa_status_t msa_qk_norm_rope_backward(const msa_norm_rope_t* p, const void* dq_
                 (reinterpret_cast<uintptr_t>(positions) & 7u)))
     return MSA_ERR_INVALID_ARG;
   if ((st = check_ws(ws, ws_bytes, msa_norm_rope_workspace_size(p))) != MSA_OK) return st;
+  if (crossed(P, q, k, dq, dk) || crossed(P, dq_out, dk_out, dq, dk)) return MSA_ERR_INVALID_ARG;
   return msa::status_of(msa::launch_norm_rope_backward(
       P, dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, dq, dk, dq_weight,
       dk_weight, static_cast<float*>(ws), s));

@@ -1009,15 +1009,16 @@ def _span(t, stride):
     return t.data_ptr(), t.data_ptr() + n * t.element_size()
 
 
-def _check_overlap(name, dst, stride, *others):
-    """dst may be one of the others (in place) or share no memory with them; rows of
-    one buffer that interleave without touching count as sharing none.  others:
-    (tensor, its row stride)."""
+def _check_overlap(name, dst, stride, own, *others):
+    """dst may be `own`, the input that it is computed from (in place), and shares no memory
+    with the others; rows of one buffer that interleave without touching count as sharing
+    none.  own, others: (tensor, its row stride)."""
     a0, a1 = _span(dst, stride)
     esz = dst.element_size()
-    for o, ostride in others:
+    for i, (o, ostride) in enumerate((own,) + others):
         b0, b1 = _span(o, ostride)
-        if (a0 == b0 and stride == ostride and dst.shape == o.shape) or a1 <= b0 or b1 <= a0:
+        if a1 <= b0 or b1 <= a0 or (i == 0 and a0 == b0 and stride == ostride
+                                    and dst.shape == o.shape):
             continue
         row, off = stride * esz, (b0 - a0) % (stride * esz)
         la, lb = (t.shape[-2] * t.shape[-1] * esz for t in (dst, o))
@@ -1087,7 +1088,8 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps: float = 
     rotary_dim a multiple of 16 up to D, positions int64 [..].  Pair i of a head is
     elements (i, i + rotary_dim/2), or (2i, 2i + 1) if interleaved.  Serves the index
     branch's q_idx and k_idx (as [.., 1, D]) too.  Returns (q_out, k_out), new tensors
-    or out=(q_out, k_out), which may be q and k themselves."""
+    or out=(q_out, k_out); q_out may be q itself and k_out k, and no other memory of the
+    call is shared."""
     p, dev = _norm_rope_problem(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
     if out is None:
         qo = _contiguous_like(q)
@@ -1099,13 +1101,14 @@ def qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, *, eps: float = 
                 k is not None and ko.shape != k.shape):
             raise ValueError("out must be (q_out, k_out) shaped like q and k")
         _one_device(q, qo, ko)
-        lead, ins = q.shape[:-2], [(q, p.q_stride)]
+        lead, qs, ks = q.shape[:-2], (q, p.q_stride), (k, p.k_stride)
         p.q_out_stride = _row_stride("q_out", qo, lead, q.dtype)
-        if k is not None:
-            ins.append((k, p.k_stride))
+        if k is None:
+            _check_overlap("q_out", qo, p.q_out_stride, qs)
+        else:
             p.k_out_stride = _row_stride("k_out", ko, lead, q.dtype)
-            _check_overlap("k_out", ko, p.k_out_stride, (qo, p.q_out_stride), *ins)
-        _check_overlap("q_out", qo, p.q_out_stride, *ins)
+            _check_overlap("q_out", qo, p.q_out_stride, qs, ks)
+            _check_overlap("k_out", ko, p.k_out_stride, ks, qs, (qo, p.q_out_stride))
     _run("msa_qk_norm_rope", dev, load().msa_qk_norm_rope, ctypes.byref(p), q.data_ptr(), _addr(k),
          q_weight.data_ptr(), _addr(k_weight), inv_freq.data_ptr(), positions.data_ptr(),
          qo.data_ptr(), _addr(ko))

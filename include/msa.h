@@ -365,8 +365,9 @@ typedef struct {
 /* q [rows, num_q_heads, head_dim] with q_stride elements from row to row (heads
  * contiguous), k likewise; rows start on 16-byte boundaries.  q_weight, k_weight
  * [head_dim]; inv_freq fp64 [rotary_dim/2]; positions int64 [rows], any values.
- * q_out and k_out may be q and k themselves (same pointer and stride); any other
- * overlap is not allowed. */
+ * q_out may be q itself and k_out k itself (same pointer and stride); any other overlap
+ * is not allowed, and where an output starts on the other heads' input or output the call
+ * is refused. */
 msa_status_t msa_qk_norm_rope(const msa_norm_rope_t* p, const void* q, const void* k,
                               const void* q_weight, const void* k_weight, const double* inv_freq,
                               const int64_t* positions, void* q_out, void* k_out, void* stream);
@@ -374,7 +375,7 @@ msa_status_t msa_qk_norm_rope(const msa_norm_rope_t* p, const void* q, const voi
 /* Gradients of msa_qk_norm_rope from those of its outputs: with g the gradient
  * turned back and r = 1 / sqrt(mean(x^2) + eps),
  *   dw = sum over rows and heads of g r x,   dx = r (w g - r x mean(w g r x)).
- * dq, dk like q, k (each may be dq_out, dk_out themselves); dq_weight, dk_weight fp32
+ * dq, dk like q, k (dq may be dq_out itself and dk dk_out itself); dq_weight, dk_weight fp32
  * [head_dim], summed in a fixed order.  Workspace: msa_norm_rope_workspace_size(p). */
 msa_status_t msa_qk_norm_rope_backward(const msa_norm_rope_t* p, const void* dq_out,
                                        const void* dk_out, const void* q, const void* k,

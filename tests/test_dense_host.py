@@ -247,3 +247,32 @@ def test_overlap_and_stride_checks_of_norm_rope():
         msa._row_stride("q", q.transpose(1, 2), (6,), torch.float32)
     with pytest.raises(ValueError):
         msa._row_stride("q", torch.zeros(4, 6, 8, 128)[:, :3], (4, 3), torch.float32)
+
+
+def test_an_output_of_norm_rope_lies_on_its_own_input_only(monkeypatch):
+    """As many query as key heads: every tensor of the call has the same shape and strides."""
+    calls = []
+    monkeypatch.setattr(msa, "_one_device", lambda *t: 0)                 # CPU tensors here
+    monkeypatch.setattr(msa, "_run", lambda *a: calls.append(a))
+    w, f = torch.ones(128), torch.ones(64, dtype=torch.float64)
+    pos = torch.arange(6)
+    fused = torch.zeros(6, 3, 8, 128)
+    pairs = [[torch.zeros(6, 8, 128) for _ in range(2)], [fused[:, 0], fused[:, 1]]]
+    for q, k in pairs:
+        new = torch.zeros(6, 8, 128)
+        for out in ((k, q), (k, new), (new, q), (new, new), (q, q), (k, k), (k, fused[:, 2])):
+            with pytest.raises(ValueError, match="overlaps"):
+                msa.qk_norm_rope(q, k, w, w, f, pos, out=out)
+        assert not calls
+        for out in ((q, k), (q, new), (new, k), (fused[:, 2], new)):
+            got = msa.qk_norm_rope(q, k, w, w, f, pos, out=out)
+            assert got[0] is out[0] and got[1] is out[1] and calls.pop()
+
+
+def test_norm_rope_refuses_outputs_on_one_another(lib):
+    p = _norm(num_q_heads=8, num_kv_heads=8, k_out_stride=1024, dk_stride=1024)
+    q, k, w, new = FAKE, 2 * FAKE, 3 * FAKE, 4 * FAKE
+    for qo, ko in ((k, new), (new, q), (new, new), (q, q)):
+        assert lib.msa_qk_norm_rope(ctypes.byref(p), q, k, w, w, w, w, qo, ko, None) == INVALID
+        g = (ctypes.byref(p), q, k, 5 * FAKE, 6 * FAKE, w, w, w, w, qo, ko, w, w, FAKE, 1 << 30, None)
+        assert lib.msa_qk_norm_rope_backward(*g) == INVALID
