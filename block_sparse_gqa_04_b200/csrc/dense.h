@@ -72,10 +72,11 @@ cudaError_t launch_dense_fwd_simt(const Dense& P, const void* q, const void* k, 
 cudaError_t launch_dense_fwd_tc(const Dense& P, const void* q, const void* k, const void* v,
                                 void* out, float* lse, int32_t* counter, int32_t* status,
                                 cudaStream_t s);
-// Scratch of the gradients: on the tensor cores -lse log2 e and delta, [Hq, rows_pad] +
-// 128 values each, in fp32 delta [rows_q, Hq]; with several splits their partial sums, [splits][2][rows_k, Hkv, D].
+// Scratch of the gradients: on the tensor cores -lse log2 e, -delta and what the rounding
+// of out can have taken from delta, [Hq, rows_pad] + 128 values each, in fp32 delta
+// [rows_q, Hq]; with several splits their partial sums, [splits][2][rows_k, Hkv, D].
 struct DenseBwdSpace {
-  float *nl, *dl, *part;
+  float *nl, *dl, *room, *part;
 };
 int dense_bwd_splits(const Dense& P);
 // Zeroes the head words itself.
@@ -83,7 +84,7 @@ cudaError_t launch_dense_bwd_tc(const Dense& P, const void* dout, const void* q,
                                 const void* v, const void* out, const float* lse,
                                 const DenseBwdSpace& W, void* dq, void* dk, void* dv,
                                 int32_t* head, cudaStream_t s);
-// fp32 on the CUDA cores (nl unused).
+// fp32 on the CUDA cores (nl and room unused).
 cudaError_t launch_dense_bwd_simt(const Dense& P, const void* dout, const void* q, const void* k,
                                   const void* v, const void* out, const float* lse,
                                   const DenseBwdSpace& W, void* dq, void* dk, void* dv,

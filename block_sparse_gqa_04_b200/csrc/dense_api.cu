@@ -145,7 +145,7 @@ msa_status_t resolve_dense(const msa_problem_t* p, const int32_t* cu_q, const in
 }
 
 struct DenseLayout {
-  size_t status, recs, nl, delta, part, total;
+  size_t status, recs, nl, delta, room, part, total;
 };
 
 DenseLayout dense_layout(const Dense& P, bool packed, bool backward) {
@@ -160,6 +160,7 @@ DenseLayout dense_layout(const Dense& P, bool packed, bool backward) {
     const int splits = msa::dense_bwd_splits(P);
     if (!P.f32) L.nl = take(rows * sizeof(float));
     L.delta = take(rows * sizeof(float));
+    if (!P.f32) L.room = take(rows * sizeof(float));
     if (splits > 1) L.part = take(size_t(splits) * 2 * P.rows_k * P.Hkv * P.D * sizeof(float));
   }
   L.total = off;
@@ -315,7 +316,8 @@ msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlen
   const bool own_begin = !P.f32 && !R.r && P.rows_q > 0;
   if (!own_begin && (st = begin(&P, R, L, ws, s)) != MSA_OK) return st;
   int32_t* head = at<int32_t>(ws, L.status);
-  const msa::DenseBwdSpace W{at<float>(ws, L.nl), at<float>(ws, L.delta), at<float>(ws, L.part)};
+  const msa::DenseBwdSpace W{at<float>(ws, L.nl), at<float>(ws, L.delta), at<float>(ws, L.room),
+                             at<float>(ws, L.part)};
   if (P.f32)
     return msa::status_of(
         msa::launch_dense_bwd_simt(P, dout, q, k, v, out, lse, W, dq, dk, dv, s));

@@ -17,8 +17,12 @@
 // Roundings.  P and dS meet the MMAs as bf16.  For dq, where nothing but dS is rounded
 // before the result, dS is the sum of two bf16 numbers (the fourth product): its error
 // falls from 0.0025 to 0.0019, of which a bf16 result's own rounding is 0.0017.  delta =
-// sum_d dout out is formed from the rounded out; since P sums to 1, the dq pass knows
-// exactly what delta lacks, sum_j P (dP - delta), and leaves delta completed for dk.
+// sum_d dout out is formed from the rounded out; where P sums to 1, the dq pass knows
+// what delta lacks, sum_j P (dP - delta), and leaves delta completed for dk (error of dk
+// 0.0024 instead of 0.02 to 0.06 with values of 100 +- 8).  It does so only where the sum
+// differs from 1 by no more than fp32 leaves of it, and by no more than a rounding can
+// have taken from out: half a step of sum_d |dout out|.  So out and lse may be those of
+// more keys than the call's, whatever weight and values the others have.
 //
 // One thread issues all MMAs in an order that keeps the pipe fed while the sixteen
 // elementwise warps (four warpgroups, a quarter of the columns each) work on the other
@@ -120,14 +124,16 @@ __device__ __forceinline__ void issue_ts(uint32_t d, uint32_t a, uint32_t b, int
 }
 
 // ---------------------------------------------------------------------------
-// -c lse and -delta = -sum_d dout out per (head, row), rows of a sequence padded to
-// groups of 16 (padding: -inf, so that P = 0, and 0): one warp per (16 rows, head).
+// -c lse, -delta = -sum_d dout out and room = 2^-8 sum_d |dout out|, half a step of bf16,
+// per (head, row), rows of a sequence padded to groups of 16 (padding: -inf, so that P = 0,
+// and 0): one warp per (16 rows, head).
 // ---------------------------------------------------------------------------
 template <int D>
 __global__ void __launch_bounds__(256)
 dense_prep_kernel(Dense P, const __nv_bfloat16* __restrict__ dout,
                   const __nv_bfloat16* __restrict__ out, const float* __restrict__ lse,
-                  float* __restrict__ nl, float* __restrict__ dl, int* __restrict__ head) {
+                  float* __restrict__ nl, float* __restrict__ dl, float* __restrict__ room,
+                  int* __restrict__ head) {
   tc::griddep_wait();  // the records are in place
   tc::griddep_launch();
   if (blockIdx.x == 0 && threadIdx.x < kHeadWords) head[threadIdx.x] = 0;
@@ -144,30 +150,42 @@ dense_prep_kernel(Dense P, const __nv_bfloat16* __restrict__ dout,
     s = batch_seq(P, int(x0 / pad16(P.Sq)));
   }
   const int i0 = int(x0) - s.qp0;
-  float mine = 0.f;
+  float mine = 0.f, size = 0.f;
 #pragma unroll
   for (int r0 = 0; r0 < 16; r0 += kRowsAtOnce) {
     const int i = i0 + r0 + lane / kLanes;
-    float sum = 0.f;
+    float sum = 0.f, mag = 0.f;
     if (i < s.nq) {
       const long long at = ((long long)(s.q0 + i) * P.Hq + h) * D + (lane % kLanes) * 8;
       float a[8], b[8];
       load_vec<__nv_bfloat16, 8>(dout + at, a);
       load_vec<__nv_bfloat16, 8>(out + at, b);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) sum += a[e] * b[e];
+      for (int e = 0; e < 8; ++e) {
+        sum += a[e] * b[e];
+        mag += fabsf(a[e] * b[e]);
+      }
     }
 #pragma unroll
-    for (int o = kLanes / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(MSA_FULL_MASK, sum, o);
+    for (int o = kLanes / 2; o > 0; o >>= 1) {
+      sum += __shfl_xor_sync(MSA_FULL_MASK, sum, o);
+      mag += __shfl_xor_sync(MSA_FULL_MASK, mag, o);
+    }
     // lane r of the warp keeps row r
-    const float got = __shfl_sync(MSA_FULL_MASK, sum, (lane % kRowsAtOnce) * kLanes);
-    if (lane / kRowsAtOnce == r0 / kRowsAtOnce) mine = got;
+    const int from = (lane % kRowsAtOnce) * kLanes;
+    const float got = __shfl_sync(MSA_FULL_MASK, sum, from);
+    const float got_mag = __shfl_sync(MSA_FULL_MASK, mag, from);
+    if (lane / kRowsAtOnce == r0 / kRowsAtOnce) {
+      mine = got;
+      size = got_mag;
+    }
   }
   if (lane < 16) {
     const bool there = i0 + lane < s.nq;
     const long long at = (long long)h * P.rows_pad + x0 + lane;
     nl[at] = there ? -kLog2e * lse[(long long)(s.q0 + i0 + lane) * P.Hq + h] : -INFINITY;
     dl[at] = there ? -mine : 0.f;
+    room[at] = there ? 0x1p-8f * size : 0.f;
   }
 }
 
@@ -683,7 +701,7 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                    const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, Dense P, int items,
                    const float* __restrict__ nl, float* __restrict__ dl,
-                   __nv_bfloat16* __restrict__ dq, int* __restrict__ next_item,
+                   const float* room, __nv_bfloat16* __restrict__ dq, int* __restrict__ next_item,
                    int* __restrict__ status) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -971,15 +989,17 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         }
         // dS as the sum of two bf16 numbers, over the scores that made it
         uint32_t hi[16], lo[16];
+        uint64_t here = 0;  // P summed tile by tile: fewer roundings
 #pragma unroll
         for (int x = 0; x < 16; ++x) {
           const uint64_t y = pair_of(&d[2 * x]);
           rest = add2(rest, y);
-          mass = add2(mass, pair_of(&p[2 * x]));
+          here = add2(here, pair_of(&p[2 * x]));
           hi[x] = to_bf16x2(y);
           lo[x] = to_bf16x2(add2(y, f2(-__uint_as_float(hi[x] << 16),
                                        -__uint_as_float(hi[x] & 0xffff0000u))));
         }
+        mass = add2(mass, here);
         tmem_st8(sa, hi);
         tmem_st8(sa + 8, hi + 8);
         tmem_st8(sa + 16, lo);
@@ -991,9 +1011,9 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
       }
       if (failed) break;
       // delta was formed from the rounded out: P sums to 1, so what is left of the sum
-      // of P (dP - delta) is what delta lacks; dk gets the better one.  (Not where P does
-      // not sum to 1: lse and out may be those of more keys than this call's.)
+      // of P (dP - delta) is what delta lacks; dk gets the better one.
       float r = lo_of(rest) + hi_of(rest), sum = lo_of(mass) + hi_of(mass);
+      const float most = wg == 0 && mine ? room[at] : 0.f;  // that rounding out can take
       if (!warp_wait(&bars->acc_full, ii & 1, abort)) { failed = true; break; }
       tc::tc_fence_after();
       // Not before acc_full: it takes every warp's last dS of this item, so the previous
@@ -1035,7 +1055,14 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
         } else {
           if (!warp_wait(&bars->r_full[1], ii & 1, abort)) { failed = true; break; }
           const float2 other = bars->rest[1][row];
-          if (mine && fabsf(sum + other.y - 1.f) < 1e-3f) dl[at] = ndelta - (r + other.x);
+          // Not where more keys than this call's are in lse and out.  Units of 2^-24 that
+          // a whole row's sum may be off by: the exponentials of both passes and log2 l,
+          // 2^-22 each and more for a large l; the sums, 32 and 16 addends a tile and a
+          // tile after another, with signs that mostly cancel; 2.8 |c lse| by the three
+          // roundings between l and c lse.  A whole row that misses it keeps its delta.
+          const float off = 0x1p-24f * (256.f + 4.f * fabsf(nlse));
+          r += other.x;
+          if (mine && fabsf(sum + other.y - 1.f) <= off && fabsf(r) <= most) dl[at] = ndelta - r;
         }
       }
     }
@@ -1079,16 +1106,18 @@ cudaError_t bwd_tc(const Dense& P, const void* dout, const void* q, const void* 
   if (P.seqs) {
     e = launch_after(dense_prep_kernel<D>, unsigned((warps + 7) / 8), 256, 0, s, P,
                      static_cast<const bf16*>(dout), static_cast<const bf16*>(out), lse, W.nl, W.dl,
-                     head);
+                     W.room, head);
   } else {  // nothing of this call ran before: an ordinary launch
     dense_prep_kernel<D><<<unsigned((warps + 7) / 8), 256, 0, s>>>(
-        P, static_cast<const bf16*>(dout), static_cast<const bf16*>(out), lse, W.nl, W.dl, head);
+        P, static_cast<const bf16*>(dout), static_cast<const bf16*>(out), lse, W.nl, W.dl, W.room,
+        head);
     e = cudaGetLastError();
   }
   if (e != cudaSuccess) return e;
   const int qitems = P.qtiles * P.Hq;
   e = launch_after(dense_dq_tc_kernel<D>, std::min(sm_count(), qitems), kThreads, row_smem<D>(), s,
-                   mq, mg, mk, mv, P, qitems, W.nl, W.dl, static_cast<bf16*>(dq), head + 2, head);
+                   mq, mg, mk, mv, P, qitems, W.nl, W.dl, W.room, static_cast<bf16*>(dq), head + 2,
+                   head);
   if (e != cudaSuccess) return e;
   const int kitems = P.ktiles * P.Hkv * splits;
   e = launch_after(dkv, std::min(sm_count(), kitems), kThreads, key_smem<D>(), s, mq, mg, mk, mv, P,

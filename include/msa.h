@@ -297,9 +297,10 @@ msa_status_t msa_dense_attend(const msa_problem_t* p, const int32_t* cu_seqlens_
  * for tokens that no row sees).  dq like q, dk and dv like k, all of the problem's
  * dtype and overwritten; sums in fp32 in a fixed order: the same inputs give the same
  * bits.  bf16 problems round P and dS to bf16 for the products (dS as two bf16 numbers
- * for dq); delta is completed by what the rounding of out took from it (where P sums to
- * 1: out and lse may also be those of more keys than this call's, as where ranks hold a
- * part of the keys each).  Tokens that no row sees may hold anything.
+ * for dq); for dk delta is completed by what the rounding of out took from it, where P sums
+ * to 1 within fp32 and by half a step of bf16 of sum |dout out| at most: out and lse may
+ * also be those of more keys than this call's, as where ranks hold a part of the keys each.
+ * Tokens that no row sees may hold anything.
  * dout, out, dq [.., num_q_heads, head_dim].  num_pages must be 0 (MSA_ERR_UNSUPPORTED).
  * Workspace: msa_dense_workspace_size(.., 1) bytes. */
 msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlens_q_opt,
