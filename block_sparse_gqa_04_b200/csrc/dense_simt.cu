@@ -477,7 +477,7 @@ dense_dq_simt_kernel(Dense P, const T* __restrict__ dout, const T* __restrict__ 
 
 template <typename T>
 __global__ void __launch_bounds__(256)
-dense_dkv_sum_kernel(const float* __restrict__ part, int splits, long long n, float scale,
+dense_dkv_sum_kernel(const float* part, int splits, long long n, float scale,
                      T* __restrict__ dk, T* __restrict__ dv) {
   tc::griddep_wait();
   const long long i = ((long long)blockIdx.x * 256 + threadIdx.x) * 4;

@@ -256,7 +256,7 @@ dense_dkv_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                     const __grid_constant__ CUtensorMap tmap_g,
                     const __grid_constant__ CUtensorMap tmap_k,
                     const __grid_constant__ CUtensorMap tmap_v, Dense P, int splits, int items,
-                    const float* __restrict__ nl, const float* __restrict__ dl,
+                    const float* nl, const float* dl,
                     __nv_bfloat16* __restrict__ dk, __nv_bfloat16* __restrict__ dv,
                     float* __restrict__ part, int* __restrict__ next_item,
                     int* __restrict__ status) {
@@ -700,8 +700,8 @@ dense_dq_tc_kernel(const __grid_constant__ CUtensorMap tmap_q,
                    const __grid_constant__ CUtensorMap tmap_g,
                    const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, Dense P, int items,
-                   const float* __restrict__ nl, float* __restrict__ dl,
-                   const float* room, __nv_bfloat16* __restrict__ dq, int* __restrict__ next_item,
+                   const float* nl, float* dl, const float* room,
+                   __nv_bfloat16* __restrict__ dq, int* __restrict__ next_item,
                    int* __restrict__ status) {
   using C = Cfg<D>;
   extern __shared__ __align__(1024) uint8_t smem[];

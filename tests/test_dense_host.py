@@ -2,6 +2,7 @@
 refusals, all decided before any launch (no GPU needed; the pointers are never read)."""
 import ctypes
 import os
+import re
 import subprocess
 
 import pytest
@@ -276,3 +277,23 @@ def test_norm_rope_refuses_outputs_on_one_another(lib):
         assert lib.msa_qk_norm_rope(ctypes.byref(p), q, k, w, w, w, w, qo, ko, None) == INVALID
         g = (ctypes.byref(p), q, k, 5 * FAKE, 6 * FAKE, w, w, w, w, qo, ko, w, w, FAKE, 1 << 30, None)
         assert lib.msa_qk_norm_rope_backward(*g) == INVALID
+
+
+def test_kernels_that_start_early_promise_nothing_about_scratch():
+    """A kernel that waits for its predecessor inside itself must not declare what that one
+    writes as read-only for its whole life (const and __restrict__): loads of it could move in
+    front of the wait.  The caller's tensors are older than the call."""
+    tensors = {"q", "k", "v", "out", "dout", "lse", "mask"}
+    src = os.path.join(ROOT, "block_sparse_gqa_04_b200", "csrc")
+    found = 0
+    kernels = re.compile(r"__global__ void(?: __launch_bounds__\([^)]*\))?\s+(\w+)\((.*?)\) \{\n"
+                         r"(.*?)\n\}\n", re.S)
+    for name in sorted(os.listdir(src)):
+        for kernel, parameters, body in kernels.findall(open(os.path.join(src, name)).read()):
+            if "griddep_wait()" not in body:
+                continue
+            found += 1
+            for par in parameters.split(","):
+                if "const" in par.split() and "__restrict__" in par:
+                    assert par.split()[-1] in tensors, (kernel, par.strip())
+    assert found == 7
