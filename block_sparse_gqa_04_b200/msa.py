@@ -759,11 +759,23 @@ def _raise_device_status(wp, dev, where):
     _run(f"{where} (device status)", dev, load().msa_device_status, wp, ctypes.byref(code))
 
 
+def _fits(p, scale, **fields):
+    """The Problem's fields hold these numbers: ctypes cuts what is too wide for them, and a
+    scale too small for fp32 would turn into 0, the default."""
+    for name, x in fields.items():
+        if getattr(p, name) != x:
+            raise ValueError(f"{name} = {x} is out of range")
+    if scale != 0.0 and p.softmax_scale == 0.0:
+        raise ValueError(f"softmax_scale = {scale} is below the range of fp32")
+
+
 @functools.lru_cache(maxsize=512)
 def _plan(op, B, Sq, Skv, Hq, Hkv, D, dtype, q_pos0, scale, pages):
     """(Problem, workspace bytes) of a call on these sizes; a paged call fills its block
     table into a copy."""
     p = make_problem(B, Sq, Skv, Hq, Hkv, D, 32, dtype=dtype, q_pos0=q_pos0, softmax_scale=scale)
+    _fits(p, scale, batch=B, q_len=Sq, kv_len=Skv, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D,
+          q_pos0=q_pos0)
     if pages:
         p.num_pages, p.block_table = pages, 256  # any address: only sizes are looked at here
     lib = load()
@@ -778,6 +790,9 @@ def _packed_plan(op, cu_q, cu_k, Hq, Hkv, D, dtype, scale):
     packed call; cu_q and cu_k are tuples."""
     p, cq, ck = varlen_problem(list(cu_q), list(cu_k), Hq, Hkv, D, 32, dtype=dtype,
                                softmax_scale=scale)
+    _fits(p, scale, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D)
+    if tuple(cq) != cu_q or tuple(ck) != cu_k:
+        raise ValueError("prefix sums must be 32-bit integers")
     n = load().msa_dense_workspace_size(ctypes.byref(p), cq, ck, int(op == "backward"))
     return p, cq, ck, n, cq[len(cq) - 1], ck[len(ck) - 1]
 
@@ -829,7 +844,10 @@ def _dense_setup(op, q, k, v, cu_q, cu_k, q_pos0, softmax_scale, block_table=Non
                              f"{qs[0]} / {ks[0]} rows")
         return p, cq, ck, n, dev
     pages = _paged(block_table, kv_len, qs[0], ks[0], 128).get("num_pages", 0)
-    p, n = _plan(op, qs[0], qs[1], int(kv_len) if pages else ks[1], Hq, Hkv, D, dt, int(q_pos0),
+    pos0 = int(q_pos0)
+    if pos0 != q_pos0:
+        raise ValueError(f"q_pos0 = {q_pos0} is not an integer")
+    p, n = _plan(op, qs[0], qs[1], int(kv_len) if pages else ks[1], Hq, Hkv, D, dt, pos0,
                  float(softmax_scale), pages)
     return _with_table(p, block_table), None, None, n, dev
 

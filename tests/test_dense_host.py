@@ -297,3 +297,48 @@ def test_kernels_that_start_early_promise_nothing_about_scratch():
                 if "const" in par.split() and "__restrict__" in par:
                     assert par.split()[-1] in tensors, (kernel, par.strip())
     assert found == 7
+
+
+@pytest.mark.parametrize("kw", [dict(q_pos0=2**64), dict(q_pos0=2**63), dict(q_pos0=-2**64),
+                                dict(q_pos0=1.5), dict(softmax_scale=1e-60),
+                                dict(softmax_scale=-1e-60)])
+def test_numbers_that_do_not_fit_the_call_are_refused(lib, monkeypatch, kw):
+    """The C structure would hold another number: 2^64 as 0, a tiny scale as the default."""
+    calls = []
+    monkeypatch.setattr(msa, "_one_device", lambda *t: 0)                 # CPU tensors here
+    monkeypatch.setattr(msa, "_run", lambda *a: calls.append(a))
+    q, k = torch.zeros(1, 4, 8, 64), torch.zeros(1, 8, 2, 64)
+    lse = torch.zeros(1, 4, 8)
+    for call in (lambda: msa.dense_attend(q, k, k, **kw),
+                 lambda: msa.dense_backward(q, q, k, k, q, lse, **kw)):
+        with pytest.raises((ValueError, TypeError)):
+            call()
+    if "softmax_scale" in kw:
+        with pytest.raises(ValueError):
+            msa.dense_attend_varlen(q[0], k[0], k[0], [0, 4], [0, 8], **kw)
+        with pytest.raises(ValueError):
+            msa.tree_attend(q, k, k, torch.ones(4, 4, dtype=torch.bool),
+                            torch.zeros(1, dtype=torch.int32), **kw)
+    assert not calls
+
+
+@pytest.mark.parametrize("cq,ck", [([0, 2**32 + 2, 4], [0, 4, 8]), ([0, 2, 4], [0, 2**32 + 4, 8]),
+                                   ([-2**32, 2, 4], [0, 4, 8]), ([0, 2.5, 4], [0, 4, 8])])
+def test_prefix_sums_that_do_not_fit_are_refused(lib, monkeypatch, cq, ck):
+    calls = []
+    monkeypatch.setattr(msa, "_one_device", lambda *t: 0)
+    monkeypatch.setattr(msa, "_run", lambda *a: calls.append(a))
+    q, k = torch.zeros(4, 8, 64), torch.zeros(8, 2, 64)
+    with pytest.raises((ValueError, TypeError)):
+        msa.dense_attend_varlen(q, k, k, cq, ck)
+    with pytest.raises((ValueError, TypeError)):
+        msa.dense_backward_varlen(q, q, k, k, q, torch.zeros(4, 8), cq, ck)
+    assert not calls
+
+
+def test_a_cache_longer_than_32_bits_is_refused():
+    """kv_len as the structure would hold it, 100."""
+    with pytest.raises(ValueError):
+        msa._plan("tree", 1, 4, 2**32 + 100, 8, 2, 64, torch.bfloat16, 0, 0.0, 9)
+    with pytest.raises(ValueError):
+        msa._plan("forward", 1, 4, 2**32 + 100, 8, 2, 64, torch.bfloat16, 0, 0.0, 9)
