@@ -932,7 +932,7 @@ def tree_attend(q, k, v, tree_mask, kv_lens, *, softmax_scale: float = 0.0,
                 block_table=None, kv_len=None):
     """Dense attention of a tree of drafted tokens over a KV cache (msa_tree_attend).
 
-    q [B, n, Hq, D]: n drafted tokens (1..128) of each sequence; k, v: the cache [B,
+    q [B, n, Hq, D]: n drafted tokens (0..128) of each sequence; k, v: the cache [B,
     capacity, Hkv, D], or pages [pages, 128, Hkv, D] with block_table [B, ceil(kv_len /
     128)] and kv_len, the tokens per sequence that it covers.  kv_lens (CUDA int32 [B])
     counts the cached tokens of each sequence; its drafted tokens' keys and values are

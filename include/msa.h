@@ -46,7 +46,10 @@
  *    in the workspace status word, read with msa_device_status(); such entries
  *    are skipped, such pages read as page 0, such lengths clamped.
  *  - q_len == 0 is a valid empty problem: the call returns MSA_OK without
- *    looking at the pointers or launching anything.
+ *    looking at the tensors' pointers or launching a kernel.  msa_dense_attend and
+ *    msa_tree_attend clear the status word then if ws is aligned and ws_bytes is
+ *    4 at least; msa_dense_backward needs k, v, dk, dv and its workspace where
+ *    there are keys, whose gradients it sets to zero.
  */
 #ifndef MSA_H
 #define MSA_H
@@ -300,7 +303,10 @@ msa_status_t msa_dense_attend(const msa_problem_t* p, const int32_t* cu_seqlens_
  * for dq); for dk delta is completed by what the rounding of out took from it, where P sums
  * to 1 within fp32 and by half a step of bf16 of sum |dout out| at most: out and lse may
  * also be those of more keys than this call's, as where ranks hold a part of the keys each.
- * Tokens that no row sees may hold anything.
+ * Tokens that no row sees may hold anything.  A number that is not finite in a row of q or
+ * dout, or in the k of a token that some rows see, may also reach the gradients of tokens
+ * (in dq: of rows) up to 127 places away, where its weight is zero.  No rows at all: dk and
+ * dv are zeros, and dout, q, out, lse and dq are not looked at.
  * dout, out, dq [.., num_q_heads, head_dim].  num_pages must be 0 (MSA_ERR_UNSUPPORTED).
  * Workspace: msa_dense_workspace_size(.., 1) bytes. */
 msa_status_t msa_dense_backward(const msa_problem_t* p, const int32_t* cu_seqlens_q_opt,
@@ -316,7 +322,7 @@ size_t msa_dense_workspace_size(const msa_problem_t* p, const int32_t* cu_seqlen
 
 /* Dense attention of a tree of drafted tokens over a KV cache; with q_len 1, the
  * decoding step of a layer whose attention is dense.  p: batch sequences, q_len
- * drafted tokens (nodes, 1..128) per sequence, kv_len the rows of k and v per
+ * drafted tokens (nodes, 0..128) per sequence, kv_len the rows of k and v per
  * sequence (the cache's capacity; with pages the tokens that block_table's
  * ceil(kv_len/128) pages cover); other fields as in msa_dense_attend, q_pos0 ignored.
  * Sequence b holds kv_lens[b] cached tokens (device int32 [batch], read when the

@@ -342,3 +342,19 @@ def test_a_cache_longer_than_32_bits_is_refused():
         msa._plan("tree", 1, 4, 2**32 + 100, 8, 2, 64, torch.bfloat16, 0, 0.0, 9)
     with pytest.raises(ValueError):
         msa._plan("forward", 1, 4, 2**32 + 100, 8, 2, 64, torch.bfloat16, 0, 0.0, 9)
+
+
+def test_a_backward_call_without_rows_needs_the_keys_alone(lib):
+    """It sets dk and dv to zero: with no rows the other tensors are not looked at."""
+    p = _problem(q_len=0)
+    n = lib.msa_dense_workspace_size(ctypes.byref(p), None, None, 1)
+    assert n > 0
+
+    def call(k=FAKE, v=FAKE, dk=FAKE, dv=FAKE, ws=FAKE, ws_bytes=0):
+        return lib.msa_dense_backward(ctypes.byref(p), None, None, None, None, k, v, None, None,
+                                      None, dk, dv, ws, ws_bytes, None)
+
+    assert call() == WORKSPACE and call(ws_bytes=n - 1) == WORKSPACE
+    for kw in (dict(k=None), dict(v=None), dict(dk=None), dict(dv=None), dict(ws=None)):
+        assert call(ws_bytes=n, **kw) == INVALID
+    assert _tree(lib, p, mask=None, lens=None, ws=None) == OK
