@@ -104,11 +104,14 @@ __device__ __forceinline__ void rotate(float (&y)[16], const float2 (&cs)[8], fl
   }
 }
 
-__device__ __forceinline__ void fill_angles(float2 (*cs)[kMaxHalf], long long t0, int nt, int half,
-                                            const double* inv_freq, const int64_t* pos) {
-  for (int i = threadIdx.x; i < nt * half; i += kThreads) {
+// Angles of a block's tokens, of which nt are there.  The others get no turn: what the
+// memory held may be NaN, which times their rows of zeros would reach the weights' gradients.
+__device__ __forceinline__ void fill_angles(float2 (*cs)[kMaxHalf], long long t0, int nt,
+                                            int tokens, int half, const double* inv_freq,
+                                            const int64_t* pos) {
+  for (int i = threadIdx.x; i < tokens * half; i += kThreads) {
     const int t = i / half, f = i % half;
-    cs[t][f] = cos_sin(pos[t0 + t], inv_freq[f]);
+    cs[t][f] = t < nt ? cos_sin(pos[t0 + t], inv_freq[f]) : make_float2(1.f, 0.f);
   }
 }
 
@@ -162,7 +165,7 @@ norm_rope_kernel(NormRope P, Cut cq, Cut ck, const T* q, const T* k, const T* qw
     fetch(h0, cur);  // the angles are formed under the first loads
     if (!first) __syncthreads();
     first = false;
-    fill_angles(cs, t0, nt, P.rot >> 1, inv_freq, pos);
+    fill_angles(cs, t0, nt, c.tokens, P.rot >> 1, inv_freq, pos);
     __syncthreads();
     float2 ang[8];
     my_angles(ang, cs, tok, lane, at.turned);
@@ -231,7 +234,7 @@ norm_rope_backward_kernel(NormRope P, Cut cq, Cut ck, const T* gq, const T* gk, 
     Raw<T> cx, cg, nx, ng;
     fetch(h0, cx, cg);
     __syncthreads();  // the previous tokens' angles are read
-    fill_angles(cs, t0, nt, P.rot >> 1, inv_freq, pos);
+    fill_angles(cs, t0, nt, c.tokens, P.rot >> 1, inv_freq, pos);
     __syncthreads();
     float2 ang[8];
     my_angles(ang, cs, tok, lane, at.turned);

@@ -215,3 +215,23 @@ def test_refusals():
     for call in bad:
         with pytest.raises((ValueError, msa.MsaError)):
             call()
+
+
+@pytest.mark.parametrize("rows", [1185, 1215, 5003])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_weight_gradients_do_not_depend_on_what_shared_memory_held(rows, interleaved):
+    """A block's tokens behind the last row add nothing.  The call before, attention over NaN,
+    leaves NaN in the shared memory of every SM."""
+    hq, hkv, d = 32, 2, 128
+    q, k = randn((rows, hq, d), BF16, 50), randn((rows, hkv, d), BF16, 51)
+    gq, gk = randn((rows, hq, d), BF16, 52), randn((rows, hkv, d), BF16, 53)
+    w, f = torch.ones(d, dtype=BF16, device="cuda"), _freqs(d)
+    pos = torch.arange(rows, device="cuda")
+    args = (gq, gk, q, k, w, w, f, pos)
+    want = msa.qk_norm_rope_backward(*args, interleaved=interleaved)
+    nan = torch.full((8, 1024, 8, 128), float("nan"), device="cuda")
+    for _ in range(5):
+        msa.dense_attend(nan, nan, nan)
+        got = msa.qk_norm_rope_backward(*args, interleaved=interleaved)
+        assert all(torch.equal(a, b) for a, b in zip(want, got))
+        assert all(x.isfinite().all() for x in got)
