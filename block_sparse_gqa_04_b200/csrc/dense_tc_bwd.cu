@@ -31,8 +31,8 @@
 // second warp gathers every other condition of the products into the barrier that the
 // elementwise warps complete, so that the issuing thread waits for one thing at a time.
 //
-// What bounds them (2 x 4096 rows x 64 heads x 128: dk, dv 0.87 ms, dq 0.86 ms; the tensor
-// pipe 69 and 67 % busy): a dk, dv step has 2048 cycles of MMA and takes ~2870, the chain
+// What bounds them (2 x 4096 rows x 64 heads x 128: dk, dv 0.87 ms, dq 0.85 ms; the tensor
+// pipe 66 % busy in both): a dk, dv step has 2048 cycles of MMA and takes ~2900, the chain
 // dV, S, P (its exponentials) and the barriers between them; a dq step has 2048 and takes
 // ~2900, of which the elementwise warps are busy 2500.
 //
@@ -68,10 +68,10 @@ __device__ __forceinline__ float lo_of(uint64_t x) { return __uint_as_float(uint
 __device__ __forceinline__ float hi_of(uint64_t x) { return __uint_as_float(uint32_t(x >> 32)); }
 
 // P of the pair of columns `pair`, POLY of every 8 pairs on the FMA pipe.  The dk, dv pass
-// waits for P on the exp2 unit's 1024 cycles a step: 3 of 8 take it from 0.88 to 0.83 ms
-// (2 x 4096 rows; 1 of 8 0.85, 4 of 8 0.84).  The dq pass does not gain (0.83 with none,
-// 0.84 with 3 of 8; before it summed P), nor does the forward pass (0.93 ms for 8192 rows with none, 0.95
-// with 1 of 8): there a warp alone on its scheduler pays for every instruction.
+// waits for P on the exp2 unit's 1024 cycles a step: 3 of 8 take it from 0.886 to 0.865 ms
+// (2 x 4096 rows; 1 of 8 0.878, 2 0.866, 4 0.909).  The dq pass does not gain (0.847 with
+// none, 0.871 with 3 of 8), nor does the forward pass (0.885 ms for 8192 rows with none,
+// 0.954 with 1 of 8): there a warp alone on its scheduler pays for every instruction.
 template <int POLY>
 __device__ __forceinline__ void exp2_pair(uint32_t* p, uint64_t z, int pair) {
   if ((pair * POLY) % 8 < POLY) {

@@ -9,15 +9,16 @@
 // launch to join.
 //
 // Inside a CTA the even and the odd key tiles of a piece are two independent chains,
-// each with its own softmax warpgroup, running maximum and sum, and accumulator O, so that one chain's MMAs and copies run under the other's softmax;
-// the epilogue joins the two.  Scores, probabilities and the moving maximum are as in
-// the forward pass over whole prompts.  K and V tiles come through a ring of TMA
-// stages (160 KB); Q comes a piece ahead.
+// each with its own softmax warpgroup, running maximum and sum, and accumulator O, so that
+// one chain's MMAs and copies run under the other's softmax; the epilogue joins the two.
+// Scores, probabilities (bf16 for P V: out is 0.0023 of its 2-norm from 64 bits, 0.0017 by
+// its own rounding) and the moving maximum are as in the forward pass over whole prompts.
+// K and V tiles come through a ring of TMA stages (160 KB); Q comes a piece ahead.
 //
-// 8 drafted tokens each over four contexts of 128K (1.07 GB): 174 us, 6.1 TB/s, the rate of
-// a copy; 32 sequences of 2000 to 6000 tokens, one token each: 59 us, 4.4 TB/s (the first
-// tiles' latency and the border pieces weigh more).  The order of use in the ring took the
-// former from 222 us: with K and V of a tile requested together the V tiles held three
+// 8 drafted tokens each over four contexts of 128K (1.07 GB): 178 us, 6.0 TB/s, nearly the
+// rate of a copy; 32 sequences of 2000 to 6000 tokens, one token each: 56 us, 4.7 TB/s (the
+// first tiles' latency and the border pieces weigh more).  The order of use in the ring took
+// the former from 222 us: with K and V of a tile requested together the V tiles held three
 // of the five stages through the softmax.
 //
 // Which drafted tokens a node sees comes as one bit mask per node, and which are seen
